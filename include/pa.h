@@ -494,6 +494,157 @@ pa_status pa_step_prepare(int32_t* block_tables, int32_t num_seqs, int32_t max_b
                           int32_t* slot_mapping, pa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Block-sparse decode step.  The pages stop at attention over a sequence's
+ * whole context; these four calls are this library's additions for long
+ * ones: append the step's rotated keys, keep a per-channel range of every
+ * full block's keys, let each query choose the blocks whose ranges allow the
+ * largest logits, and attend to those.  None needs a workspace.  In stream
+ * order:
+ *     pa_rope_and_cache -> pa_summarize_blocks -> pa_select_blocks
+ *                                              -> pa_decode_selected
+ * Each is useful alone: the append in front of any attention call, a
+ * selection for several layers, a list made by other means.
+ * ---------------------------------------------------------------------- */
+
+/* Rotary embedding.  Pair i < rot_dim / 2 of a head is channels
+ * (i, i + rot_dim / 2), or (2 i, 2 i + 1) with adjacent_pairs; channels from
+ * rot_dim on are left as they are.  With several position axes (time, height
+ * and width of an image patch, say) each pair is turned by one of them:
+ * sections[a] pairs by axis a, in a row, or with sections_in_turn pair i by
+ * axis i % num_axes while that axis has pairs left, else by axis 0.
+ * Supported: rot_dim a multiple of 16 up to head_dim, num_axes 1 to 4,
+ * sections >= 0 with sum rot_dim / 2 (ignored for one axis), and in turn
+ * each axis a > 0 must find its pairs: a + num_axes * (sections[a] - 1) <
+ * rot_dim / 2. */
+typedef struct {
+  int32_t rot_dim;
+  int32_t max_position; /* rows of cos_sin */
+  int32_t num_axes;
+  int32_t sections[4];
+  int32_t sections_in_turn; /* 0 or 1 */
+  int32_t adjacent_pairs;   /* 0 or 1 */
+} pa_rope_desc;
+
+/* ------------------------------------------------------------------------
+ * pa_rope_and_cache -- pa_reshape_and_cache with the position rotation
+ * applied on the way: for a pair (x, y) with cosine c and sine s of its
+ * token's position, (x c - y s, y c + x s) in fp32, rounded once (queries to
+ * bf16; keys to the cache's type, e4m3 from the fp32 quotient by k_scale).
+ *
+ *  q_out         device, [num_tokens, num_heads, head_dim] bf16, written.
+ *                May be `query` itself if q_stride is num_heads * head_dim;
+ *                must not overlap it otherwise.
+ *  query, key, value  device bf16; token t's [heads, head_dim] row starts
+ *                q_stride / k_stride / v_stride elements after token t - 1's
+ *                (multiples of 8, at least heads * head_dim; slices of one
+ *                projection's output qualify).  16-byte aligned.
+ *  num_heads     query heads; any number from 0 (then q_out, query: NULL).
+ *  slot_mapping  device, [num_tokens] int32; a negative or out-of-range slot
+ *                skips the cache write (padding), q_out is still written.
+ *                No slot may appear twice.
+ *  positions     device, [num_axes, num_tokens] int32.  A token with a
+ *                position outside [0, max_position) is skipped: neither its
+ *                q_out row nor its cache rows are written.
+ *  cos_sin       device, [max_position, rot_dim] fp32: row p holds the
+ *                rot_dim / 2 cosines, then the sines, of position p's angles
+ *                (any base, scaling or attention factor is in the table).
+ *                4-byte aligned.
+ *  Other arguments as pa_reshape_and_cache.
+ * ---------------------------------------------------------------------- */
+pa_status pa_rope_and_cache(void* q_out, const void* query, int64_t q_stride, int32_t num_heads,
+                            const void* key, int64_t k_stride, const void* value,
+                            int64_t v_stride, void* k_cache, void* v_cache, pa_cache_desc cache,
+                            const int32_t* slot_mapping, const int32_t* positions,
+                            const float* cos_sin, pa_rope_desc rope, int32_t num_tokens,
+                            const float* k_scale, const float* v_scale, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_summarize_blocks -- the keys' range of each block that the step filled:
+ * a block whose last slot (block * block_size + block_size - 1) is in
+ * slot_mapping is full, and per KV head and channel the largest and smallest
+ * of its block_size keys are kept in 8 bits under one power of two u:
+ *     u = the smallest 2^e >= 2^-50 with max |k| / u <= 127
+ *     codes[block][head][0][d] = ceil (max_t k[t][d] / u)
+ *     codes[block][head][1][d] = floor(min_t k[t][d] / u)
+ *     scales[block][head]      = u
+ * so the codes bound the keys.  Of an e4m3 cache the keys are the codes'
+ * values, without k_scale.  Keys beyond +-2^50 count as that, a NaN is
+ * passed over, a channel of NaNs alone counts as 0.
+ * Other slots, negative ones among them, leave everything as it was.  Call
+ * it after the write, on the same stream, with the write's slot_mapping; to
+ * summarise given blocks (swapped in, say), pass their last slots.
+ *
+ *  codes         device, [num_blocks, num_kv_heads, 2, head_dim] int8,
+ *                16-byte aligned.
+ *  scales        device, [num_blocks, num_kv_heads] fp32.
+ *  num_tokens == 0 is valid and launches nothing.
+ * ---------------------------------------------------------------------- */
+pa_status pa_summarize_blocks(const void* k_cache, pa_cache_desc cache,
+                              const int32_t* slot_mapping, int32_t num_tokens, int8_t* codes,
+                              float* scales, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_select_blocks -- the blocks each query attends to, per KV head.
+ * A block's score is the largest, over the KV head's query heads, of
+ *     sum_d max(c_d codes[0][d], c_d codes[1][d]) * u_q * scales,
+ * c the query rounded to 8 bits: c_d = round-half-even(q_d / u_q) under the
+ * query's own power of two u_q (as u above): a bound on the block's logits,
+ * up to the query's rounding and positive factors common to all blocks.
+ * Scores are exact in fp32, so the result does not depend on the order of
+ * sums.
+ * Row r has nb = ceil(context_lens[r] / block_size) blocks.  If nb <= top,
+ * all are selected.  Otherwise the first `sink` and the last `recent`, and
+ * of the others the top - sink - recent with the largest scores, equal
+ * scores in rising order of index.
+ *
+ *  selected      device, [num_rows, num_kv_heads, top] int32, written:
+ *                logical block indices in rising order, then -1.
+ *  q             device, [num_rows, num_heads, head_dim] bf16, 16-byte
+ *                aligned.  NaN counts as 0, values beyond +-2^50 as that.
+ *  codes, scales as pa_summarize_blocks wrote them for every block but a
+ *                row's last `recent` (codes in [-127, 127]; scales powers of
+ *                two from 2^-50 to 2^44).  16- and 4-byte aligned.
+ *  cache         the cache's shape (its dtype is not used).
+ *  block_tables  device, [num_seqs, max_blocks_per_seq] int32.  A block
+ *                outside the pool has the lowest score.
+ *  context_lens  device, [num_rows] int32: tokens each row may see; what is
+ *                over max_blocks_per_seq * block_size is cut.
+ *  row_seqs      device, [num_rows] int32: the sequence (block table row) of
+ *                each query row, for several queries of one sequence; NULL:
+ *                row r is sequence r (num_rows == num_seqs).  A row naming
+ *                no sequence selects nothing.
+ *  sink, recent  sink >= 0, recent >= 1, sink + recent <= top.  With recent
+ *                >= 1 a block that is not full yet is never scored.
+ *  Limits: num_heads / num_kv_heads in {1, 2, 4, 8}; max_blocks_per_seq up
+ *  to 262144; num_rows * num_kv_heads up to 2^27; else PA_ERR_UNSUPPORTED.
+ *  num_rows == 0 is valid and launches nothing.
+ * ---------------------------------------------------------------------- */
+pa_status pa_select_blocks(int32_t* selected, const void* q, const int8_t* codes,
+                           const float* scales, pa_cache_desc cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens,
+                           const int32_t* row_seqs, int32_t num_rows, int32_t num_seqs,
+                           int32_t num_heads, int32_t top, int32_t sink, int32_t recent,
+                           pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_decode_selected -- pa_decode over listed blocks: out[r, h] attends to
+ * the tokens below context_lens[r] of the logical blocks listed in
+ * selected[r, h / G].  Entries may be in any order; one that is negative, at
+ * or past the context's end or outside the pool is passed over; one listed
+ * twice counts twice.  A row and head without a token gives zeros.
+ *
+ *  selected      device, [num_rows, num_kv_heads, top] int32, top <= 4096.
+ *  Rows, row_seqs, limits and alignment as pa_select_blocks; out, q and the
+ *  other arguments as pa_decode.
+ * ---------------------------------------------------------------------- */
+pa_status pa_decode_selected(void* out, const void* q, const void* k_cache, const void* v_cache,
+                             pa_cache_desc cache, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             const int32_t* row_seqs, const int32_t* selected, int32_t num_rows,
+                             int32_t num_seqs, int32_t num_heads, int32_t top, float scale,
+                             const float* k_scale, const float* v_scale, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Host-side block pool (off the hot path; not thread-safe: one owner).
  * Free queue is FIFO: allocation takes from the head, blocks whose ref count
  * drops to 0 join the tail.  [PKV] "Implementation" (BlockPool: deque free

@@ -28,6 +28,12 @@ class DecodeOpts(ctypes.Structure):
     _fields_ = [("partition_tokens", ctypes.c_int32), ("kernel", ctypes.c_int32)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("max_position", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("sections_in_turn", ctypes.c_int32), ("adjacent_pairs", ctypes.c_int32)]
+
+
 class PaError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {msg}")
@@ -46,6 +52,7 @@ _lib = None
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
+I64 = ctypes.c_int64
 PI32 = ctypes.POINTER(ctypes.c_int32)
 SIZE = ctypes.c_size_t
 
@@ -76,6 +83,13 @@ SIGNATURES = {
                                   P, ctypes.c_size_t, P]),
     "pa_varlen_attention_ex": (I32, [P, P, P, P, CacheDesc, P, I32, P, P, I32, I32, I32,
                                      ctypes.c_float, P, P, I32, P, ctypes.c_size_t, P]),
+    "pa_rope_and_cache": (I32, [P, P, I64, I32, P, I64, P, I64, P, P, CacheDesc, P, P, P, RopeDesc,
+                                I32, P, P, P]),
+    "pa_summarize_blocks": (I32, [P, CacheDesc, P, I32, P, P, P]),
+    "pa_select_blocks": (I32, [P, P, P, P, CacheDesc, P, I32, P, P, I32, I32, I32, I32, I32, I32,
+                               P]),
+    "pa_decode_selected": (I32, [P, P, P, P, CacheDesc, P, I32, P, P, P, I32, I32, I32, I32,
+                                 ctypes.c_float, P, P, P]),
     "pa_slot_mapping": (I32, [PI32, I32, I32, I32, PI32, PI32, I32, PI32]),
     "pa_pool_create": (P, [I32]),
     "pa_pool_create_ordered": (P, [I32, PI32]),

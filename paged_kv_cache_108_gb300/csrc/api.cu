@@ -117,6 +117,32 @@ pa_status check_scales(const pa_cache_desc& c, const float* ks, const float* vs,
   return PA_OK;
 }
 
+// What the calls over query rows share: row r belongs to sequence
+// row_seqs[r], or r.
+pa_status check_rows(const pa_cache_desc& c, int32_t max_blocks, const int32_t* row_seqs,
+                     int32_t num_rows, int32_t num_seqs, int32_t num_heads, const char* fn) {
+  char buf[192];
+  if (num_rows < 0 || num_seqs < 0 || num_heads <= 0 || max_blocks <= 0 ||
+      num_heads % c.num_kv_heads) {
+    snprintf(buf, sizeof buf, "%s: bad sizes (num_heads must be a multiple of num_kv_heads)", fn);
+    return pa_fail(PA_ERR_INVALID, buf);
+  }
+  if (!row_seqs && num_rows != num_seqs) {
+    snprintf(buf, sizeof buf, "%s: without row_seqs num_rows must be num_seqs", fn);
+    return pa_fail(PA_ERR_INVALID, buf);
+  }
+  const int32_t g = num_heads / c.num_kv_heads;
+  if (g != 1 && g != 2 && g != 4 && g != 8) {
+    snprintf(buf, sizeof buf, "%s: GQA group %d unsupported (1, 2, 4, 8)", fn, g);
+    return pa_fail(PA_ERR_UNSUPPORTED, buf);
+  }
+  if ((int64_t)num_rows * c.num_kv_heads > (1 << 27)) {
+    snprintf(buf, sizeof buf, "%s: num_rows * num_kv_heads above 2^27", fn);
+    return pa_fail(PA_ERR_UNSUPPORTED, buf);
+  }
+  return PA_OK;
+}
+
 pa_status cuda_status(cudaError_t e, const char* fn) {
   if (e == cudaSuccess) return PA_OK;
   char buf[256];
@@ -834,6 +860,215 @@ pa_status pa_step_prepare(int32_t* block_tables, int32_t num_seqs, int32_t max_b
                                              context_lens, num_seqs, table_updates, num_updates,
                                              advance, slot_mapping,
                                              reinterpret_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+pa_status pa_rope_and_cache(void* q_out, const void* query, int64_t q_stride, int32_t num_heads,
+                            const void* key, int64_t k_stride, const void* value,
+                            int64_t v_stride, void* k_cache, void* v_cache, pa_cache_desc cache,
+                            const int32_t* slot_mapping, const int32_t* positions,
+                            const float* cos_sin, pa_rope_desc rope, int32_t num_tokens,
+                            const float* k_scale, const float* v_scale, pa_stream_t stream) {
+  const char* fn = "pa_rope_and_cache";
+  pa_status st = check_cache(cache, fn);
+  if (st != PA_OK) return st;
+  if ((st = check_scales(cache, k_scale, v_scale, fn)) != PA_OK) return st;
+  if (num_tokens < 0 || num_heads < 0)
+    return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: num_tokens or num_heads < 0");
+  const int32_t pairs = rope.rot_dim / 2;
+  if (rope.max_position <= 0 || rope.num_axes < 1)
+    return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: max_position and num_axes must be positive");
+  if (rope.rot_dim <= 0 || rope.rot_dim % 16 || rope.rot_dim > cache.head_dim || rope.num_axes > 4)
+    return pa_fail(PA_ERR_UNSUPPORTED,
+                   "pa_rope_and_cache: rot_dim must be a multiple of 16 up to head_dim, num_axes at most 4");
+  if (rope.num_axes > 1) {
+    int64_t sum = 0;
+    for (int a = 0; a < rope.num_axes; ++a) {
+      const int64_t n = rope.sections[a];
+      if (n < 0) return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: negative section");
+      sum += n;
+      if (rope.sections_in_turn && a > 0 && n > 0 && a + rope.num_axes * (n - 1) >= pairs)
+        return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: a section in turn runs past rot_dim / 2");
+    }
+    if (sum != pairs)
+      return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: sections must sum to rot_dim / 2");
+  }
+  const int64_t q_row = (int64_t)num_heads * cache.head_dim;
+  const int64_t kv_row = (int64_t)cache.num_kv_heads * cache.head_dim;
+  if (q_row + 2 * kv_row > (1 << 24))
+    return pa_fail(PA_ERR_UNSUPPORTED, "pa_rope_and_cache: too many heads");
+  if ((num_heads && (q_stride < q_row || q_stride % 8)) || k_stride < kv_row || k_stride % 8 ||
+      v_stride < kv_row || v_stride % 8)
+    return pa_fail(PA_ERR_INVALID,
+                   "pa_rope_and_cache: strides must be multiples of 8 and hold a token's heads");
+  if (num_tokens == 0) return PA_OK;
+  if ((num_heads && (!q_out || !query)) || !key || !value || !k_cache || !v_cache ||
+      !slot_mapping || !positions || !cos_sin)
+    return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: NULL pointer");
+  if (!aligned(q_out, 16) || !aligned(query, 16) || !aligned(key, 16) || !aligned(value, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 4) ||
+      !aligned(positions, 4) || !aligned(cos_sin, 4))
+    return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: misaligned pointer");
+  if (num_heads && !(q_out == query && q_stride == q_row)) {
+    // another layout over the same bytes would be read after it is written
+    const char* q0 = static_cast<const char*>(query);
+    const char* o0 = static_cast<const char*>(q_out);
+    const int64_t q_bytes = 2 * ((num_tokens - 1) * q_stride + q_row);
+    const int64_t o_bytes = 2 * num_tokens * q_row;
+    if (o0 < q0 + q_bytes && q0 < o0 + o_bytes)
+      return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: q_out overlaps query in another layout");
+  }
+  pa::RopeParams p = {};
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.query = static_cast<const __nv_bfloat16*>(query);
+  p.key = static_cast<const __nv_bfloat16*>(key);
+  p.value = static_cast<const __nv_bfloat16*>(value);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.num_slots = (int64_t)cache.num_blocks * cache.block_size;
+  p.num_tokens = num_tokens;
+  p.num_heads = num_heads;
+  p.num_kv_heads = cache.num_kv_heads;
+  p.rot_dim = rope.rot_dim;
+  p.max_position = rope.max_position;
+  p.num_axes = rope.num_axes;
+  for (int a = 0; a < 4; ++a) p.sections[a] = rope.sections[a];
+  p.in_turn = rope.sections_in_turn != 0;
+  p.adjacent = rope.adjacent_pairs != 0;
+  return cuda_status(pa::launch_rope_and_cache(p, cache.head_dim, cache.dtype == PA_KV_FP8_E4M3,
+                                               reinterpret_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+pa_status pa_summarize_blocks(const void* k_cache, pa_cache_desc cache,
+                              const int32_t* slot_mapping, int32_t num_tokens, int8_t* codes,
+                              float* scales, pa_stream_t stream) {
+  const char* fn = "pa_summarize_blocks";
+  pa_status st = check_cache(cache, fn);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0) return pa_fail(PA_ERR_INVALID, "pa_summarize_blocks: num_tokens < 0");
+  if ((int64_t)cache.num_kv_heads * cache.head_dim > (1 << 24))
+    return pa_fail(PA_ERR_UNSUPPORTED, "pa_summarize_blocks: too many heads");
+  if (num_tokens == 0) return PA_OK;
+  if (!k_cache || !slot_mapping || !codes || !scales)
+    return pa_fail(PA_ERR_INVALID, "pa_summarize_blocks: NULL pointer");
+  if (!aligned(k_cache, 16) || !aligned(slot_mapping, 4) || !aligned(codes, 16) ||
+      !aligned(scales, 4))
+    return pa_fail(PA_ERR_INVALID, "pa_summarize_blocks: misaligned pointer");
+  pa::SummaryParams p = {};
+  p.k_cache = k_cache;
+  p.slot_mapping = slot_mapping;
+  p.codes = codes;
+  p.scales = scales;
+  p.num_slots = (int64_t)cache.num_blocks * cache.block_size;
+  p.num_tokens = num_tokens;
+  p.num_kv_heads = cache.num_kv_heads;
+  p.log2_block_size = ilog2(cache.block_size);
+  return cuda_status(pa::launch_summarize_blocks(p, cache.head_dim, cache.dtype == PA_KV_FP8_E4M3,
+                                                 reinterpret_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+pa_status pa_select_blocks(int32_t* selected, const void* q, const int8_t* codes,
+                           const float* scales, pa_cache_desc cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens,
+                           const int32_t* row_seqs, int32_t num_rows, int32_t num_seqs,
+                           int32_t num_heads, int32_t top, int32_t sink, int32_t recent,
+                           pa_stream_t stream) {
+  const char* fn = "pa_select_blocks";
+  pa_status st = check_cache(cache, fn);
+  if (st != PA_OK) return st;
+  if ((st = check_rows(cache, max_blocks_per_seq, row_seqs, num_rows, num_seqs, num_heads, fn)) !=
+      PA_OK)
+    return st;
+  if (sink < 0 || recent < 1 || (int64_t)sink + recent > top)
+    return pa_fail(PA_ERR_INVALID,
+                   "pa_select_blocks: needs sink >= 0, recent >= 1 and sink + recent <= top");
+  if (max_blocks_per_seq > pa::kSelectMaxBlocks)
+    return pa_fail(PA_ERR_UNSUPPORTED, "pa_select_blocks: max_blocks_per_seq above 262144");
+  if (num_rows == 0) return PA_OK;
+  if (!selected || !q || !codes || !scales || !block_tables || !context_lens)
+    return pa_fail(PA_ERR_INVALID, "pa_select_blocks: NULL pointer");
+  if (!aligned(q, 16) || !aligned(codes, 16) || !aligned(selected, 4) || !aligned(scales, 4) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(row_seqs, 4))
+    return pa_fail(PA_ERR_INVALID, "pa_select_blocks: misaligned pointer");
+  pa::SelectParams p = {};
+  p.selected = selected;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.codes = codes;
+  p.scales = scales;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.row_seqs = row_seqs;
+  p.num_rows = num_rows;
+  p.num_seqs = num_seqs;
+  p.num_kv_heads = cache.num_kv_heads;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks_per_seq;
+  p.log2_block_size = ilog2(cache.block_size);
+  p.top = top;
+  p.sink = sink;
+  p.recent = recent;
+  return cuda_status(pa::launch_select_blocks(p, cache.head_dim, num_heads / cache.num_kv_heads,
+                                              num_sms(), reinterpret_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+pa_status pa_decode_selected(void* out, const void* q, const void* k_cache, const void* v_cache,
+                             pa_cache_desc cache, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             const int32_t* row_seqs, const int32_t* selected, int32_t num_rows,
+                             int32_t num_seqs, int32_t num_heads, int32_t top, float scale,
+                             const float* k_scale, const float* v_scale, pa_stream_t stream) {
+  const char* fn = "pa_decode_selected";
+  pa_status st = check_cache(cache, fn);
+  if (st != PA_OK) return st;
+  if ((st = check_scales(cache, k_scale, v_scale, fn)) != PA_OK) return st;
+  if ((st = check_rows(cache, max_blocks_per_seq, row_seqs, num_rows, num_seqs, num_heads, fn)) !=
+      PA_OK)
+    return st;
+  if (top < 1) return pa_fail(PA_ERR_INVALID, "pa_decode_selected: top must be positive");
+  if (top > pa::kSelectedMaxTop)
+    return pa_fail(PA_ERR_UNSUPPORTED, "pa_decode_selected: top above 4096");
+  if (!std::isfinite(scale))
+    return pa_fail(PA_ERR_INVALID, "pa_decode_selected: scale must be finite");
+  if (num_rows == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !selected)
+    return pa_fail(PA_ERR_INVALID, "pa_decode_selected: NULL pointer");
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(row_seqs, 4) ||
+      !aligned(selected, 4))
+    return pa_fail(PA_ERR_INVALID, "pa_decode_selected: misaligned pointer");
+  pa::SelectedParams p = {};
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.row_seqs = row_seqs;
+  p.selected = selected;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.num_rows = num_rows;
+  p.num_seqs = num_seqs;
+  p.num_kv_heads = cache.num_kv_heads;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks_per_seq;
+  p.log2_block_size = ilog2(cache.block_size);
+  p.top = top;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  return cuda_status(pa::launch_decode_selected(p, cache.head_dim, num_heads / cache.num_kv_heads,
+                                                cache.dtype == PA_KV_FP8_E4M3, num_sms(),
+                                                reinterpret_cast<cudaStream_t>(stream)),
                      fn);
 }
 

@@ -1,0 +1,501 @@
+// Decode attention over listed cache blocks.
+//
+// For query row r and KV head h with the listed blocks J,
+//   out = softmax(scale q . K_T^T) V_T,  T = the tokens of J's blocks below
+// the row's context length, for the head's G query heads together, so that
+// each K and V byte is read once.
+//
+// Bound: the listed blocks' bytes (at G = 4, 4 flop a byte).  Every KV head
+// of a row has a list of its own, so what is contiguous in memory is one
+// token's channels of one head (64 to 256 bytes); rows of that size are
+// gathered by 16-byte cp.async, and the matrix work beside them is small
+// enough for warp-level MMAs: each warp streams 16-token chunks through a
+// ring of its own in shared memory and keeps its own softmax state, so the
+// stream needs no barrier.  A warp's chunk:
+//   S^T [16 tokens x 8 columns] = K q^T     (mma m16n8k16, K by ldmatrix)
+//   p = 2^(s - m) per column, running max and sum in fp32
+//   O^T [D x 8 columns] += V^T P^T          (V by ldmatrix.trans)
+// Transposed so that the 16-row side of the MMA holds tokens and channels
+// and the query heads sit in the 8 columns; P turns from accumulator to
+// operand layout by movmatrix.  With G <= 4 the columns 4..7 repeat the
+// heads of columns 0..3 and carry what rounding takes from P (p - round(p)),
+// so P V keeps about 16 bits of P at no cost; with G = 8 a second MMA does.
+// An e4m3 cache is widened to f16 in registers (exact); q then enters in f16
+// under a power-of-two scale per head that puts its largest channel in
+// [1, 2) (f16 keeps 11 bits, bf16 q has 8, so channels down to 2^-16 of the
+// largest stay exact).
+// The warps' results meet in shared memory, those of the CTAs that share a
+// (row, KV head) in a cluster's distributed shared memory: no workspace, no
+// second kernel, and sums in a fixed order.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "launch.cuh"
+#include "pa_device.cuh"
+#include "pa_kernels.cuh"
+#include "tc_ptx.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kChunk = 16;  // tokens a warp handles at a time
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return pack_bf16x2_rn(lo, hi);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (F16)
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else
+    return make_float2(bf16_lo(w), bf16_hi(w));
+}
+// The two e4m3 values of a 16-bit half as an f16 pair.
+__device__ __forceinline__ uint32_t widen(uint16_t codes) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h2) : "h"(codes));
+  return h2;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ float load_peer(const float* own, uint32_t rank) {
+  uint32_t a;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_u32(own)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// The factor of a part whose running max is m under the whole's max; 1 where
+// neither has a token, so that a NaN among the logits still reaches the sums.
+__device__ __forceinline__ float weight(float m, float whole) {
+  return whole == -INFINITY ? 1.f : fast_exp2(m - whole);
+}
+// o / l, and zero for a row without tokens.
+__device__ __forceinline__ __nv_bfloat16 quotient(float o, float l) {
+  return __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+}
+
+template <int D, bool FP8>
+struct Cfg {
+  static constexpr int kRow = D * (FP8 ? 1 : 2);  // bytes of a token's channels
+  static constexpr int kPieces = kRow / 16;
+  static constexpr int kTile = kChunk * kRow;  // K (or V) bytes of a chunk
+  static constexpr int kStages = FP8 ? 4 : 3;
+  static constexpr int kRing = kWarps * kStages * 2 * kTile;
+  static constexpr int kMerge = kWarps * 8 * (D + 2) * 4;  // reuses the ring
+  static_assert(kMerge <= kRing, "the merge reuses the ring");
+  // 16-byte pieces of a tile's row, permuted so that 8 rows' pieces of one
+  // column (ldmatrix) fall in different banks
+  static __device__ __forceinline__ int swizzle(int row, int piece) {
+    if constexpr (kPieces >= 8)
+      return piece ^ (row & 7);
+    else
+      return piece ^ ((row >> 1) & 3);
+  }
+};
+
+template <int D, int G, bool FP8>
+__global__ void __launch_bounds__(kThreads)
+    decode_selected_kernel(const __grid_constant__ SelectedParams p, int clusters) {
+  using C = Cfg<D, FP8>;
+  constexpr int kSteps = D / 16;  // k16 steps of q . k; m16 tiles of O^T
+  extern __shared__ __align__(128) uint8_t smem[];
+  // listed entries of this CTA's share: first slot of the block, tokens in use
+  int2* s_entry = reinterpret_cast<int2*>(smem + C::kRing);
+  __shared__ int s_last;
+  __shared__ float s_out[G][D];        // the CTA's result, for the cluster
+  __shared__ float s_m[8], s_l[8];
+  ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int g = lane / 4, c = lane % 4;  // MMA fragment coordinates
+  const int unit = blockIdx.x / clusters, rank = blockIdx.x % clusters;
+  const int row = unit / p.num_kv_heads, kvh = unit - row * p.num_kv_heads;
+  const int seq = p.row_seqs ? p.row_seqs[row] : row;
+  const int lb = p.log2_block_size, block = 1 << lb;
+  int64_t n = p.context_lens[row];
+  n = min(n, (int64_t)p.max_blocks << lb);
+  if ((unsigned)seq >= (unsigned)p.num_seqs) n = 0;
+  const int32_t* list = p.selected + (int64_t)unit * p.top;
+  const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks;
+
+  // entries up to the last that names a block below the context's end
+  if (tid == 0) s_last = 0;
+  __syncthreads();
+  int last = 0;
+  for (int i = tid; i < p.top; i += kThreads) {
+    const int j = list[i];
+    if (j >= 0 && ((int64_t)j << lb) < n) last = i + 1;
+  }
+  last = __reduce_max_sync(0xffffffffu, last);
+  if (lane == 0 && last) atomicMax(&s_last, last);
+  __syncthreads();
+  last = s_last;
+  // this CTA's share: an equal run of 16-token chunks
+  const int all_chunks = ((last << lb) + kChunk - 1) / kChunk;  // top << lb is below 2^23
+  const int per = (all_chunks + clusters - 1) / clusters;
+  const int c0 = min(rank * per, all_chunks);
+  const int chunks = min(c0 + per, all_chunks) - c0;
+  const int slot0 = c0 * kChunk;  // in list order
+  const int e0 = slot0 >> lb;
+  const int e1 = chunks ? min(last, ((slot0 + chunks * kChunk - 1) >> lb) + 1) : e0;
+  for (int i = e0 + tid; i < e1; i += kThreads) {
+    const int j = list[i];
+    int2 e = make_int2(0, 0);
+    if (j >= 0 && ((int64_t)j << lb) < n) {
+      const int phys = table[j];
+      if ((unsigned)phys < (unsigned)p.num_blocks)
+        e = make_int2(phys << lb, (int)min((int64_t)block, n - ((int64_t)j << lb)));
+    }
+    s_entry[i - e0] = e;
+  }
+
+  // q as MMA operand B: column `col` is query head col (mod 4 when G <= 4)
+  constexpr int kColHeads = G <= 4 ? 4 : 8;
+  const int qh = g % kColHeads;
+  uint32_t qb[kSteps][2];
+  float q_scale = 1.f;  // FP8: what q's columns were divided by
+  {
+    const __nv_bfloat16* q = p.q + ((int64_t)(row * p.num_kv_heads + kvh) * G + qh) * D;
+    const bool real = qh < G;
+    if constexpr (FP8) {
+      uint2 w[kSteps];
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        w[k] = real ? *reinterpret_cast<const uint2*>(q + 16 * k + 4 * c) : make_uint2(0, 0);
+        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(w[k].x)), fabsf(bf16_hi(w[k].x))),
+                                 fmaxf(fabsf(bf16_lo(w[k].y)), fabsf(bf16_hi(w[k].y)))));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 2^floor(log2 amax); kept within the normal floats so that its
+      // reciprocal is exact (an infinite or NaN q stays what it is)
+      const int e = min(max((int)(__float_as_uint(amax) >> 23), 1), 253) - 127;
+      q_scale = __int_as_float((127 + e) << 23);
+      const float inv = __int_as_float((127 - e) << 23);
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        qb[k][0] = pack2<true>(bf16_lo(w[k].x) * inv, bf16_hi(w[k].x) * inv);
+        qb[k][1] = pack2<true>(bf16_lo(w[k].y) * inv, bf16_hi(w[k].y) * inv);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        qb[k][0] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c) : 0u;
+        qb[k][1] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 + 2 * c) : 0u;
+      }
+    }
+  }
+  // the logit factors of this lane's two accumulator columns 2c, 2c + 1
+  float f0 = p.scale_log2, f1 = p.scale_log2, v_scale = 1.f;
+  if constexpr (FP8) {
+    const float ks = *p.k_scale;
+    v_scale = *p.v_scale;
+    f0 *= ks * __shfl_sync(0xffffffffu, q_scale, 4 * (2 * c));
+    f1 *= ks * __shfl_sync(0xffffffffu, q_scale, 4 * (2 * c + 1));
+  }
+  __syncthreads();  // entries
+
+  const uint32_t ring = smem_u32(smem) + warp * C::kStages * 2 * C::kTile;
+  const int64_t stride = (int64_t)p.num_kv_heads * C::kRow;  // between tokens
+  const uint8_t* kbase = static_cast<const uint8_t*>(p.k_cache) + (int64_t)kvh * C::kRow;
+  const uint8_t* vbase = static_cast<const uint8_t*>(p.v_cache) + (int64_t)kvh * C::kRow;
+  const int my = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;  // this warp's chunks
+
+  auto load = [&](int it) {
+    if (it < my) {
+      const int s0 = slot0 + (warp + it * kWarps) * kChunk;
+      const uint32_t stage = ring + (it % C::kStages) * 2 * C::kTile;
+      constexpr int kRowsPer = 32 / C::kPieces;  // tokens per instruction
+      const int piece = lane % C::kPieces;
+#pragma unroll
+      for (int r = 0; r < kChunk / kRowsPer; ++r) {
+        const int t = r * kRowsPer + lane / C::kPieces;
+        const int e = ((s0 + t) >> lb) - e0, off = (s0 + t) & (block - 1);
+        int2 en = make_int2(0, 0);
+        if (e < e1 - e0) en = s_entry[e];
+        const bool in = off < en.y;
+        const int64_t at = (int64_t)(in ? en.x + off : 0) * stride + piece * 16;
+        const uint32_t dst = stage + t * C::kRow + C::swizzle(t, piece) * 16;
+        cp_async_16(dst, kbase + at, in ? 16 : 0);  // zeros where there is no token
+        cp_async_16(dst + C::kTile, vbase + at, in ? 16 : 0);
+      }
+    }
+    cp_async_commit();
+  };
+
+  float o[kSteps][4];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+#pragma unroll
+  for (int s = 0; s < C::kStages - 1; ++s) load(s);
+  for (int it = 0; it < my; ++it) {
+    load(it + C::kStages - 1);
+    cp_async_wait<C::kStages - 1>();
+    __syncwarp();
+    const uint32_t kt = ring + (it % C::kStages) * 2 * C::kTile;
+    const uint32_t vt = kt + C::kTile;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+      const uint32_t base = kt + r * C::kRow;
+      if constexpr (FP8) {
+#pragma unroll
+        for (int k = 0; k < kSteps; k += 2) {
+          uint32_t w[4];
+          ldmatrix_x4(w, base + C::swizzle(r, k + (lane >> 4)) * 16);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // the two 16-channel pieces
+            const uint32_t x = w[2 * h], y = w[2 * h + 1];
+            const uint32_t a[4] = {widen((uint16_t)x), widen((uint16_t)y),
+                                   widen((uint16_t)(x >> 16)), widen((uint16_t)(y >> 16))};
+            mma16816<true>(s, a, qb[k + h][0], qb[k + h][1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t a[4];
+          ldmatrix_x4(a, base + C::swizzle(r, 2 * k + (lane >> 4)) * 16);
+          mma16816<false>(s, a, qb[k][0], qb[k][1]);
+        }
+      }
+    }
+    // tokens g and g + 8 of the chunk, columns 2c and 2c + 1
+    const int s0 = slot0 + (warp + it * kWarps) * kChunk;
+    bool in[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int sl = s0 + g + 8 * h;
+      const int e = (sl >> lb) - e0;
+      in[h] = e < e1 - e0 && (sl & (block - 1)) < s_entry[e].y;
+    }
+    const float x00 = in[0] ? s[0] * f0 : -INFINITY, x01 = in[0] ? s[1] * f1 : -INFINITY;
+    const float x10 = in[1] ? s[2] * f0 : -INFINITY, x11 = in[1] ? s[3] * f1 : -INFINITY;
+    float n0 = fmaxf(x00, x10), n1 = fmaxf(x01, x11);
+#pragma unroll
+    for (int d = 4; d < 32; d *= 2) {
+      n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
+      n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, d));
+    }
+    n0 = fmaxf(n0, m0);
+    n1 = fmaxf(n1, m1);
+    if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+      const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0);
+      const float a1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
+      l0 *= a0;
+      l1 *= a1;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        o[i][0] *= a0;
+        o[i][1] *= a1;
+        o[i][2] *= a0;
+        o[i][3] *= a1;
+      }
+      m0 = n0;
+      m1 = n1;
+    }
+    const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+    const float p00 = fast_exp2(x00 - z0), p01 = fast_exp2(x01 - z1);
+    const float p10 = fast_exp2(x10 - z0), p11 = fast_exp2(x11 - z1);
+    l0 += p00 + p10;
+    l1 += p01 + p11;
+    uint32_t hi0 = pack2<FP8>(p00, p01), hi1 = pack2<FP8>(p10, p11);
+    const float2 r0 = unpack2<FP8>(hi0), r1 = unpack2<FP8>(hi1);
+    uint32_t lo0 = pack2<FP8>(p00 - r0.x, p01 - r0.y), lo1 = pack2<FP8>(p10 - r1.x, p11 - r1.y);
+    if constexpr (G <= 4) {  // columns 4..7 carry the remainders
+      if (c >= 2) {
+        hi0 = lo0;
+        hi1 = lo1;
+      }
+    }
+    const uint32_t b0 = movmatrix_trans(hi0), b1 = movmatrix_trans(hi1);
+    uint32_t d0 = 0, d1 = 0;
+    if constexpr (G > 4) {
+      d0 = movmatrix_trans(lo0);
+      d1 = movmatrix_trans(lo1);
+    }
+    if constexpr (FP8) {
+      // a transposed 16-bit unit holds channels 2g and 2g + 1 of a token: the
+      // even ones become row g of the tile, the odd ones row g + 8
+      const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+      for (int k = 0; k < kSteps; k += 2) {
+        uint32_t w[4];
+        ldmatrix_x4_trans(w, vt + r * C::kRow + C::swizzle(r, k + (lane >> 4)) * 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = __byte_perm(w[2 * h], 0, 0x3120), y = __byte_perm(w[2 * h + 1], 0, 0x3120);
+          const uint32_t a[4] = {widen((uint16_t)x), widen((uint16_t)(x >> 16)),
+                                 widen((uint16_t)y), widen((uint16_t)(y >> 16))};
+          mma16816<true>(o[k + h], a, b0, b1);
+          if constexpr (G > 4) mma16816<true>(o[k + h], a, d0, d1);
+        }
+      }
+    } else {
+      const int r = (lane & 7) + (lane >> 4) * 8;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        uint32_t a[4];
+        ldmatrix_x4_trans(a, vt + r * C::kRow + C::swizzle(r, 2 * k + ((lane >> 3) & 1)) * 16);
+        mma16816<false>(o[k], a, b0, b1);
+        if constexpr (G > 4) mma16816<false>(o[k], a, d0, d1);
+      }
+    }
+    __syncwarp();  // the stage may be filled again
+  }
+  cp_async_wait<0>();
+
+  // the warps' results: max, sum and channels per column
+#pragma unroll
+  for (int d = 4; d < 32; d *= 2) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+  }
+  __syncthreads();  // the ring is free
+  float* mo = reinterpret_cast<float*>(smem);  // [warp][column][D]
+  float* ml = mo + kWarps * 8 * D;             // [warp][column][2]
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int d0 = 16 * i + (FP8 ? 2 * g : g), d1 = FP8 ? d0 + 1 : d0 + 8;
+    float* w0 = mo + (warp * 8 + 2 * c) * D;
+    w0[d0] = o[i][0];
+    w0[D + d0] = o[i][1];
+    w0[d1] = o[i][2];
+    w0[D + d1] = o[i][3];
+  }
+  if (g == 0) {
+    float* w = ml + (warp * 8 + 2 * c) * 2;
+    w[0] = m0;
+    w[1] = l0;
+    w[2] = m1;
+    w[3] = l1;
+  }
+  __syncthreads();
+  // every CTA of the cluster: its own result, unnormalised
+  for (int i = tid; i < G * D; i += kThreads) {
+    const int h = i / D, d = i % D;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[(w * 8 + h) * 2]);
+    float acc = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float a = weight(ml[(w * 8 + h) * 2], mm);
+      float x = mo[(w * 8 + h) * D + d];
+      if (G <= 4) x += mo[(w * 8 + h + 4) * D + d];
+      acc += a * x;
+      l += a * ml[(w * 8 + h) * 2 + 1];
+    }
+    __nv_bfloat16* out = p.out + ((int64_t)(row * p.num_kv_heads + kvh) * G + h) * D + d;
+    if (clusters == 1) {
+      *out = quotient(acc * v_scale, l);
+    } else {
+      s_out[h][d] = acc;
+      if (d == 0) {
+        s_m[h] = mm;
+        s_l[h] = l;
+      }
+    }
+  }
+  if (clusters == 1) return;
+  cluster_sync();
+  for (int i = rank * kThreads + tid; i < G * D; i += clusters * kThreads) {
+    const int h = i / D, d = i % D;
+    float mm = -INFINITY;
+    for (int r = 0; r < clusters; ++r) mm = fmaxf(mm, load_peer(&s_m[h], r));
+    float acc = 0.f, l = 0.f;
+    for (int r = 0; r < clusters; ++r) {
+      const float a = weight(load_peer(&s_m[h], r), mm);
+      acc += a * load_peer(&s_out[h][d], r);
+      l += a * load_peer(&s_l[h], r);
+    }
+    p.out[((int64_t)(row * p.num_kv_heads + kvh) * G + h) * D + d] = quotient(acc * v_scale, l);
+  }
+  cluster_sync();  // no CTA leaves while a peer may read its memory
+}
+
+template <int D, int G, bool FP8>
+cudaError_t launch_one(const SelectedParams& p, int num_sms, cudaStream_t stream) {
+  using C = Cfg<D, FP8>;
+  const int64_t units = (int64_t)p.num_rows * p.num_kv_heads;
+  const int64_t tokens = (int64_t)p.top << p.log2_block_size;  // of a unit, at most
+  int c = 1;
+  while (c < 8 && units * c < 2 * num_sms && tokens / (2 * c) >= 128) c *= 2;
+  const size_t smem = C::kRing + (size_t)p.top * sizeof(int2);
+  return launch_dependent(decode_selected_kernel<D, G, FP8>, dim3((unsigned)(units * c)),
+                          dim3(kThreads), smem, stream, c, p, c);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_g(const SelectedParams& p, int group, int num_sms, cudaStream_t stream) {
+  switch (group) {
+    case 1: return launch_one<D, 1, FP8>(p, num_sms, stream);
+    case 2: return launch_one<D, 2, FP8>(p, num_sms, stream);
+    case 4: return launch_one<D, 4, FP8>(p, num_sms, stream);
+    case 8: return launch_one<D, 8, FP8>(p, num_sms, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_decode_selected(const SelectedParams& p, int head_dim, int group, bool fp8,
+                                   int num_sms, cudaStream_t stream) {
+  if (head_dim == 128)
+    return fp8 ? launch_g<128, true>(p, group, num_sms, stream)
+               : launch_g<128, false>(p, group, num_sms, stream);
+  return fp8 ? launch_g<64, true>(p, group, num_sms, stream)
+             : launch_g<64, false>(p, group, num_sms, stream);
+}
+
+}  // namespace pa

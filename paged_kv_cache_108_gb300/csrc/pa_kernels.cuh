@@ -1,6 +1,7 @@
 // Internal declarations of the library's kernels and their launch helpers.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -138,5 +139,74 @@ cudaError_t launch_copy_blocks(void* k_cache, void* v_cache,
                                int64_t block_bytes, int num_blocks,
                                const int32_t* pairs, int num_pairs,
                                cudaStream_t stream);
+
+// Rotation and cache write (rope_cache.cu).  Strides in elements.
+struct RopeParams {
+  __nv_bfloat16* q_out;        // [N, H, D]
+  const __nv_bfloat16* query;  // N rows of [H, D], q_stride apart
+  const __nv_bfloat16* key;
+  const __nv_bfloat16* value;
+  int64_t q_stride, k_stride, v_stride;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* slot_mapping;  // [N]
+  const int32_t* positions;     // [num_axes, N]
+  const float* cos_sin;         // [max_position, rot_dim]: cosines, then sines
+  const float* k_scale;         // fp8 only
+  const float* v_scale;
+  int64_t num_slots;
+  int64_t num_tokens;
+  int32_t num_heads, num_kv_heads;
+  int32_t rot_dim, max_position;
+  int32_t num_axes, sections[4], in_turn, adjacent;
+  int32_t tokens_per_cta;  // set by the launch
+};
+cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, cudaStream_t stream);
+
+// Key ranges of full blocks and block selection (block_select.cu).
+struct SummaryParams {
+  const void* k_cache;          // [NB, B, Hkv, D]
+  const int32_t* slot_mapping;  // [N]
+  int8_t* codes;                // [NB, Hkv, 2, D]: maxima, then minima
+  float* scales;                // [NB, Hkv]
+  int64_t num_slots;
+  int32_t num_tokens, num_kv_heads, log2_block_size;
+};
+cudaError_t launch_summarize_blocks(const SummaryParams& p, int head_dim, bool fp8,
+                                    cudaStream_t stream);
+
+struct SelectParams {
+  int32_t* selected;           // [R, Hkv, top]
+  const __nv_bfloat16* q;      // [R, H, D]
+  const int8_t* codes;         // [NB, Hkv, 2, D]
+  const float* scales;         // [NB, Hkv]
+  const int32_t* block_tables;  // [S, max_blocks]
+  const int32_t* context_lens;  // [R]
+  const int32_t* row_seqs;      // [R] or null (row r is sequence r)
+  int32_t num_rows, num_seqs, num_kv_heads, num_blocks, max_blocks, log2_block_size;
+  int32_t top, sink, recent;
+};
+constexpr int kSelectMaxBlocks = 262144;  // table entries per sequence at most
+cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, int group, int num_sms,
+                                 cudaStream_t stream);
+
+// Decode over listed blocks (decode_selected.cu).
+struct SelectedParams {
+  __nv_bfloat16* out;     // [R, H, D]
+  const __nv_bfloat16* q;
+  const void* k_cache;    // [NB, B, Hkv, D]
+  const void* v_cache;
+  const int32_t* block_tables;  // [S, max_blocks]
+  const int32_t* context_lens;  // [R]
+  const int32_t* row_seqs;      // [R] or null
+  const int32_t* selected;      // [R, Hkv, top]
+  const float* k_scale;         // fp8 only
+  const float* v_scale;
+  int32_t num_rows, num_seqs, num_kv_heads, num_blocks, max_blocks, log2_block_size, top;
+  float scale_log2;  // scale * log2(e)
+};
+constexpr int kSelectedMaxTop = 4096;  // list entries at most
+cudaError_t launch_decode_selected(const SelectedParams& p, int head_dim, int group, bool fp8,
+                                   int num_sms, cudaStream_t stream);
 
 }  // namespace pa

@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import CacheDesc, DecodeOpts, PA_KV_BF16, PA_KV_FP8_E4M3
+from ._lib import CacheDesc, DecodeOpts, PA_KV_BF16, PA_KV_FP8_E4M3, RopeDesc
 
 _FP8_DTYPES = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
 
@@ -324,6 +324,186 @@ def write_and_decode(key, value, slot_mapping, out, q, k_cache, v_cache, block_t
         _dev(v_cache, "v_cache"), desc, _dev(block_tables, "block_tables", torch.int32),
         int(block_tables.shape[1]), _dev(context_lens, "context_lens", torch.int32), num_seqs,
         num_heads, ctypes.c_float(scale), ks, vs, ws_ptr, ws_bytes, _stream(stream)))
+    return out
+
+
+class _on_device:
+    """Makes the tensors' device current for a call and checks that they share
+    it; the call's default stream is that device's current one."""
+
+    def __init__(self, **tensors):
+        devices = {t.device for t in tensors.values() if t is not None}
+        if len(devices) > 1:
+            raise ValueError(f"{', '.join(tensors)} must be on one device")
+        index = devices.pop().index
+        self._guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _head_rows(t: torch.Tensor, name: str):
+    """Pointer and token stride of a [tokens, heads, head_dim] tensor whose
+    tokens may lie apart (a slice of a projection's output)."""
+    ptr = _dev(t, name, torch.bfloat16, contiguous=False)
+    n, h, d = t.shape
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: a token's heads and channels must be contiguous")
+    return ptr, (t.stride(0) if n > 1 else h * d)
+
+
+def rope_and_cache(q_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                   k_scale=None, v_scale=None, sections=None, sections_in_turn=False,
+                   adjacent_pairs=False, stream=None) -> None:
+    """``reshape_and_cache`` with the position rotation applied on the way:
+    queries [N, H_q, d] rotated into ``q_out`` (contiguous; ``query`` itself
+    if that is), keys [N, H_kv, d] rotated into the cache, values as they are.
+    Tokens of query, key and value may lie apart.  ``positions``: [N] or
+    [axes, N] int32; ``cos_sin``: [max_position, rot_dim] fp32, cosines then
+    sines; ``sections``: pairs turned by each axis."""
+    _same_cache(k_cache, v_cache)
+    desc = cache_desc(k_cache)
+    ks, vs = _scales(desc, k_scale, v_scale)
+    n = int(slot_mapping.numel())
+    want = (n, desc.num_kv_heads, desc.head_dim)
+    if tuple(key.shape) != want or tuple(value.shape) != want:
+        raise ValueError(f"key and value must be {list(want)} (one row per slot), "
+                         f"got {list(key.shape)} and {list(value.shape)}")
+    if query.dim() != 3 or query.shape[0] != n or query.shape[2] != desc.head_dim \
+            or q_out.shape != query.shape:
+        raise ValueError(f"query and q_out must be [{n}, num_heads, {desc.head_dim}], "
+                         f"got {list(query.shape)} and {list(q_out.shape)}")
+    axes = 1 if positions.dim() == 1 else int(positions.shape[0])
+    if positions.dim() not in (1, 2) or positions.shape[-1] != n:
+        raise ValueError(f"positions must be [{n}] or [axes, {n}], got {list(positions.shape)}")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_position, rot_dim]")
+    max_position, rot_dim = cos_sin.shape
+    sections = [rot_dim // 2] if sections is None and axes == 1 else list(sections or ())
+    if len(sections) != axes:
+        raise ValueError(f"sections must have one entry for each of the {axes} position axes")
+    if axes > 4:
+        raise ValueError("at most 4 position axes")
+    rope = RopeDesc(int(rot_dim), int(max_position), axes,
+                    (ctypes.c_int32 * 4)(*(int(x) for x in sections)), int(sections_in_turn),
+                    int(adjacent_pairs))
+    (qp, q_stride), (kp, k_stride), (vp, v_stride) = (
+        _head_rows(query, "query"), _head_rows(key, "key"), _head_rows(value, "value"))
+    args = (_dev(q_out, "q_out", torch.bfloat16), qp, q_stride, int(query.shape[1]), kp, k_stride,
+            vp, v_stride, _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), desc,
+            _dev(slot_mapping, "slot_mapping", torch.int32),
+            _dev(positions, "positions", torch.int32), _dev(cos_sin, "cos_sin", torch.float32),
+            rope, n, ks, vs)
+    with _on_device(q_out=q_out, query=query, key=key, value=value, k_cache=k_cache,
+                    v_cache=v_cache, slot_mapping=slot_mapping, positions=positions,
+                    cos_sin=cos_sin, k_scale=k_scale, v_scale=v_scale):
+        _lib.check(_lib.lib().pa_rope_and_cache(*args, _stream(stream)))
+
+
+def _check_ranges(desc, codes, scales):
+    if tuple(codes.shape) != (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim):
+        raise ValueError(f"codes must be [num_blocks, num_kv_heads, 2, head_dim] = "
+                         f"{[desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim]}, "
+                         f"got {list(codes.shape)}")
+    if tuple(scales.shape) != (desc.num_blocks, desc.num_kv_heads):
+        raise ValueError(f"scales must be [num_blocks, num_kv_heads] = "
+                         f"{[desc.num_blocks, desc.num_kv_heads]}, got {list(scales.shape)}")
+
+
+def alloc_block_ranges(k_cache):
+    """(codes, scales) for a cache: zeroed int8 [num_blocks, H_kv, 2, d] and
+    fp32 [num_blocks, H_kv] on its device."""
+    desc = cache_desc(k_cache)
+    return (torch.zeros(desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim, dtype=torch.int8,
+                        device=k_cache.device),
+            torch.zeros(desc.num_blocks, desc.num_kv_heads, dtype=torch.float32,
+                        device=k_cache.device))
+
+
+def summarize_blocks(k_cache, slot_mapping, codes, scales, stream=None) -> None:
+    """Keys' range per channel, in 8 bits, of every block whose last slot is
+    in ``slot_mapping`` (the step's writes, already done on the stream)."""
+    desc = cache_desc(k_cache)
+    _check_ranges(desc, codes, scales)
+    args = (_dev(k_cache, "k_cache"), desc, _dev(slot_mapping, "slot_mapping", torch.int32),
+            int(slot_mapping.numel()), _dev(codes, "codes", torch.int8),
+            _dev(scales, "scales", torch.float32))
+    with _on_device(k_cache=k_cache, slot_mapping=slot_mapping, codes=codes, scales=scales):
+        _lib.check(_lib.lib().pa_summarize_blocks(*args, _stream(stream)))
+
+
+def _check_rows(q, block_tables, context_lens, row_seqs, selected, num_kv_heads):
+    """Sizes shared by the calls over query rows; (rows, sequences)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [num_rows, num_heads, head_dim]")
+    rows = int(q.shape[0])
+    if block_tables.dim() != 2 or (row_seqs is None and block_tables.shape[0] != rows):
+        raise ValueError(f"block_tables must be [{'num_seqs' if row_seqs is not None else rows}, "
+                         f"max_blocks_per_seq], got {list(block_tables.shape)}")
+    if context_lens.numel() != rows:
+        raise ValueError(f"context_lens needs {rows} entries, got {context_lens.numel()}")
+    if row_seqs is not None and row_seqs.numel() != rows:
+        raise ValueError(f"row_seqs needs {rows} entries, got {row_seqs.numel()}")
+    if selected.dim() != 3 or tuple(selected.shape[:2]) != (rows, num_kv_heads):
+        raise ValueError(f"selected must be [{rows}, {num_kv_heads}, top], "
+                         f"got {list(selected.shape)}")
+    return rows, int(block_tables.shape[0])
+
+
+def select_blocks(selected, q, codes, scales, block_tables, context_lens, block_size, sink=1,
+                  recent=1, row_seqs=None, stream=None):
+    """The blocks each query row attends to, per KV head: writes ``selected``
+    [num_rows, H_kv, top] int32 (rising logical block indices, then -1) and
+    returns it.  ``row_seqs`` [num_rows] names each row's sequence when there
+    are several queries to one."""
+    if codes.dim() != 4 or codes.shape[2] != 2:
+        raise ValueError("codes must be [num_blocks, num_kv_heads, 2, head_dim]")
+    nb, hkv, _, d = codes.shape
+    desc = CacheDesc(int(nb), int(block_size), int(hkv), int(d), PA_KV_BF16)
+    _check_ranges(desc, codes, scales)
+    rows, seqs = _check_rows(q, block_tables, context_lens, row_seqs, selected, hkv)
+    if q.shape[2] != d:
+        raise ValueError(f"q's head_dim {q.shape[2]} differs from the codes' {d}")
+    args = (_dev(selected, "selected", torch.int32), _dev(q, "q", torch.bfloat16),
+            _dev(codes, "codes", torch.int8), _dev(scales, "scales", torch.float32), desc,
+            _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
+            _dev(context_lens, "context_lens", torch.int32),
+            None if row_seqs is None else _dev(row_seqs, "row_seqs", torch.int32), rows, seqs,
+            int(q.shape[1]), int(selected.shape[2]), int(sink), int(recent))
+    with _on_device(selected=selected, q=q, codes=codes, scales=scales,
+                    block_tables=block_tables, context_lens=context_lens, row_seqs=row_seqs):
+        _lib.check(_lib.lib().pa_select_blocks(*args, _stream(stream)))
+    return selected
+
+
+def decode_selected(out, q, k_cache, v_cache, block_tables, context_lens, selected, scale,
+                    k_scale=None, v_scale=None, row_seqs=None, stream=None):
+    """``decode`` over the blocks listed in ``selected`` [num_rows, H_kv, top];
+    writes ``out`` [num_rows, H_q, d] bf16 and returns it."""
+    _same_cache(k_cache, v_cache)
+    desc = cache_desc(k_cache)
+    ks, vs = _scales(desc, k_scale, v_scale)
+    if out.shape != q.shape:
+        raise ValueError("q and out must both be [num_rows, num_heads, head_dim]")
+    rows, seqs = _check_rows(q, block_tables, context_lens, row_seqs, selected, desc.num_kv_heads)
+    if q.shape[2] != desc.head_dim:
+        raise ValueError(f"q's head_dim {q.shape[2]} differs from the cache's {desc.head_dim}")
+    args = (_dev(out, "out", torch.bfloat16), _dev(q, "q", torch.bfloat16),
+            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), desc,
+            _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
+            _dev(context_lens, "context_lens", torch.int32),
+            None if row_seqs is None else _dev(row_seqs, "row_seqs", torch.int32),
+            _dev(selected, "selected", torch.int32), rows, seqs, int(q.shape[1]),
+            int(selected.shape[2]), ctypes.c_float(scale), ks, vs)
+    with _on_device(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                    context_lens=context_lens, row_seqs=row_seqs, selected=selected,
+                    k_scale=k_scale, v_scale=v_scale):
+        _lib.check(_lib.lib().pa_decode_selected(*args, _stream(stream)))
     return out
 
 
