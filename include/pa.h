@@ -616,7 +616,7 @@ pa_status pa_summarize_blocks(const void* k_cache, pa_cache_desc cache,
  *  sink, recent  sink >= 0, recent >= 1, sink + recent <= top.  With recent
  *                >= 1 a block that is not full yet is never scored.
  *  Limits: num_heads / num_kv_heads in {1, 2, 4, 8}; max_blocks_per_seq up
- *  to 262144; num_rows * num_kv_heads up to 2^27; else PA_ERR_UNSUPPORTED.
+ *  to 196608; num_rows * num_kv_heads up to 2^27; else PA_ERR_UNSUPPORTED.
  *  num_rows == 0 is valid and launches nothing.
  * ---------------------------------------------------------------------- */
 pa_status pa_select_blocks(int32_t* selected, const void* q, const int8_t* codes,

@@ -115,6 +115,8 @@ SIGNATURES = {
 def lib():
     """The loaded library (built on first use if the CUDA toolkit is here)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -993,7 +993,7 @@ pa_status pa_select_blocks(int32_t* selected, const void* q, const int8_t* codes
     return pa_fail(PA_ERR_INVALID,
                    "pa_select_blocks: needs sink >= 0, recent >= 1 and sink + recent <= top");
   if (max_blocks_per_seq > pa::kSelectMaxBlocks)
-    return pa_fail(PA_ERR_UNSUPPORTED, "pa_select_blocks: max_blocks_per_seq above 262144");
+    return pa_fail(PA_ERR_UNSUPPORTED, "pa_select_blocks: max_blocks_per_seq above 196608");
   if (num_rows == 0) return PA_OK;
   if (!selected || !q || !codes || !scales || !block_tables || !context_lens)
     return pa_fail(PA_ERR_INVALID, "pa_select_blocks: NULL pointer");

@@ -186,7 +186,7 @@ struct SelectParams {
   int32_t num_rows, num_seqs, num_kv_heads, num_blocks, max_blocks, log2_block_size;
   int32_t top, sink, recent;
 };
-constexpr int kSelectMaxBlocks = 262144;  // table entries per sequence at most
+constexpr int kSelectMaxBlocks = 196608;  // table entries per sequence at most
 cudaError_t launch_select_blocks(const SelectParams& p, int head_dim, int group, int num_sms,
                                  cudaStream_t stream);
 

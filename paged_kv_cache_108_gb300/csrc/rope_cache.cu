@@ -199,10 +199,12 @@ cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, cudaStre
   t = t < 1 ? 1 : (t > kRopeMaxTokens ? kRopeMaxTokens : t);
   p.tokens_per_cta = (int)t;
   const int64_t grid = (p.num_tokens + t - 1) / t;
-  auto kernel = head_dim == 128
-                    ? (fp8 ? rope_and_cache_kernel<128, true> : rope_and_cache_kernel<128, false>)
-                    : (fp8 ? rope_and_cache_kernel<64, true> : rope_and_cache_kernel<64, false>);
-  return launch_dependent(kernel, dim3((unsigned)grid), dim3(kRopeThreads), 0, stream, 1, p);
+  const dim3 g((unsigned)grid), b(kRopeThreads);
+  if (head_dim == 128)
+    return fp8 ? launch_dependent<rope_and_cache_kernel<128, true>>(g, b, 0, stream, 1, p)
+               : launch_dependent<rope_and_cache_kernel<128, false>>(g, b, 0, stream, 1, p);
+  return fp8 ? launch_dependent<rope_and_cache_kernel<64, true>>(g, b, 0, stream, 1, p)
+             : launch_dependent<rope_and_cache_kernel<64, false>>(g, b, 0, stream, 1, p);
 }
 
 }  // namespace pa

@@ -7,6 +7,7 @@ Names and argument order follow include/pa.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -327,34 +328,68 @@ def write_and_decode(key, value, slot_mapping, out, q, k_cache, v_cache, block_t
     return out
 
 
-class _on_device:
-    """Makes the tensors' device current for a call and checks that they share
-    it; the call's default stream is that device's current one."""
+# The block-sparse step's calls take 5 to 15 us on the device for a decode
+# batch, so their binding is kept short: one pass over the tensors, cached
+# descriptors (plain sizes), the raw stream handle.
 
-    def __init__(self, **tensors):
-        devices = {t.device for t in tensors.values() if t is not None}
-        if len(devices) > 1:
-            raise ValueError(f"{', '.join(tensors)} must be on one device")
-        index = devices.pop().index
-        self._guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+@functools.lru_cache(maxsize=256)
+def _desc_of(num_blocks, block_size, num_kv_heads, head_dim, dtype) -> CacheDesc:
+    return CacheDesc(num_blocks, block_size, num_kv_heads, head_dim, dtype)
 
 
-def _head_rows(t: torch.Tensor, name: str):
+@functools.lru_cache(maxsize=256)
+def _rope_of(rot_dim, max_position, axes, sections, in_turn, adjacent) -> RopeDesc:
+    return RopeDesc(rot_dim, max_position, axes, (ctypes.c_int32 * 4)(*sections), in_turn, adjacent)
+
+
+def _desc_cached(k_cache) -> CacheDesc:
+    dt = k_cache.dtype
+    if k_cache.dim() != 4 or not (dt is torch.bfloat16 or dt in _FP8_DTYPES):
+        return cache_desc(k_cache)  # raises
+    return _desc_of(*k_cache.shape, PA_KV_BF16 if dt is torch.bfloat16 else PA_KV_FP8_E4M3)
+
+
+def _pointers(device: int, *tensors):
+    """Addresses of (tensor, name, dtype or None) items, None for an absent
+    tensor; each must be contiguous on CUDA device ``device``."""
+    out = []
+    for t, name, dtype in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not isinstance(t, torch.Tensor) or t.get_device() != device or device < 0:
+            if isinstance(t, torch.Tensor) and t.is_cuda and device >= 0:
+                raise ValueError(f"{name} is on {t.device}, other tensors are on cuda:{device}")
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dtype is not None and t.dtype is not dtype:
+            raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _call(device: int, fn: str, args, stream) -> None:
+    """Calls library function ``fn`` with the tensors' device current and, by
+    default, on that device's current stream."""
+    if device != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return _call(device, fn, args, stream)
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    status = getattr(_lib.lib(), fn)(*args, raw)
+    if status:
+        _lib.check(status)
+
+
+def _head_rows(t: torch.Tensor, name: str, device: int):
     """Pointer and token stride of a [tokens, heads, head_dim] tensor whose
     tokens may lie apart (a slice of a projection's output)."""
-    ptr = _dev(t, name, torch.bfloat16, contiguous=False)
-    n, h, d = t.shape
-    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+    if t.get_device() != device or t.dtype is not torch.bfloat16:
+        _pointers(device, (t, name, torch.bfloat16))  # raises
+    (n, h, d), (s0, s1, s2) = t.shape, t.stride()
+    if t.numel() and ((d > 1 and s2 != 1) or (h > 1 and s1 != d)):
         raise ValueError(f"{name}: a token's heads and channels must be contiguous")
-    return ptr, (t.stride(0) if n > 1 else h * d)
+    return t.data_ptr(), (s0 if n > 1 else h * d)
 
 
 def rope_and_cache(q_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
@@ -367,50 +402,51 @@ def rope_and_cache(q_out, query, key, value, k_cache, v_cache, slot_mapping, pos
     [axes, N] int32; ``cos_sin``: [max_position, rot_dim] fp32, cosines then
     sines; ``sections``: pairs turned by each axis."""
     _same_cache(k_cache, v_cache)
-    desc = cache_desc(k_cache)
-    ks, vs = _scales(desc, k_scale, v_scale)
-    n = int(slot_mapping.numel())
+    desc = _desc_cached(k_cache)
+    if (k_scale is None or v_scale is None) if desc.dtype else (k_scale is not None or v_scale is not None):
+        _scales(desc, k_scale, v_scale)  # raises
+    n = slot_mapping.numel()
     want = (n, desc.num_kv_heads, desc.head_dim)
-    if tuple(key.shape) != want or tuple(value.shape) != want:
+    if key.shape != want or value.shape != want:
         raise ValueError(f"key and value must be {list(want)} (one row per slot), "
                          f"got {list(key.shape)} and {list(value.shape)}")
-    if query.dim() != 3 or query.shape[0] != n or query.shape[2] != desc.head_dim \
-            or q_out.shape != query.shape:
+    q_shape = query.shape
+    if len(q_shape) != 3 or q_shape[0] != n or q_shape[2] != want[2] or q_out.shape != q_shape:
         raise ValueError(f"query and q_out must be [{n}, num_heads, {desc.head_dim}], "
                          f"got {list(query.shape)} and {list(q_out.shape)}")
-    axes = 1 if positions.dim() == 1 else int(positions.shape[0])
-    if positions.dim() not in (1, 2) or positions.shape[-1] != n:
+    p_shape = positions.shape
+    if len(p_shape) not in (1, 2) or p_shape[-1] != n:
         raise ValueError(f"positions must be [{n}] or [axes, {n}], got {list(positions.shape)}")
+    axes = 1 if len(p_shape) == 1 else p_shape[0]
     if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_position, rot_dim]")
     max_position, rot_dim = cos_sin.shape
-    sections = [rot_dim // 2] if sections is None and axes == 1 else list(sections or ())
+    sections = (rot_dim // 2,) if sections is None and axes == 1 else tuple(sections or ())
     if len(sections) != axes:
         raise ValueError(f"sections must have one entry for each of the {axes} position axes")
     if axes > 4:
         raise ValueError("at most 4 position axes")
-    rope = RopeDesc(int(rot_dim), int(max_position), axes,
-                    (ctypes.c_int32 * 4)(*(int(x) for x in sections)), int(sections_in_turn),
+    rope = _rope_of(rot_dim, max_position, axes, sections, int(sections_in_turn),
                     int(adjacent_pairs))
-    (qp, q_stride), (kp, k_stride), (vp, v_stride) = (
-        _head_rows(query, "query"), _head_rows(key, "key"), _head_rows(value, "value"))
-    args = (_dev(q_out, "q_out", torch.bfloat16), qp, q_stride, int(query.shape[1]), kp, k_stride,
-            vp, v_stride, _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), desc,
-            _dev(slot_mapping, "slot_mapping", torch.int32),
-            _dev(positions, "positions", torch.int32), _dev(cos_sin, "cos_sin", torch.float32),
-            rope, n, ks, vs)
-    with _on_device(q_out=q_out, query=query, key=key, value=value, k_cache=k_cache,
-                    v_cache=v_cache, slot_mapping=slot_mapping, positions=positions,
-                    cos_sin=cos_sin, k_scale=k_scale, v_scale=v_scale):
-        _lib.check(_lib.lib().pa_rope_and_cache(*args, _stream(stream)))
+    device = k_cache.get_device()
+    qp, q_stride = _head_rows(query, "query", device)
+    kp, k_stride = _head_rows(key, "key", device)
+    vp, v_stride = _head_rows(value, "value", device)
+    o, kc, vc, slots, pos, table, ks, vs = _pointers(
+        device, (q_out, "q_out", torch.bfloat16), (k_cache, "k_cache", None),
+        (v_cache, "v_cache", None), (slot_mapping, "slot_mapping", torch.int32),
+        (positions, "positions", torch.int32), (cos_sin, "cos_sin", torch.float32),
+        (k_scale, "k_scale", torch.float32), (v_scale, "v_scale", torch.float32))
+    _call(device, "pa_rope_and_cache", (o, qp, q_stride, q_shape[1], kp, k_stride, vp, v_stride, kc,
+                                        vc, desc, slots, pos, table, rope, n, ks, vs), stream)
 
 
 def _check_ranges(desc, codes, scales):
-    if tuple(codes.shape) != (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim):
+    if codes.shape != (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim):
         raise ValueError(f"codes must be [num_blocks, num_kv_heads, 2, head_dim] = "
                          f"{[desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim]}, "
                          f"got {list(codes.shape)}")
-    if tuple(scales.shape) != (desc.num_blocks, desc.num_kv_heads):
+    if scales.shape != codes.shape[:2]:
         raise ValueError(f"scales must be [num_blocks, num_kv_heads] = "
                          f"{[desc.num_blocks, desc.num_kv_heads]}, got {list(scales.shape)}")
 
@@ -428,31 +464,34 @@ def alloc_block_ranges(k_cache):
 def summarize_blocks(k_cache, slot_mapping, codes, scales, stream=None) -> None:
     """Keys' range per channel, in 8 bits, of every block whose last slot is
     in ``slot_mapping`` (the step's writes, already done on the stream)."""
-    desc = cache_desc(k_cache)
+    desc = _desc_cached(k_cache)
     _check_ranges(desc, codes, scales)
-    args = (_dev(k_cache, "k_cache"), desc, _dev(slot_mapping, "slot_mapping", torch.int32),
-            int(slot_mapping.numel()), _dev(codes, "codes", torch.int8),
-            _dev(scales, "scales", torch.float32))
-    with _on_device(k_cache=k_cache, slot_mapping=slot_mapping, codes=codes, scales=scales):
-        _lib.check(_lib.lib().pa_summarize_blocks(*args, _stream(stream)))
+    device = k_cache.get_device()
+    kc, slots, c, s = _pointers(
+        device, (k_cache, "k_cache", None), (slot_mapping, "slot_mapping", torch.int32),
+        (codes, "codes", torch.int8), (scales, "scales", torch.float32))
+    _call(device, "pa_summarize_blocks", (kc, desc, slots, slot_mapping.numel(), c, s), stream)
 
 
-def _check_rows(q, block_tables, context_lens, row_seqs, selected, num_kv_heads):
-    """Sizes shared by the calls over query rows; (rows, sequences)."""
+def _check_rows(q, block_tables, context_lens, row_seqs, selected, num_kv_heads, head_dim):
+    """Sizes shared by the calls over query rows; (rows, heads, sequences, top)."""
     if q.dim() != 3:
         raise ValueError("q must be [num_rows, num_heads, head_dim]")
-    rows = int(q.shape[0])
-    if block_tables.dim() != 2 or (row_seqs is None and block_tables.shape[0] != rows):
+    rows, heads, d = q.shape
+    t_shape, s_shape = block_tables.shape, selected.shape
+    if len(t_shape) != 2 or (row_seqs is None and t_shape[0] != rows):
         raise ValueError(f"block_tables must be [{'num_seqs' if row_seqs is not None else rows}, "
                          f"max_blocks_per_seq], got {list(block_tables.shape)}")
     if context_lens.numel() != rows:
         raise ValueError(f"context_lens needs {rows} entries, got {context_lens.numel()}")
     if row_seqs is not None and row_seqs.numel() != rows:
         raise ValueError(f"row_seqs needs {rows} entries, got {row_seqs.numel()}")
-    if selected.dim() != 3 or tuple(selected.shape[:2]) != (rows, num_kv_heads):
+    if len(s_shape) != 3 or s_shape[0] != rows or s_shape[1] != num_kv_heads:
         raise ValueError(f"selected must be [{rows}, {num_kv_heads}, top], "
                          f"got {list(selected.shape)}")
-    return rows, int(block_tables.shape[0])
+    if d != head_dim:
+        raise ValueError(f"q's head_dim {d} differs from the cache's {head_dim}")
+    return rows, heads, t_shape[0], t_shape[1], s_shape[2]
 
 
 def select_blocks(selected, q, codes, scales, block_tables, context_lens, block_size, sink=1,
@@ -464,20 +503,18 @@ def select_blocks(selected, q, codes, scales, block_tables, context_lens, block_
     if codes.dim() != 4 or codes.shape[2] != 2:
         raise ValueError("codes must be [num_blocks, num_kv_heads, 2, head_dim]")
     nb, hkv, _, d = codes.shape
-    desc = CacheDesc(int(nb), int(block_size), int(hkv), int(d), PA_KV_BF16)
+    desc = _desc_of(nb, int(block_size), hkv, d, PA_KV_BF16)
     _check_ranges(desc, codes, scales)
-    rows, seqs = _check_rows(q, block_tables, context_lens, row_seqs, selected, hkv)
-    if q.shape[2] != d:
-        raise ValueError(f"q's head_dim {q.shape[2]} differs from the codes' {d}")
-    args = (_dev(selected, "selected", torch.int32), _dev(q, "q", torch.bfloat16),
-            _dev(codes, "codes", torch.int8), _dev(scales, "scales", torch.float32), desc,
-            _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
-            _dev(context_lens, "context_lens", torch.int32),
-            None if row_seqs is None else _dev(row_seqs, "row_seqs", torch.int32), rows, seqs,
-            int(q.shape[1]), int(selected.shape[2]), int(sink), int(recent))
-    with _on_device(selected=selected, q=q, codes=codes, scales=scales,
-                    block_tables=block_tables, context_lens=context_lens, row_seqs=row_seqs):
-        _lib.check(_lib.lib().pa_select_blocks(*args, _stream(stream)))
+    rows, heads, seqs, max_blocks, top = _check_rows(q, block_tables, context_lens, row_seqs,
+                                                     selected, hkv, d)
+    device = codes.get_device()
+    sel, qp, c, s, bt, cl, rs = _pointers(
+        device, (selected, "selected", torch.int32), (q, "q", torch.bfloat16),
+        (codes, "codes", torch.int8), (scales, "scales", torch.float32),
+        (block_tables, "block_tables", torch.int32), (context_lens, "context_lens", torch.int32),
+        (row_seqs, "row_seqs", torch.int32))
+    _call(device, "pa_select_blocks", (sel, qp, c, s, desc, bt, max_blocks, cl, rs, rows, seqs,
+                                       heads, top, int(sink), int(recent)), stream)
     return selected
 
 
@@ -486,24 +523,22 @@ def decode_selected(out, q, k_cache, v_cache, block_tables, context_lens, select
     """``decode`` over the blocks listed in ``selected`` [num_rows, H_kv, top];
     writes ``out`` [num_rows, H_q, d] bf16 and returns it."""
     _same_cache(k_cache, v_cache)
-    desc = cache_desc(k_cache)
-    ks, vs = _scales(desc, k_scale, v_scale)
+    desc = _desc_cached(k_cache)
+    if (k_scale is None or v_scale is None) if desc.dtype else (k_scale is not None or v_scale is not None):
+        _scales(desc, k_scale, v_scale)  # raises
     if out.shape != q.shape:
         raise ValueError("q and out must both be [num_rows, num_heads, head_dim]")
-    rows, seqs = _check_rows(q, block_tables, context_lens, row_seqs, selected, desc.num_kv_heads)
-    if q.shape[2] != desc.head_dim:
-        raise ValueError(f"q's head_dim {q.shape[2]} differs from the cache's {desc.head_dim}")
-    args = (_dev(out, "out", torch.bfloat16), _dev(q, "q", torch.bfloat16),
-            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), desc,
-            _dev(block_tables, "block_tables", torch.int32), int(block_tables.shape[1]),
-            _dev(context_lens, "context_lens", torch.int32),
-            None if row_seqs is None else _dev(row_seqs, "row_seqs", torch.int32),
-            _dev(selected, "selected", torch.int32), rows, seqs, int(q.shape[1]),
-            int(selected.shape[2]), ctypes.c_float(scale), ks, vs)
-    with _on_device(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                    context_lens=context_lens, row_seqs=row_seqs, selected=selected,
-                    k_scale=k_scale, v_scale=v_scale):
-        _lib.check(_lib.lib().pa_decode_selected(*args, _stream(stream)))
+    rows, heads, seqs, max_blocks, top = _check_rows(
+        q, block_tables, context_lens, row_seqs, selected, desc.num_kv_heads, desc.head_dim)
+    device = k_cache.get_device()
+    o, qp, kc, vc, bt, cl, rs, sel, ks, vs = _pointers(
+        device, (out, "out", torch.bfloat16), (q, "q", torch.bfloat16), (k_cache, "k_cache", None),
+        (v_cache, "v_cache", None), (block_tables, "block_tables", torch.int32),
+        (context_lens, "context_lens", torch.int32), (row_seqs, "row_seqs", torch.int32),
+        (selected, "selected", torch.int32), (k_scale, "k_scale", torch.float32),
+        (v_scale, "v_scale", torch.float32))
+    _call(device, "pa_decode_selected", (o, qp, kc, vc, desc, bt, max_blocks, cl, rs, sel, rows,
+                                         seqs, heads, top, scale, ks, vs), stream)
     return out
 
 

@@ -113,7 +113,7 @@ def _row_args(kw):
 @pytest.mark.parametrize("kw,want", ROWS + [
     (dict(sink=-1), INVALID), (dict(recent=0), INVALID), (dict(sink=3, recent=2), INVALID),
     (dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1), INVALID),
-    (dict(max_blocks=262145), UNSUPPORTED),
+    (dict(max_blocks=196609), UNSUPPORTED),
 ])
 def test_select_blocks_refuses(kw, want):
     a = _row_args(kw)
