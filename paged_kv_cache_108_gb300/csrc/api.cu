@@ -944,7 +944,7 @@ pa_status pa_rope_and_cache(void* q_out, const void* query, int64_t q_stride, in
   p.in_turn = rope.sections_in_turn != 0;
   p.adjacent = rope.adjacent_pairs != 0;
   return cuda_status(pa::launch_rope_and_cache(p, cache.head_dim, cache.dtype == PA_KV_FP8_E4M3,
-                                               reinterpret_cast<cudaStream_t>(stream)),
+                                               num_sms(), reinterpret_cast<cudaStream_t>(stream)),
                      fn);
 }
 

@@ -58,7 +58,7 @@ struct Pair<true> {
 
 // Bound: the keys' bytes, read once.  The unit of work is a full block's
 // column of 32 consecutive 16-byte pieces (512 bytes of each token's row,
-// whole heads): a warp reads it with 16 loads in flight, and the extremes
+// whole heads): a warp reads it with 8 loads in flight, and the extremes
 // stay packed in the cache's own precision, where they are exact.  A CTA
 // looks at up to 32 consecutive tokens of the step and takes the blocks
 // whose last slot is among them.  kSplit = 1: each warp takes a column of
@@ -66,12 +66,12 @@ struct Pair<true> {
 // and more, where one warp's walk would be the call's time): all 8 warps of
 // the CTA share a column's tokens and their results meet in shared memory.
 template <int D, bool FP8, int kSplit>
-__global__ void __launch_bounds__(32 * kSumWarps, 2)
+__global__ void __launch_bounds__(32 * kSumWarps, FP8 ? 2 : 4)
     summarize_kernel(const __grid_constant__ SummaryParams p, int tokens_per_cta) {
   using P2 = typename Pair<FP8>::T;
   constexpr int kPieces = D * (FP8 ? 1 : 2) / 16;  // 16-byte pieces per head
   constexpr int kPairs = FP8 ? 8 : 4;              // channel pairs per piece
-  constexpr int kLoads = FP8 ? 8 : 16;             // in flight per lane
+  constexpr int kLoads = 8;                        // in flight per lane
   __shared__ P2 s_hi[kSplit > 1 ? kSplit : 1][kPairs][32];
   __shared__ P2 s_lo[kSplit > 1 ? kSplit : 1][kPairs][32];
   ptx::grid_dependency_wait();

@@ -29,7 +29,6 @@
 // second kernel, and sums in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cstdlib>
 
 #include "launch.cuh"
 #include "pa_device.cuh"
@@ -40,7 +39,8 @@ namespace pa {
 
 namespace {
 
-constexpr int kChunk = 32;  // tokens a warp handles at a time: two 16-row MMA tiles
+constexpr int kChunk = 16;      // tokens a warp handles at a time
+constexpr int kMaxCluster = 8;  // CTAs that share a (row, KV head)
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
@@ -125,9 +125,13 @@ struct Cfg {
   static constexpr int kRow = D * (FP8 ? 1 : 2);  // bytes of a token's channels
   static constexpr int kPieces = kRow / 16;
   static constexpr int kTile = kChunk * kRow;  // K (or V) bytes of a chunk
-  static constexpr int kWarps = FP8 ? 4 : 2;
+  // A warp's stage is 8 KB of bf16 or 4 KB of e4m3 (D = 128), and e4m3 has
+  // twice the instructions a byte, so twice the warps to hide them behind
+  // (8 rows of 8192 tokens: 34.8 us with 4 warps of 3 stages, 28.5 with 8 of
+  // 2; 64 rows of 1024 tokens in bf16: 46.4 with 4 of 3, 56.8 with 8 of 2).
+  static constexpr int kWarps = FP8 ? 8 : 4;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kStages = 2;
+  static constexpr int kStages = FP8 ? 2 : 3;
   static constexpr int kRing = kWarps * kStages * 2 * kTile;
   static constexpr int kMerge = kWarps * 8 * (D + 2) * 4;  // reuses the ring
   static_assert(kMerge <= kRing, "the merge reuses the ring");
@@ -251,39 +255,23 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads)
   const uint8_t* vbase = static_cast<const uint8_t*>(p.v_cache) + (int64_t)kvh * C::kRow;
   const int my = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;  // this warp's chunks
 
-  // The listed tokens from slot s0 (in list order) on, 16 of them: the first
-  // one's slot in the cache and how many hold a token.  Blocks of 16 and more
-  // hold such a run whole.
-  auto run_of = [&](int s0) {
-    const int e = (s0 >> lb) - e0, off = s0 & (block - 1);
-    const int2 en = e < e1 - e0 ? s_entry[e] : make_int2(0, 0);
-    return make_int2(en.x + off, en.y - off);
-  };
   auto load = [&](int it) {
     if (it < my) {
       const int s0 = slot0 + (warp + it * kWarps) * kChunk;
       const uint32_t stage = ring + (it % C::kStages) * 2 * C::kTile;
       constexpr int kRowsPer = 32 / C::kPieces;  // tokens per instruction
-      const int piece = lane % C::kPieces, sub = lane / C::kPieces;
+      const int piece = lane % C::kPieces;
 #pragma unroll
-      for (int h = 0; h < kChunk; h += 16) {
-        int2 run = make_int2(0, 0);
-        if (lb >= 4) run = run_of(s0 + h);
-#pragma unroll
-        for (int r = 0; r < 16; r += kRowsPer) {
-          const int t = r + sub;
-          int slot = run.x + t;
-          bool in = t < run.y;
-          if (lb < 4) {
-            const int2 one = run_of(s0 + h + t);
-            slot = one.x;
-            in = one.y > 0;
-          }
-          const int64_t at = (int64_t)(in ? slot : 0) * stride + piece * 16;
-          const uint32_t dst = stage + (h + t) * C::kRow + C::swizzle(t, piece) * 16;
-          cp_async_16(dst, kbase + at, in ? 16 : 0);  // zeros where there is no token
-          cp_async_16(dst + C::kTile, vbase + at, in ? 16 : 0);
-        }
+      for (int r = 0; r < kChunk / kRowsPer; ++r) {
+        const int t = r * kRowsPer + lane / C::kPieces;
+        const int e = ((s0 + t) >> lb) - e0, off = (s0 + t) & (block - 1);
+        int2 en = make_int2(0, 0);
+        if (e < e1 - e0) en = s_entry[e];
+        const bool in = off < en.y;
+        const int64_t at = (int64_t)(in ? en.x + off : 0) * stride + piece * 16;
+        const uint32_t dst = stage + t * C::kRow + C::swizzle(t, piece) * 16;
+        cp_async_16(dst, kbase + at, in ? 16 : 0);  // zeros where there is no token
+        cp_async_16(dst + C::kTile, vbase + at, in ? 16 : 0);
       }
     }
     cp_async_commit();
@@ -302,47 +290,44 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads)
     __syncwarp();
     const uint32_t kt = ring + (it % C::kStages) * 2 * C::kTile;
     const uint32_t vt = kt + C::kTile;
-    // S^T of the two tiles: accumulator rows g and g + 8, columns 2c, 2c + 1
-    float s[2][4] = {};
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
     {
       const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+      const uint32_t base = kt + r * C::kRow;
+      if constexpr (FP8) {
 #pragma unroll
-      for (int k = 0; k < kSteps; k += FP8 ? 2 : 1) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int k = 0; k < kSteps; k += 2) {
           uint32_t w[4];
-          const int piece = (FP8 ? k : 2 * k) + (lane >> 4);
-          ldmatrix_x4(w, kt + (16 * h + r) * C::kRow + C::swizzle(r, piece) * 16);
-          if constexpr (FP8) {
+          ldmatrix_x4(w, base + C::swizzle(r, k + (lane >> 4)) * 16);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {  // the two 16-channel pieces
-              const uint32_t x = w[2 * i], y = w[2 * i + 1];
-              const uint32_t a[4] = {widen((uint16_t)x), widen((uint16_t)y),
-                                     widen((uint16_t)(x >> 16)), widen((uint16_t)(y >> 16))};
-              mma16816<true>(s[h], a, qb[k + i][0], qb[k + i][1]);
-            }
-          } else {
-            mma16816<false>(s[h], w, qb[k][0], qb[k][1]);
+          for (int h = 0; h < 2; ++h) {  // the two 16-channel pieces
+            const uint32_t x = w[2 * h], y = w[2 * h + 1];
+            const uint32_t a[4] = {widen((uint16_t)x), widen((uint16_t)y),
+                                   widen((uint16_t)(x >> 16)), widen((uint16_t)(y >> 16))};
+            mma16816<true>(s, a, qb[k + h][0], qb[k + h][1]);
           }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          uint32_t a[4];
+          ldmatrix_x4(a, base + C::swizzle(r, 2 * k + (lane >> 4)) * 16);
+          mma16816<false>(s, a, qb[k][0], qb[k][1]);
         }
       }
     }
+    // tokens g and g + 8 of the chunk, columns 2c and 2c + 1
     const int s0 = slot0 + (warp + it * kWarps) * kChunk;
-    float n0 = -INFINITY, n1 = -INFINITY;
+    bool in[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      int2 run = make_int2(0, 0);
-      if (lb >= 4) run = run_of(s0 + 16 * h);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = g + 8 * i;
-        const bool in = lb >= 4 ? t < run.y : run_of(s0 + 16 * h + t).y > 0;
-        s[h][2 * i] = in ? s[h][2 * i] * f0 : -INFINITY;
-        s[h][2 * i + 1] = in ? s[h][2 * i + 1] * f1 : -INFINITY;
-        n0 = fmaxf(n0, s[h][2 * i]);
-        n1 = fmaxf(n1, s[h][2 * i + 1]);
-      }
+      const int sl = s0 + g + 8 * h;
+      const int e = (sl >> lb) - e0;
+      in[h] = e < e1 - e0 && (sl & (block - 1)) < s_entry[e].y;
     }
+    const float x00 = in[0] ? s[0] * f0 : -INFINITY, x01 = in[0] ? s[1] * f1 : -INFINITY;
+    const float x10 = in[1] ? s[2] * f0 : -INFINITY, x11 = in[1] ? s[3] * f1 : -INFINITY;
+    float n0 = fmaxf(x00, x10), n1 = fmaxf(x01, x11);
 #pragma unroll
     for (int d = 4; d < 32; d *= 2) {
       n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
@@ -366,52 +351,50 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads)
       m1 = n1;
     }
     const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-    // P as MMA operand B of each tile: [h][tokens 0..7, 8..15]
-    uint32_t b[2][2], rest[2][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float p0 = fast_exp2(s[h][2 * i] - z0), p1 = fast_exp2(s[h][2 * i + 1] - z1);
-        l0 += p0;
-        l1 += p1;
-        uint32_t hi = pack2<FP8>(p0, p1);
-        const float2 r = unpack2<FP8>(hi);
-        const uint32_t lo = pack2<FP8>(p0 - r.x, p1 - r.y);
-        if (G <= 4 && c >= 2) hi = lo;  // columns 4..7 carry the remainders
-        b[h][i] = movmatrix_trans(hi);
-        if (G > 4) rest[h][i] = movmatrix_trans(lo);
+    const float p00 = fast_exp2(x00 - z0), p01 = fast_exp2(x01 - z1);
+    const float p10 = fast_exp2(x10 - z0), p11 = fast_exp2(x11 - z1);
+    l0 += p00 + p10;
+    l1 += p01 + p11;
+    uint32_t hi0 = pack2<FP8>(p00, p01), hi1 = pack2<FP8>(p10, p11);
+    const float2 r0 = unpack2<FP8>(hi0), r1 = unpack2<FP8>(hi1);
+    uint32_t lo0 = pack2<FP8>(p00 - r0.x, p01 - r0.y), lo1 = pack2<FP8>(p10 - r1.x, p11 - r1.y);
+    if constexpr (G <= 4) {  // columns 4..7 carry the remainders
+      if (c >= 2) {
+        hi0 = lo0;
+        hi1 = lo1;
       }
+    }
+    const uint32_t b0 = movmatrix_trans(hi0), b1 = movmatrix_trans(hi1);
+    uint32_t d0 = 0, d1 = 0;
+    if constexpr (G > 4) {
+      d0 = movmatrix_trans(lo0);
+      d1 = movmatrix_trans(lo1);
+    }
+    if constexpr (FP8) {
+      // a transposed 16-bit unit holds channels 2g and 2g + 1 of a token: the
+      // even ones become row g of the tile, the odd ones row g + 8
+      const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (FP8) {
-        // a transposed 16-bit unit holds channels 2g and 2g + 1 of a token: the
-        // even ones become row g of the tile, the odd ones row g + 8
-        const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+      for (int k = 0; k < kSteps; k += 2) {
+        uint32_t w[4];
+        ldmatrix_x4_trans(w, vt + r * C::kRow + C::swizzle(r, k + (lane >> 4)) * 16);
 #pragma unroll
-        for (int k = 0; k < kSteps; k += 2) {
-          uint32_t w[4];
-          ldmatrix_x4_trans(w, vt + (16 * h + r) * C::kRow + C::swizzle(r, k + (lane >> 4)) * 16);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t x = __byte_perm(w[2 * i], 0, 0x3120);
-            const uint32_t y = __byte_perm(w[2 * i + 1], 0, 0x3120);
-            const uint32_t a[4] = {widen((uint16_t)x), widen((uint16_t)(x >> 16)),
-                                   widen((uint16_t)y), widen((uint16_t)(y >> 16))};
-            mma16816<true>(o[k + i], a, b[h][0], b[h][1]);
-            if constexpr (G > 4) mma16816<true>(o[k + i], a, rest[h][0], rest[h][1]);
-          }
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = __byte_perm(w[2 * h], 0, 0x3120), y = __byte_perm(w[2 * h + 1], 0, 0x3120);
+          const uint32_t a[4] = {widen((uint16_t)x), widen((uint16_t)(x >> 16)),
+                                 widen((uint16_t)y), widen((uint16_t)(y >> 16))};
+          mma16816<true>(o[k + h], a, b0, b1);
+          if constexpr (G > 4) mma16816<true>(o[k + h], a, d0, d1);
         }
-      } else {
-        const int r = (lane & 7) + (lane >> 4) * 8;
+      }
+    } else {
+      const int r = (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t a[4];
-          ldmatrix_x4_trans(a, vt + (16 * h + r) * C::kRow +
-                                   C::swizzle(r, 2 * k + ((lane >> 3) & 1)) * 16);
-          mma16816<false>(o[k], a, b[h][0], b[h][1]);
-          if constexpr (G > 4) mma16816<false>(o[k], a, rest[h][0], rest[h][1]);
-        }
+      for (int k = 0; k < kSteps; ++k) {
+        uint32_t a[4];
+        ldmatrix_x4_trans(a, vt + r * C::kRow + C::swizzle(r, 2 * k + ((lane >> 3) & 1)) * 16);
+        mma16816<false>(o[k], a, b0, b1);
+        if constexpr (G > 4) mma16816<false>(o[k], a, d0, d1);
       }
     }
     __syncwarp();  // the stage may be filled again
@@ -492,14 +475,17 @@ cudaError_t launch_one(const SelectedParams& p, int num_sms, cudaStream_t stream
   using C = Cfg<D, FP8>;
   const int64_t units = (int64_t)p.num_rows * p.num_kv_heads;
   const int64_t tokens = (int64_t)p.top << p.log2_block_size;  // of a unit, at most
-  int c = 1;
-  while (c < 8 && units * c < 2 * num_sms && tokens / (2 * c) >= 128) c *= 2;
-  if (getenv("PA_C")) c = atoi(getenv("PA_C"));  // XXX sweep
+  // CTAs per unit: as many as run at two to an SM, while each has a chunk for
+  // every warp (8 rows of 8 heads, 8192 tokens each in e4m3: 55.6 us with 1,
+  // 32.9 with 2, 28.5 with 4, and 41.5 with 5, which no longer run at once)
+  int64_t c = 2 * num_sms / units;
+  if (c > tokens / (kChunk * C::kWarps)) c = tokens / (kChunk * C::kWarps);
+  c = c < 1 ? 1 : (c > kMaxCluster ? kMaxCluster : c);
   const size_t smem = C::kRing + (size_t)p.top * sizeof(int2);
   const cudaError_t e = allow_large<decode_selected_kernel<D, G, FP8>>();
   if (e != cudaSuccess) return e;
   return launch_dependent<decode_selected_kernel<D, G, FP8>>(
-      dim3((unsigned)(units * c)), dim3(C::kThreads), smem, stream, c, p, c);
+      dim3((unsigned)(units * c)), dim3(C::kThreads), smem, stream, (int)c, p, (int)c);
 }
 
 template <int D, bool FP8>

@@ -159,9 +159,11 @@ struct RopeParams {
   int32_t num_heads, num_kv_heads;
   int32_t rot_dim, max_position;
   int32_t num_axes, sections[4], in_turn, adjacent;
-  int32_t tokens_per_cta;  // set by the launch
+  int32_t tokens_per_cta;  // these two are set by the launch
+  uint32_t heads_inverse;
 };
-cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, cudaStream_t stream);
+cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, int num_sms,
+                                  cudaStream_t stream);
 
 // Key ranges of full blocks and block selection (block_select.cu).
 struct SummaryParams {

@@ -28,7 +28,8 @@ namespace pa {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeUnroll = 4;     // work items in flight per thread
+constexpr int kRopeCtas = 8;       // per SM: what the registers are kept to
+constexpr int kRopeUnroll = 3;     // items in flight per thread
 constexpr int kRopeMaxTokens = 8;  // tokens per CTA at most
 
 // The position axis of pair i: one axis, sections in a row, or axes in turn
@@ -68,11 +69,18 @@ __device__ __forceinline__ void store_piece(void* cache, int64_t elem, const flo
   }
 }
 
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float u = x * c - y * s;
+  y = y * c + x * s;
+  x = u;
+}
+
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kCols = D / 16;  // items (two 8-element pieces) per head
-  __shared__ float2 s_cs[kRopeMaxTokens][D / 2];
+  constexpr int kRows = kRopeThreads / kCols;  // heads the CTA takes at a time
+  __shared__ __align__(16) float2 s_cs[kRopeMaxTokens][D / 2];
   __shared__ int s_slot[kRopeMaxTokens];
   __shared__ int s_ok[kRopeMaxTokens];
   ptx::grid_dependency_wait();
@@ -81,46 +89,35 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int64_t tok0 = (int64_t)blockIdx.x * p.tokens_per_cta;
   const int ntok = (int)min((int64_t)p.tokens_per_cta, p.num_tokens - tok0);
   const int half = p.rot_dim / 2;
-  const int rot_cols = p.rot_dim / 16;
-  const int heads = p.num_heads + 2 * p.num_kv_heads;
-  const int per_token = heads * kCols;
-  const int items = ntok * per_token;
+  const int kv0 = p.num_heads, v0 = kv0 + p.num_kv_heads, heads = v0 + p.num_kv_heads;
+  // a thread's two pieces start at the same channels in every head: column c
+  // and its partner half the rotated width on, or two neighbours where pairs
+  // are adjacent and where nothing is rotated
+  const int c = tid % kCols;
+  const bool turned = c < p.rot_dim / 16;
+  const bool split = turned && !p.adjacent;
+  const int e0 = split ? 8 * c : 16 * c, e1 = split ? half + 8 * c : 16 * c + 8;
+  const int first = tid / kCols, rows = ntok * heads;
   float ks = 1.f, vs = 1.f;
   if (FP8) {
     ks = *p.k_scale;
     vs = *p.v_scale;
   }
-  bool staged = false;
-  for (int base = 0; base < items; base += kRopeThreads * kRopeUnroll) {
+  for (int base = 0; base < rows; base += kRows * kRopeUnroll) {
     uint4 a[kRopeUnroll], b[kRopeUnroll];
-    int tl[kRopeUnroll], hd[kRopeUnroll], e0[kRopeUnroll], e1[kRopeUnroll], col[kRopeUnroll];
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
-      const int it = base + u * kRopeThreads + tid;
-      tl[u] = -1;
-      if (it >= items) continue;
-      const int t = it / per_token, r = it - t * per_token;
-      const int h = r / kCols, c = r % kCols;
-      tl[u] = t;
-      hd[u] = h;
-      col[u] = c;
-      // the pieces' first elements: c and its partner half the rotated width
-      // on; neighbours for adjacent pairs and for channels left unrotated
-      const bool split = !p.adjacent && c < rot_cols;
-      e0[u] = split ? 8 * c : 16 * c;
-      e1[u] = split ? half + 8 * c : 16 * c + 8;
-      const __nv_bfloat16* row;
-      if (h < p.num_heads)
-        row = p.query + (tok0 + t) * p.q_stride + h * D;
-      else if (h < p.num_heads + p.num_kv_heads)
-        row = p.key + (tok0 + t) * p.k_stride + (h - p.num_heads) * D;
-      else
-        row = p.value + (tok0 + t) * p.v_stride + (h - p.num_heads - p.num_kv_heads) * D;
-      a[u] = *reinterpret_cast<const uint4*>(row + e0[u]);
-      b[u] = *reinterpret_cast<const uint4*>(row + e1[u]);
+      const int r = base + u * kRows + first;
+      if (r >= rows) continue;
+      const int t = (int)__umulhi((unsigned)r, p.heads_inverse), h = r - t * heads;
+      const __nv_bfloat16* row =
+          h < kv0 ? p.query + (tok0 + t) * p.q_stride + h * D
+                  : (h < v0 ? p.key + (tok0 + t) * p.k_stride + (h - kv0) * D
+                            : p.value + (tok0 + t) * p.v_stride + (h - v0) * D);
+      a[u] = *reinterpret_cast<const uint4*>(row + e0);
+      b[u] = *reinterpret_cast<const uint4*>(row + e1);
     }
-    if (!staged) {  // the same for every thread of the CTA
-      staged = true;
+    if (base == 0) {
       if (tid < ntok) {
         const int64_t tok = tok0 + tid;
         s_slot[tid] = p.slot_mapping[tok];
@@ -130,7 +127,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         s_ok[tid] = ok;
       }
       for (int i = tid; i < ntok * half; i += kRopeThreads) {
-        const int t = i / half, pair = i - t * half;
+        const int t = ntok == 1 ? 0 : i / half, pair = i - t * half;
         const int pos = p.positions[axis_of_pair(p, pair) * p.num_tokens + tok0 + t];
         float2 cs = make_float2(1.f, 0.f);
         if ((unsigned)pos < (unsigned)p.max_position) {
@@ -143,48 +140,46 @@ __global__ void __launch_bounds__(kRopeThreads)
     }
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
-      if (tl[u] < 0 || !s_ok[tl[u]]) continue;
-      const int64_t tok = tok0 + tl[u];
-      const bool is_q = hd[u] < p.num_heads;
-      const bool is_v = hd[u] >= p.num_heads + p.num_kv_heads;
+      const int r = base + u * kRows + first;
+      if (r >= rows) continue;
+      const int t = (int)__umulhi((unsigned)r, p.heads_inverse), h = r - t * heads;
+      if (!s_ok[t]) continue;
       float x[8], y[8];
       Unpack16<false>::run(a[u], x);
       Unpack16<false>::run(b[u], y);
-      if (!is_v && col[u] < rot_cols) {
-        const float2* cs = &s_cs[tl[u]][8 * col[u]];
+      if (h < v0 && turned) {
+        const float4* cs = reinterpret_cast<const float4*>(&s_cs[t][8 * c]);
         if (p.adjacent) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 c0 = cs[i], c1 = cs[4 + i];
-            const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
-            x[2 * i] = x0 * c0.x - x1 * c0.y;
-            x[2 * i + 1] = x1 * c0.x + x0 * c0.y;
-            y[2 * i] = y0 * c1.x - y1 * c1.y;
-            y[2 * i + 1] = y1 * c1.x + y0 * c1.y;
+          for (int i = 0; i < 2; ++i) {
+            const float4 m = cs[i], n = cs[2 + i];
+            turn(x[4 * i], x[4 * i + 1], m.x, m.y);
+            turn(x[4 * i + 2], x[4 * i + 3], m.z, m.w);
+            turn(y[4 * i], y[4 * i + 1], n.x, n.y);
+            turn(y[4 * i + 2], y[4 * i + 3], n.z, n.w);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 c = cs[i];
-            const float xi = x[i], yi = y[i];
-            x[i] = xi * c.x - yi * c.y;
-            y[i] = yi * c.x + xi * c.y;
+          for (int i = 0; i < 4; ++i) {
+            const float4 m = cs[i];
+            turn(x[2 * i], y[2 * i], m.x, m.y);
+            turn(x[2 * i + 1], y[2 * i + 1], m.z, m.w);
           }
         }
       }
-      if (is_q) {
-        const int64_t row = (tok * p.num_heads + hd[u]) * D;
-        store_piece(p.q_out, row + e0[u], x, false, 1.f);
-        store_piece(p.q_out, row + e1[u], y, false, 1.f);
+      if (h < kv0) {
+        const int64_t row = ((tok0 + t) * kv0 + h) * D;
+        store_piece(p.q_out, row + e0, x, false, 1.f);
+        store_piece(p.q_out, row + e1, y, false, 1.f);
       } else {
-        const int slot = s_slot[tl[u]];
+        const int slot = s_slot[t];
         if (slot < 0 || slot >= p.num_slots) continue;  // padding token or bad slot
-        const int h = hd[u] - p.num_heads - (is_v ? p.num_kv_heads : 0);
-        const int64_t row = ((int64_t)slot * p.num_kv_heads + h) * D;
+        const bool is_v = h >= v0;
+        const int64_t row = ((int64_t)slot * p.num_kv_heads + h - (is_v ? v0 : kv0)) * D;
         void* cache = is_v ? p.v_cache : p.k_cache;
         const float scale = is_v ? vs : ks;
-        store_piece(cache, row + e0[u], x, FP8, scale);
-        store_piece(cache, row + e1[u], y, FP8, scale);
+        store_piece(cache, row + e0, x, FP8, scale);
+        store_piece(cache, row + e1, y, FP8, scale);
       }
     }
   }
@@ -192,11 +187,22 @@ __global__ void __launch_bounds__(kRopeThreads)
 
 }  // namespace
 
-cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, cudaStream_t stream) {
+cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, int num_sms,
+                                  cudaStream_t stream) {
   // tokens per CTA: enough items for every thread's loads in flight
-  const int64_t per_token = (int64_t)(p.num_heads + 2 * p.num_kv_heads) * (head_dim / 16);
+  const int heads = p.num_heads + 2 * p.num_kv_heads;
+  const int64_t per_token = (int64_t)heads * (head_dim / 16);
   int64_t t = kRopeThreads * kRopeUnroll / per_token;
   t = t < 1 ? 1 : (t > kRopeMaxTokens ? kRopeMaxTokens : t);
+  // A long call's CTAs take two tokens at least: the wait for positions, then
+  // table rows, then the barrier is paid once for both (8192 tokens of 48
+  // heads: 49.1 us with one, 40.2 with two, 40.5 with four).  A short call is
+  // spread over the SMs instead.
+  if (p.num_tokens >= 2 * kRopeCtas * num_sms && t < 2) t = 2;
+  const int64_t spread = p.num_tokens / (2 * num_sms);
+  if (t > spread) t = spread < 1 ? 1 : spread;
+  // ceil(2^32 / heads): r / heads is the high half of r * it for r < 8 * heads <= 2^20
+  p.heads_inverse = (uint32_t)((((uint64_t)1 << 32) + heads - 1) / heads);
   p.tokens_per_cta = (int)t;
   const int64_t grid = (p.num_tokens + t - 1) / t;
   const dim3 g((unsigned)grid), b(kRopeThreads);
