@@ -538,7 +538,8 @@ typedef struct {
  *                q_stride / k_stride / v_stride elements after token t - 1's
  *                (multiples of 8, at least heads * head_dim; slices of one
  *                projection's output qualify).  16-byte aligned.
- *  num_heads     query heads; any number from 0 (then q_out, query: NULL).
+ *  num_heads     query heads, from 0 (then q_out, query: NULL) up to
+ *                num_heads + 2 num_kv_heads = 32768.
  *  slot_mapping  device, [num_tokens] int32; a negative or out-of-range slot
  *                skips the cache write (padding), q_out is still written.
  *                No slot may appear twice.
@@ -577,7 +578,7 @@ pa_status pa_rope_and_cache(void* q_out, const void* query, int64_t q_stride, in
  *  codes         device, [num_blocks, num_kv_heads, 2, head_dim] int8,
  *                16-byte aligned.
  *  scales        device, [num_blocks, num_kv_heads] fp32.
- *  num_tokens == 0 is valid and launches nothing.
+ *  Up to 32768 KV heads.  num_tokens == 0 is valid and launches nothing.
  * ---------------------------------------------------------------------- */
 pa_status pa_summarize_blocks(const void* k_cache, pa_cache_desc cache,
                               const int32_t* slot_mapping, int32_t num_tokens, int8_t* codes,

@@ -895,8 +895,8 @@ pa_status pa_rope_and_cache(void* q_out, const void* query, int64_t q_stride, in
   }
   const int64_t q_row = (int64_t)num_heads * cache.head_dim;
   const int64_t kv_row = (int64_t)cache.num_kv_heads * cache.head_dim;
-  if (q_row + 2 * kv_row > (1 << 24))
-    return pa_fail(PA_ERR_UNSUPPORTED, "pa_rope_and_cache: too many heads");
+  if ((int64_t)num_heads + 2 * (int64_t)cache.num_kv_heads > 32768)
+    return pa_fail(PA_ERR_UNSUPPORTED, "pa_rope_and_cache: more than 32768 heads in all");
   if ((num_heads && (q_stride < q_row || q_stride % 8)) || k_stride < kv_row || k_stride % 8 ||
       v_stride < kv_row || v_stride % 8)
     return pa_fail(PA_ERR_INVALID,
@@ -955,8 +955,8 @@ pa_status pa_summarize_blocks(const void* k_cache, pa_cache_desc cache,
   pa_status st = check_cache(cache, fn);
   if (st != PA_OK) return st;
   if (num_tokens < 0) return pa_fail(PA_ERR_INVALID, "pa_summarize_blocks: num_tokens < 0");
-  if ((int64_t)cache.num_kv_heads * cache.head_dim > (1 << 24))
-    return pa_fail(PA_ERR_UNSUPPORTED, "pa_summarize_blocks: too many heads");
+  if (cache.num_kv_heads > 32768)
+    return pa_fail(PA_ERR_UNSUPPORTED, "pa_summarize_blocks: num_kv_heads above 32768");
   if (num_tokens == 0) return PA_OK;
   if (!k_cache || !slot_mapping || !codes || !scales)
     return pa_fail(PA_ERR_INVALID, "pa_summarize_blocks: NULL pointer");

@@ -201,7 +201,8 @@ cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, int num_
   if (p.num_tokens >= 2 * kRopeCtas * num_sms && t < 2) t = 2;
   const int64_t spread = p.num_tokens / (2 * num_sms);
   if (t > spread) t = spread < 1 ? 1 : spread;
-  // ceil(2^32 / heads): r / heads is the high half of r * it for r < 8 * heads <= 2^20
+  // ceil(2^32 / heads): r / heads is the high half of r * it while r * heads
+  // is below 2^32 (r < 2 * heads <= 2^16, or 8 * heads <= 2^9)
   p.heads_inverse = (uint32_t)((((uint64_t)1 << 32) + heads - 1) / heads);
   p.tokens_per_cta = (int)t;
   const int64_t grid = (p.num_tokens + t - 1) / t;

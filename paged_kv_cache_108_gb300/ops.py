@@ -332,6 +332,9 @@ def write_and_decode(key, value, slot_mapping, out, q, k_cache, v_cache, block_t
 # batch, so their binding is kept short: one pass over the tensors, cached
 # descriptors (plain sizes), the raw stream handle.
 
+_BF16, _I32, _F32, _I8 = torch.bfloat16, torch.int32, torch.float32, torch.int8
+
+
 @functools.lru_cache(maxsize=256)
 def _desc_of(num_blocks, block_size, num_kv_heads, head_dim, dtype) -> CacheDesc:
     return CacheDesc(num_blocks, block_size, num_kv_heads, head_dim, dtype)
@@ -342,31 +345,39 @@ def _rope_of(rot_dim, max_position, axes, sections, in_turn, adjacent) -> RopeDe
     return RopeDesc(rot_dim, max_position, axes, (ctypes.c_int32 * 4)(*sections), in_turn, adjacent)
 
 
-def _desc_cached(k_cache) -> CacheDesc:
-    dt = k_cache.dtype
-    if k_cache.dim() != 4 or not (dt is torch.bfloat16 or dt in _FP8_DTYPES):
-        return cache_desc(k_cache)  # raises
-    return _desc_of(*k_cache.shape, PA_KV_BF16 if dt is torch.bfloat16 else PA_KV_FP8_E4M3)
+def _caches(k_cache, v_cache, k_scale, v_scale):
+    """Descriptor of a K and V cache pair, after the checks of their shapes,
+    dtypes and scales."""
+    shape, dt = k_cache.shape, k_cache.dtype
+    if shape != v_cache.shape or dt is not v_cache.dtype:
+        _same_cache(k_cache, v_cache)  # raises
+    if dt is torch.bfloat16:
+        if len(shape) == 4 and k_scale is None and v_scale is None:
+            return _desc_of(*shape, PA_KV_BF16)
+    elif len(shape) == 4 and dt in _FP8_DTYPES and k_scale is not None and v_scale is not None:
+        return _desc_of(*shape, PA_KV_FP8_E4M3)
+    desc = cache_desc(k_cache)
+    _scales(desc, k_scale, v_scale)
+    return desc
 
 
-def _pointers(device: int, *tensors):
-    """Addresses of (tensor, name, dtype or None) items, None for an absent
-    tensor; each must be contiguous on CUDA device ``device``."""
-    out = []
-    for t, name, dtype in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if not isinstance(t, torch.Tensor) or t.get_device() != device or device < 0:
-            if isinstance(t, torch.Tensor) and t.is_cuda and device >= 0:
-                raise ValueError(f"{name} is on {t.device}, other tensors are on cuda:{device}")
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dtype is not None and t.dtype is not dtype:
-            raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        out.append(t.data_ptr())
-    return out
+def _ptr(t, name, dtype, device: int):
+    """Address of a contiguous tensor of ``dtype`` on CUDA device ``device``;
+    None for an absent one."""
+    if t is None:
+        return None
+    try:
+        if t.get_device() == device >= 0 and t.dtype is dtype and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, other tensors are on cuda:{device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _call(device: int, fn: str, args, stream) -> None:
@@ -384,10 +395,11 @@ def _call(device: int, fn: str, args, stream) -> None:
 def _head_rows(t: torch.Tensor, name: str, device: int):
     """Pointer and token stride of a [tokens, heads, head_dim] tensor whose
     tokens may lie apart (a slice of a projection's output)."""
-    if t.get_device() != device or t.dtype is not torch.bfloat16:
-        _pointers(device, (t, name, torch.bfloat16))  # raises
-    (n, h, d), (s0, s1, s2) = t.shape, t.stride()
-    if t.numel() and ((d > 1 and s2 != 1) or (h > 1 and s1 != d)):
+    if t.get_device() != device or device < 0 or t.dtype is not _BF16:
+        _ptr(t, name, _BF16, device)  # raises
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"{name}: a token's heads and channels must be contiguous")
     return t.data_ptr(), (s0 if n > 1 else h * d)
 
@@ -401,44 +413,42 @@ def rope_and_cache(q_out, query, key, value, k_cache, v_cache, slot_mapping, pos
     Tokens of query, key and value may lie apart.  ``positions``: [N] or
     [axes, N] int32; ``cos_sin``: [max_position, rot_dim] fp32, cosines then
     sines; ``sections``: pairs turned by each axis."""
-    _same_cache(k_cache, v_cache)
-    desc = _desc_cached(k_cache)
-    if (k_scale is None or v_scale is None) if desc.dtype else (k_scale is not None or v_scale is not None):
-        _scales(desc, k_scale, v_scale)  # raises
+    desc = _caches(k_cache, v_cache, k_scale, v_scale)
+    _, _, kv_heads, d = k_cache.shape
     n = slot_mapping.numel()
-    want = (n, desc.num_kv_heads, desc.head_dim)
+    want = (n, kv_heads, d)
     if key.shape != want or value.shape != want:
         raise ValueError(f"key and value must be {list(want)} (one row per slot), "
                          f"got {list(key.shape)} and {list(value.shape)}")
     q_shape = query.shape
-    if len(q_shape) != 3 or q_shape[0] != n or q_shape[2] != want[2] or q_out.shape != q_shape:
-        raise ValueError(f"query and q_out must be [{n}, num_heads, {desc.head_dim}], "
+    if len(q_shape) != 3 or q_shape[0] != n or q_shape[2] != d or q_out.shape != q_shape:
+        raise ValueError(f"query and q_out must be [{n}, num_heads, {d}], "
                          f"got {list(query.shape)} and {list(q_out.shape)}")
     p_shape = positions.shape
     if len(p_shape) not in (1, 2) or p_shape[-1] != n:
         raise ValueError(f"positions must be [{n}] or [axes, {n}], got {list(positions.shape)}")
     axes = 1 if len(p_shape) == 1 else p_shape[0]
-    if cos_sin.dim() != 2:
+    t_shape = cos_sin.shape
+    if len(t_shape) != 2:
         raise ValueError("cos_sin must be [max_position, rot_dim]")
-    max_position, rot_dim = cos_sin.shape
-    sections = (rot_dim // 2,) if sections is None and axes == 1 else tuple(sections or ())
+    sections = (t_shape[1] // 2,) if sections is None and axes == 1 else tuple(sections or ())
     if len(sections) != axes:
         raise ValueError(f"sections must have one entry for each of the {axes} position axes")
     if axes > 4:
         raise ValueError("at most 4 position axes")
-    rope = _rope_of(rot_dim, max_position, axes, sections, int(sections_in_turn),
-                    int(adjacent_pairs))
-    device = k_cache.get_device()
-    qp, q_stride = _head_rows(query, "query", device)
-    kp, k_stride = _head_rows(key, "key", device)
-    vp, v_stride = _head_rows(value, "value", device)
-    o, kc, vc, slots, pos, table, ks, vs = _pointers(
-        device, (q_out, "q_out", torch.bfloat16), (k_cache, "k_cache", None),
-        (v_cache, "v_cache", None), (slot_mapping, "slot_mapping", torch.int32),
-        (positions, "positions", torch.int32), (cos_sin, "cos_sin", torch.float32),
-        (k_scale, "k_scale", torch.float32), (v_scale, "v_scale", torch.float32))
-    _call(device, "pa_rope_and_cache", (o, qp, q_stride, q_shape[1], kp, k_stride, vp, v_stride, kc,
-                                        vc, desc, slots, pos, table, rope, n, ks, vs), stream)
+    rope = _rope_of(t_shape[1], t_shape[0], axes, sections, bool(sections_in_turn),
+                    bool(adjacent_pairs))
+    dev = k_cache.get_device()
+    kv = k_cache.dtype
+    q, q_stride = _head_rows(query, "query", dev)
+    k, k_stride = _head_rows(key, "key", dev)
+    v, v_stride = _head_rows(value, "value", dev)
+    _call(dev, "pa_rope_and_cache", (
+        _ptr(q_out, "q_out", _BF16, dev), q, q_stride, q_shape[1], k, k_stride, v, v_stride,
+        _ptr(k_cache, "k_cache", kv, dev), _ptr(v_cache, "v_cache", kv, dev), desc,
+        _ptr(slot_mapping, "slot_mapping", _I32, dev), _ptr(positions, "positions", _I32, dev),
+        _ptr(cos_sin, "cos_sin", _F32, dev), rope, n, _ptr(k_scale, "k_scale", _F32, dev),
+        _ptr(v_scale, "v_scale", _F32, dev)), stream)
 
 
 def _check_ranges(desc, codes, scales):
@@ -464,13 +474,15 @@ def alloc_block_ranges(k_cache):
 def summarize_blocks(k_cache, slot_mapping, codes, scales, stream=None) -> None:
     """Keys' range per channel, in 8 bits, of every block whose last slot is
     in ``slot_mapping`` (the step's writes, already done on the stream)."""
-    desc = _desc_cached(k_cache)
+    if k_cache.dim() != 4 or not (k_cache.dtype is _BF16 or k_cache.dtype in _FP8_DTYPES):
+        cache_desc(k_cache)  # raises
+    desc = _desc_of(*k_cache.shape, PA_KV_BF16 if k_cache.dtype is _BF16 else PA_KV_FP8_E4M3)
     _check_ranges(desc, codes, scales)
-    device = k_cache.get_device()
-    kc, slots, c, s = _pointers(
-        device, (k_cache, "k_cache", None), (slot_mapping, "slot_mapping", torch.int32),
-        (codes, "codes", torch.int8), (scales, "scales", torch.float32))
-    _call(device, "pa_summarize_blocks", (kc, desc, slots, slot_mapping.numel(), c, s), stream)
+    dev = k_cache.get_device()
+    _call(dev, "pa_summarize_blocks", (
+        _ptr(k_cache, "k_cache", k_cache.dtype, dev), desc,
+        _ptr(slot_mapping, "slot_mapping", _I32, dev), slot_mapping.numel(),
+        _ptr(codes, "codes", _I8, dev), _ptr(scales, "scales", _F32, dev)), stream)
 
 
 def _check_rows(q, block_tables, context_lens, row_seqs, selected, num_kv_heads, head_dim):
@@ -507,14 +519,13 @@ def select_blocks(selected, q, codes, scales, block_tables, context_lens, block_
     _check_ranges(desc, codes, scales)
     rows, heads, seqs, max_blocks, top = _check_rows(q, block_tables, context_lens, row_seqs,
                                                      selected, hkv, d)
-    device = codes.get_device()
-    sel, qp, c, s, bt, cl, rs = _pointers(
-        device, (selected, "selected", torch.int32), (q, "q", torch.bfloat16),
-        (codes, "codes", torch.int8), (scales, "scales", torch.float32),
-        (block_tables, "block_tables", torch.int32), (context_lens, "context_lens", torch.int32),
-        (row_seqs, "row_seqs", torch.int32))
-    _call(device, "pa_select_blocks", (sel, qp, c, s, desc, bt, max_blocks, cl, rs, rows, seqs,
-                                       heads, top, int(sink), int(recent)), stream)
+    dev = codes.get_device()
+    _call(dev, "pa_select_blocks", (
+        _ptr(selected, "selected", _I32, dev), _ptr(q, "q", _BF16, dev),
+        _ptr(codes, "codes", _I8, dev), _ptr(scales, "scales", _F32, dev), desc,
+        _ptr(block_tables, "block_tables", _I32, dev), max_blocks,
+        _ptr(context_lens, "context_lens", _I32, dev), _ptr(row_seqs, "row_seqs", _I32, dev), rows,
+        seqs, heads, top, sink, recent), stream)
     return selected
 
 
@@ -522,23 +533,21 @@ def decode_selected(out, q, k_cache, v_cache, block_tables, context_lens, select
                     k_scale=None, v_scale=None, row_seqs=None, stream=None):
     """``decode`` over the blocks listed in ``selected`` [num_rows, H_kv, top];
     writes ``out`` [num_rows, H_q, d] bf16 and returns it."""
-    _same_cache(k_cache, v_cache)
-    desc = _desc_cached(k_cache)
-    if (k_scale is None or v_scale is None) if desc.dtype else (k_scale is not None or v_scale is not None):
-        _scales(desc, k_scale, v_scale)  # raises
+    desc = _caches(k_cache, v_cache, k_scale, v_scale)
     if out.shape != q.shape:
         raise ValueError("q and out must both be [num_rows, num_heads, head_dim]")
-    rows, heads, seqs, max_blocks, top = _check_rows(
-        q, block_tables, context_lens, row_seqs, selected, desc.num_kv_heads, desc.head_dim)
-    device = k_cache.get_device()
-    o, qp, kc, vc, bt, cl, rs, sel, ks, vs = _pointers(
-        device, (out, "out", torch.bfloat16), (q, "q", torch.bfloat16), (k_cache, "k_cache", None),
-        (v_cache, "v_cache", None), (block_tables, "block_tables", torch.int32),
-        (context_lens, "context_lens", torch.int32), (row_seqs, "row_seqs", torch.int32),
-        (selected, "selected", torch.int32), (k_scale, "k_scale", torch.float32),
-        (v_scale, "v_scale", torch.float32))
-    _call(device, "pa_decode_selected", (o, qp, kc, vc, desc, bt, max_blocks, cl, rs, sel, rows,
-                                         seqs, heads, top, scale, ks, vs), stream)
+    _, _, kv_heads, d = k_cache.shape
+    rows, heads, seqs, max_blocks, top = _check_rows(q, block_tables, context_lens, row_seqs,
+                                                     selected, kv_heads, d)
+    dev = k_cache.get_device()
+    kv = k_cache.dtype
+    _call(dev, "pa_decode_selected", (
+        _ptr(out, "out", _BF16, dev), _ptr(q, "q", _BF16, dev), _ptr(k_cache, "k_cache", kv, dev),
+        _ptr(v_cache, "v_cache", kv, dev), desc, _ptr(block_tables, "block_tables", _I32, dev),
+        max_blocks, _ptr(context_lens, "context_lens", _I32, dev),
+        _ptr(row_seqs, "row_seqs", _I32, dev), _ptr(selected, "selected", _I32, dev), rows, seqs,
+        heads, top, scale, _ptr(k_scale, "k_scale", _F32, dev),
+        _ptr(v_scale, "v_scale", _F32, dev)), stream)
     return out
 
 

@@ -60,7 +60,7 @@ def _rope_call(desc=None, rope=None, q_out=OTHER, q=FAKE, qs=256, heads=4, key=F
     (dict(key=ODD), INVALID),
     (dict(q_out=FAKE, qs=512), INVALID),                        # in place, rows apart
     (dict(q_out=ctypes.c_void_p(0x100000 + 512)), INVALID),     # overlaps by a row
-    (dict(heads=1 << 20, qs=1 << 26), UNSUPPORTED),
+    (dict(heads=32768 - 3, qs=1 << 26), UNSUPPORTED),
     (dict(n=0, q_out=None, key=None), OK),
 ])
 def test_rope_and_cache_refuses(kw, want):
@@ -76,6 +76,7 @@ def test_rope_and_cache_refuses(kw, want):
     (dict(codes=ODD), INVALID),
     (dict(scales=ODD), INVALID),
     (dict(k=None), INVALID),
+    (dict(desc=_desc(num_kv_heads=32769)), UNSUPPORTED),
     (dict(n=0, k=None), OK),
 ])
 def test_summarize_blocks_refuses(kw, want):

@@ -151,6 +151,14 @@ def test_rope_and_cache(case):
     _check_rope(c, out, kc0, vc0)
 
 
+@pytest.mark.parametrize("tokens,H,Hkv,rot", [(2501, 45, 3, 16), (2500, 6, 1, 16), (700, 3, 1, 32)])
+def test_rope_long_calls(tokens, H, Hkv, rot):
+    # two tokens a CTA, the last one alone; several of few heads
+    c = _rope_case(tokens, H, Hkv, 64, rot, None, False, False, "bf16", seed=6)
+    kc0, vc0 = c["kc"].clone(), c["vc"].clone()
+    _check_rope(c, _rope_run(c), kc0, vc0)
+
+
 def test_rope_skips_tokens_with_a_position_outside_the_table():
     c = _rope_case(20, 4, 2, 64, 32, [4, 6, 6], False, False, "bf16", seed=3)
     c["pos"][1, 4], c["pos"][0, 9], c["pos"][2, 19] = -1, 5000, 2 ** 31 - 1
@@ -308,6 +316,18 @@ def test_select_among_many(rows, blocks, top):
     _check_select(rng, lens, 4, 2, 128, 16, top, NB=500)
 
 
+@pytest.mark.parametrize("G,rows,Hkv,blocks", [(1, 310, 4, 40), (2, 310, 4, 33), (4, 310, 4, 20),
+                                               (2, 160, 4, 45), (8, 160, 4, 25), (4, 90, 4, 50),
+                                               (1, 40, 8, 60), (4, 30, 2, 1100), (2, 70, 4, 530)])
+def test_select_launch_shapes(G, rows, Hkv, blocks):
+    # from a warp a unit up to several CTAs a unit
+    rng = np.random.default_rng(rows + G)
+    lens = [max(1, (blocks - r % 7) * 16 - r) for r in range(rows)]
+    if blocks > 500:  # the oracle's time goes by the long rows
+        lens = [n if r % 9 == 0 else n % 300 for r, n in enumerate(lens)]
+    _check_select(rng, lens, G, Hkv, 64, 16, 11, NB=211)
+
+
 @pytest.mark.parametrize("rows,blocks", [(1, 4096), (70, 150)])
 def test_select_ties_go_to_the_lowest_index(rows, blocks):
     rng = np.random.default_rng(7)
@@ -427,7 +447,8 @@ def test_decode_selected(B, top, G, Hkv, d, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
-@pytest.mark.parametrize("rows,blocks,top", [(1, 300, 200), (1, 70, 64), (2, 130, 90), (9, 60, 31)])
+@pytest.mark.parametrize("rows,blocks,top", [(1, 300, 200), (1, 70, 64), (2, 130, 90), (9, 60, 31),
+                                             (50, 40, 33), (30, 50, 48), (25, 60, 56), (21, 64, 60)])
 def test_decode_selected_shared_by_a_cluster(rows, blocks, top, kv):
     rng = np.random.default_rng(blocks)
     lens = [blocks * 16 - 5 - 9 * r for r in range(rows)]
@@ -494,6 +515,49 @@ def test_decode_selected_of_every_block_is_decode():
     ops.decode_selected(b, q, kc, vc, _dev(tables), _dev(lens), _dev(every), d ** -0.5)
     # each within the bf16 decode tolerance of the true value
     assert ((a.float() - b.float()).abs() <= 2 * (1e-2 + 2e-2 * a.float().abs())).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_cache_beyond_32_bit_offsets(kv):
+    # K and V of over 2^32 bytes each; the blocks in use are at both ends
+    Hkv, d, B = 8, 128, 16
+    NB = 2 ** 32 // (B * Hkv * d * (2 if kv == "bf16" else 1)) + 5
+    rng = np.random.default_rng(30)
+    dt = torch.bfloat16 if kv == "bf16" else torch.uint8
+    kc, vc = (torch.zeros(NB, B, Hkv, d, device=DEV, dtype=dt) for _ in range(2))
+    ks, vs = (None, None) if kv == "bf16" else (_dev([0.02], torch.float32), _dev([0.02], torch.float32))
+    table = np.array([[NB - 1, 0, NB - 2, NB // 2 + 1]], np.int32)
+    n = 61
+    p = np.arange(n)
+    slots = _dev(table[0, p // B] * B + p % B)
+    x = _bf16(rng, n, 16 + 2 * Hkv, d)
+    q_out = torch.empty(n, 16, d, device=DEV, dtype=torch.bfloat16)
+    tab = _table(100, d)
+    ops.rope_and_cache(q_out, x[:, :16], x[:, 16:16 + Hkv], x[:, 16 + Hkv:], kc, vc, slots, _dev(p),
+                       _dev(tab, torch.float32), ks, vs)
+    codes, scales = ops.alloc_block_ranges(kc)
+    ops.summarize_blocks(kc, slots, codes, scales)
+    used = [int(b) for b in table[0]]
+    small = lambda t: torch.stack([t[b] for b in used])  # noqa: E731
+    k, v = ((_np(small(t)) if kv == "bf16" else _codes_np(small(t))) for t in (kc, vc))
+    want, mag = bs.rope_rows(_np(x[:, 16:16 + Hkv]), p[None], tab.astype(np.float64), [64], False, False)
+    got = k.reshape(-1, Hkv, d)[:n] * (1.0 if kv == "bf16" else float(ks.item()))
+    step = 2 ** -8 * np.abs(want) if kv == "bf16" else np.maximum(2 ** -4 * np.abs(want), 2 ** -10 * 0.02)
+    assert (np.abs(got - want) <= step + 2 ** -21 * mag).all()
+    for i, b in enumerate(used[:3]):
+        c, u = bs.block_range(k[i])
+        assert np.array_equal(codes[b].cpu().numpy(), c) and np.array_equal(scales[b].cpu().numpy(), u)
+    q, sel = q_out[-1:].contiguous(), torch.empty(1, Hkv, 3, device=DEV, dtype=torch.int32)
+    ops.select_blocks(sel, q, codes, scales, _dev(table), _dev([n]), B)
+    cs = np.stack([codes[b].cpu().numpy() for b in used])
+    us = np.stack([scales[b].cpu().numpy() for b in used]).astype(np.float64)
+    assert np.array_equal(sel[0].cpu().numpy(), bs.select(_np(q)[0], cs, us, [0, 1, 2, 3], n, B, 3, 1, 1))
+    out = torch.empty_like(q)
+    ops.decode_selected(out, q, kc, vc, _dev(table), _dev([n]), sel, d ** -0.5, ks, vs)
+    if kv == "fp8":
+        k, v = k * float(ks.item()), v * float(vs.item())
+    want, mag = bs.decode_selected(_np(q)[0], k, v, [0, 1, 2, 3], n, sel[0].cpu().numpy(), d ** -0.5)
+    assert (np.abs(_np(out)[0] - want) <= 2 ** -8 * np.abs(want) + 2 ** -11 * mag).all()
 
 
 # ------------------------------------------------------------- the whole step
