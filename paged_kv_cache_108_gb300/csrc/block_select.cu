@@ -382,10 +382,8 @@ struct Scorer<D, G, false> {
   }
 };
 
-constexpr int kMaxCluster = 8;   // CTAs that share a unit
-
-// Steps of 16 rows in a warp's ring.
-constexpr int select_stages(int threads) { return threads == 32 ? 2 : 3; }
+constexpr int kMaxCluster = 8;  // CTAs that share a unit
+constexpr int kStages = 2;      // steps of 16 rows in a warp's ring (3 and 4: no faster)
 
 // One cluster of CTAs per (query row, KV head).  Each CTA scores an equal
 // run of the candidate blocks and keeps their keys in its shared memory;
@@ -401,15 +399,15 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
     select_kernel(const __grid_constant__ SelectParams p, int clusters) {
   constexpr int kPieces = D / 32;  // 16-byte pieces of a row per lane
   constexpr int kWarps = NT / 32;
-  constexpr int kStages = select_stages(NT);
+  constexpr bool kShared = NT >= 256;  // a cluster may share the unit
   constexpr int kEarly = NT == 32 ? 4 : 1;  // ids per thread loaded before the length is known
   // (a copy whose 32-byte sectors were split in shared memory would fetch them twice)
   extern __shared__ __align__(128) uint8_t s_ring[];
   uint32_t* s_key = reinterpret_cast<uint32_t*>(s_ring + kWarps * kStages * 32 * D);
-  __shared__ uint32_t s_hists[NT == 32 ? 1 : 2][256];
-  __shared__ uint32_t s_total[NT == 32 ? 1 : 256];
-  __shared__ uint32_t s_pub[4];  // what peers read: least key, largest key, counts
-  __shared__ uint32_t s_warp[kWarps][2];
+  __shared__ uint32_t s_hists[kShared ? 2 : 1][256];
+  __shared__ uint32_t s_total[kShared ? 256 : 1];
+  __shared__ uint32_t s_pub[2];  // what peers read: least key, largest key
+  __shared__ uint32_t s_warp[kWarps][4];
   __shared__ uint32_t s_cut[3];
   __shared__ QueryCodes<D, G> s_q;
   auto sync = [] {
@@ -554,7 +552,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
     kmin = __reduce_min_sync(0xffffffffu, s_warp[lane % kWarps][0]);
     kmax = __reduce_max_sync(0xffffffffu, s_warp[lane % kWarps][1]);
   }
-  if (clusters > 1) {
+  if (kShared && clusters > 1) {
     if (tid == 0) {
       s_pub[0] = kmin;
       s_pub[1] = kmax;
@@ -573,9 +571,12 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
   // to it there are still wanted.
   int shift = 32 - __clz(kmax - kmin);
   uint32_t prefix = 0, left = want, equal = (uint32_t)cand;
+  // keys of the cluster's lower ranks above the cut and equal to it, as this
+  // thread's bins show them (before any pass all are equal)
+  uint32_t lower_gt = 0, lower_eq = tid == 0 ? (uint32_t)j0 : 0u;
   for (int pass = 0; shift > 0 && equal != left; ++pass) {
     // two histograms in turn: peers may still read the last pass's
-    uint32_t* s_hist = s_hists[NT == 32 ? 0 : pass & 1];
+    uint32_t* s_hist = s_hists[kShared ? pass & 1 : 0];
     const int bits = min(shift, 8);
     for (int i = tid; i < 256; i += NT) s_hist[i] = 0;
     sync();
@@ -586,15 +587,19 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
       if (((k >> (shift - 1)) >> 1) == prefix) atomicAdd(&s_hist[(k >> next) & ((1u << bits) - 1)], 1u);
     }
     const uint32_t* total = s_hist;
-    if (NT > 32 && clusters > 1) {
+    uint32_t lower = 0;  // lower ranks' keys in bin tid
+    if (kShared && clusters > 1) {
       cluster_sync();
-      for (int i = tid; i < 256; i += NT) {
+      if (tid < 256) {
         uint32_t t[kMaxCluster], sum = 0;
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) t[r] = r < clusters ? load_peer(&s_hist[i], r) : 0u;
+        for (int r = 0; r < kMaxCluster; ++r) t[r] = r < clusters ? load_peer(&s_hist[tid], r) : 0u;
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) sum += t[r];
-        s_total[i] = sum;
+        for (int r = 0; r < kMaxCluster; ++r) {
+          sum += t[r];
+          lower += r < rank ? t[r] : 0u;
+        }
+        s_total[tid] = sum;
       }
       total = s_total;
       __syncthreads();
@@ -627,12 +632,19 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
       }
     }
     sync();
+    if (kShared) {
+      lower_gt += tid > (int)s_cut[0] ? lower : 0u;
+      lower_eq = tid == (int)s_cut[0] ? lower : 0u;
+    }
     prefix = (prefix << bits) | s_cut[0];
     left = s_cut[1];
     equal = s_cut[2];
     shift = next;
     // (the next pass writes s_cut only after two more barriers)
   }
+  // nothing of a peer's memory is read from here on; no CTA leaves before all
+  // have come here
+  if (kShared && clusters > 1) asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory");
 
   // write: keys above the cut, and the first `left` of those equal to it;
   // each thread owns a run of the CTA's keys
@@ -653,36 +665,30 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
       b += w;
     }
   }
+  if (kShared) {
+    lower_gt = __reduce_add_sync(0xffffffffu, lower_gt);
+    lower_eq = __reduce_add_sync(0xffffffffu, lower_eq);
+  }
   sync();  // s_warp's extremes have been read
   if (lane == 31) {
     s_warp[warp][0] = a;
     s_warp[warp][1] = b;
+    s_warp[warp][2] = lower_gt;
+    s_warp[warp][3] = lower_eq;
   }
   sync();
   a -= gt;
   b -= eq;
-  uint32_t all_gt = 0, all_eq = 0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w == warp) {
-      a += all_gt;
-      b += all_eq;
+    if (w < warp) {
+      a += s_warp[w][0];
+      b += s_warp[w][1];
     }
-    all_gt += s_warp[w][0];
-    all_eq += s_warp[w][1];
-  }
-  if (clusters > 1) {
-    if (tid == 0) {
-      s_pub[2] = all_gt;
-      s_pub[3] = all_eq;
+    if (kShared && clusters > 1) {
+      a += s_warp[w][2];
+      b += s_warp[w][3];
     }
-    cluster_sync();
-    uint32_t before_gt = 0, before_eq = 0;
-    if (lane < rank) {
-      before_gt = load_peer(&s_pub[2], lane);
-      before_eq = load_peer(&s_pub[3], lane);
-    }
-    a += __reduce_add_sync(0xffffffffu, before_gt);
-    b += __reduce_add_sync(0xffffffffu, before_eq);
   }
   for (int i = i0; i < i1; ++i) {
     const uint32_t k = shift ? ((s_key[i] - kmin) >> (shift - 1)) >> 1 : s_key[i] - kmin;
@@ -691,13 +697,13 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
     a += k > prefix;
     b += is_eq;
   }
-  if (clusters > 1) cluster_sync();  // no CTA leaves while a peer may read its memory
+  if (kShared && clusters > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
 }
 
 template <int D, int G, int NT>
 cudaError_t launch_select_nt(const SelectParams& p, int c, cudaStream_t stream) {
   // the warps' rings, then a word for each candidate
-  const size_t smem = (size_t)NT / 32 * select_stages(NT) * 32 * D +
+  const size_t smem = (size_t)NT / 32 * kStages * 32 * D +
                       (size_t)((p.max_blocks + c - 1) / c) * sizeof(uint32_t);
   const int64_t units = (int64_t)p.num_rows * p.num_kv_heads;
   const cudaError_t e = allow_large<select_kernel<D, G, NT>>();
