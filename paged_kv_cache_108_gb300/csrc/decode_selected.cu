@@ -40,7 +40,8 @@ namespace pa {
 namespace {
 
 constexpr int kChunk = 16;      // tokens a warp handles at a time
-constexpr int kMaxCluster = 8;  // CTAs that share a (row, KV head)
+// CTAs that share a (row, KV head): what every device runs, and what this one does
+constexpr int kMaxCluster = 8, kLargeCluster = 12;
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
@@ -478,9 +479,16 @@ cudaError_t launch_one(const SelectedParams& p, int num_sms, cudaStream_t stream
   // CTAs per unit: as many as run at two to an SM, while each has a chunk for
   // every warp (8 rows of 8 heads, 8192 tokens each in e4m3: 55.6 us with 1,
   // 32.9 with 2, 28.5 with 4, and 41.5 with 5, which no longer run at once)
+  // Up to 8, and 12 where these few units' lists leave each CTA four chunks a
+  // warp and the SMs are not yet full (one row of 8 heads in bf16: 2048 blocks
+  // 57.1 us with 8, 40.9 with 12, 63.5 with 16; 256 blocks 11.2, 10.0, 9.5; 64
+  // blocks 6.0, 6.5; 4 rows of 256 blocks 16.4, 25.1).
+  const int64_t chunks = tokens / (kChunk * C::kWarps);  // for every warp of a CTA
+  const bool large = units * kLargeCluster <= 3 * num_sms / 2 && chunks >= 4 * kLargeCluster;
   int64_t c = 2 * num_sms / units;
-  if (c > tokens / (kChunk * C::kWarps)) c = tokens / (kChunk * C::kWarps);
-  c = c < 1 ? 1 : (c > kMaxCluster ? kMaxCluster : c);
+  if (c > chunks) c = chunks;
+  if (c > kMaxCluster) c = large ? kLargeCluster : kMaxCluster;
+  if (c < 1) c = 1;
   const size_t smem = C::kRing + (size_t)p.top * sizeof(int2);
   const cudaError_t e = allow_large<decode_selected_kernel<D, G, FP8>>();
   if (e != cudaSuccess) return e;

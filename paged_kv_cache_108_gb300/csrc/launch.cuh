@@ -9,7 +9,7 @@
 namespace pa {
 
 // Once per device: let `Kernel` take as much dynamic shared memory as a CTA
-// can have.
+// can have, and run in clusters of more than 8 CTAs.
 template <auto Kernel>
 cudaError_t allow_large() {
   static std::atomic<uint64_t> done{0};  // a bit per device
@@ -24,6 +24,8 @@ cudaError_t allow_large() {
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              227 * 1024 - (int)a.sharedSizeBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
   return e;
 }

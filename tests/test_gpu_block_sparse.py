@@ -448,7 +448,8 @@ def test_decode_selected(B, top, G, Hkv, d, kv):
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("rows,blocks,top", [(1, 300, 200), (1, 70, 64), (2, 130, 90), (9, 60, 31),
-                                             (50, 40, 33), (30, 50, 48), (25, 60, 56), (21, 64, 60)])
+                                             (50, 40, 33), (30, 50, 48), (25, 60, 56), (21, 64, 60),
+                                             (1, 430, 400)])
 def test_decode_selected_shared_by_a_cluster(rows, blocks, top, kv):
     rng = np.random.default_rng(blocks)
     lens = [blocks * 16 - 5 - 9 * r for r in range(rows)]
