@@ -7,6 +7,7 @@ missing: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -49,6 +50,7 @@ STATUS_NAMES = {0: "PA_OK", 1: "PA_ERR_INVALID", 2: "PA_ERR_OOM", 3: "PA_ERR_CUD
 
 _lock = threading.Lock()
 _lib = None
+_binding = None
 
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
@@ -131,6 +133,20 @@ def lib():
                 fn.argtypes = args
             _lib = handle
     return _lib
+
+
+def binding():
+    """The compiled binding of the block-sparse step's calls (_binding.so)."""
+    global _binding
+    if _binding is None:
+        lib()
+        if not os.path.exists(os.path.join(_HERE, "_binding.so")):
+            from . import build as _build
+            _build.build()
+        import torch  # noqa: F401  (its libraries are what the binding links against)
+
+        _binding = importlib.import_module("._binding", __package__)
+    return _binding
 
 
 def check(status: int) -> None:

@@ -1,18 +1,22 @@
-"""Build libpa.so (the C-ABI library) from csrc/ with nvcc for sm_103a.
+"""Build libpa.so (the C-ABI library) from csrc/ with nvcc for sm_103a, and
+_binding.so (csrc/binding.cpp, the compiled part of the torch binding).
 
 Each translation unit is compiled in parallel into _build/ at the repository
-root, then linked into paged_kv_cache_108_gb300/libpa.so (static CUDA runtime).
-A rebuild happens only when a source or header is newer than the library.
+root, then linked into paged_kv_cache_108_gb300/libpa.so (static CUDA runtime);
+_binding.so links against it and the installed torch.  A rebuild happens only
+when a source or header is newer than the libraries.
 Run ``python -m paged_kv_cache_108_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpa.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -30,19 +36,28 @@ def _nvcc() -> str:
     return cand
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found: the binding is compiled against its headers")
+    return spec.submodule_search_locations[0]
+
+
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
+    """The library's translation units."""
+    cpp = [s for s in glob.glob(os.path.join(CSRC, "*.cpp")) if s != BINDING_SRC]
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + cpp)
 
 
 def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
+    return [*sources(), BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
         os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "pa.h"), __file__]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -56,6 +71,12 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     else:
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", INCLUDE, "-I", CSRC,
                "-c", src, "-o", obj]
+        if src == BINDING_SRC:
+            inc = os.path.join(_torch_dir(), "include")
+            cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+            for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+                      sysconfig.get_path("include"), cuda):
+                cmd[1:1] = ["-isystem", d]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
@@ -69,17 +90,25 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
     if not force and not verbose_ptxas and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = sources()
+    srcs = [*sources(), BINDING_SRC]
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lpthread"]
+        *objs, binding = ex.map(lambda s: _compile(s, verbose_ptxas), srcs)
+    _link([_nvcc(), *ARCH, "-shared"], [*objs, "-lpthread"], LIB)
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    _link(["g++", "-shared"],
+          [binding, "-L", PKG, "-l:libpa.so", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"], BINDING)
+    return LIB
+
+
+def _link(cmd, inputs, out: str) -> None:
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = [*cmd, "-o", tmp, *inputs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, out)
 
 
 if __name__ == "__main__":

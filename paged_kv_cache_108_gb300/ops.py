@@ -7,12 +7,11 @@ Names and argument order follow include/pa.h.
 from __future__ import annotations
 
 import ctypes
-import functools
 
 import torch
 
 from . import _lib
-from ._lib import CacheDesc, DecodeOpts, PA_KV_BF16, PA_KV_FP8_E4M3, RopeDesc
+from ._lib import CacheDesc, DecodeOpts, PA_KV_BF16, PA_KV_FP8_E4M3
 
 _FP8_DTYPES = (torch.uint8, getattr(torch, "float8_e4m3fn", torch.uint8))
 
@@ -328,81 +327,8 @@ def write_and_decode(key, value, slot_mapping, out, q, k_cache, v_cache, block_t
     return out
 
 
-# The block-sparse step's calls take 5 to 15 us on the device for a decode
-# batch, so their binding is kept short: one pass over the tensors, cached
-# descriptors (plain sizes), the raw stream handle.
-
-_BF16, _I32, _F32, _I8 = torch.bfloat16, torch.int32, torch.float32, torch.int8
-
-
-@functools.lru_cache(maxsize=256)
-def _desc_of(num_blocks, block_size, num_kv_heads, head_dim, dtype) -> CacheDesc:
-    return CacheDesc(num_blocks, block_size, num_kv_heads, head_dim, dtype)
-
-
-@functools.lru_cache(maxsize=256)
-def _rope_of(rot_dim, max_position, axes, sections, in_turn, adjacent) -> RopeDesc:
-    return RopeDesc(rot_dim, max_position, axes, (ctypes.c_int32 * 4)(*sections), in_turn, adjacent)
-
-
-def _caches(k_cache, v_cache, k_scale, v_scale):
-    """Descriptor of a K and V cache pair, after the checks of their shapes,
-    dtypes and scales."""
-    shape, dt = k_cache.shape, k_cache.dtype
-    if shape != v_cache.shape or dt is not v_cache.dtype:
-        _same_cache(k_cache, v_cache)  # raises
-    if dt is torch.bfloat16:
-        if len(shape) == 4 and k_scale is None and v_scale is None:
-            return _desc_of(*shape, PA_KV_BF16)
-    elif len(shape) == 4 and dt in _FP8_DTYPES and k_scale is not None and v_scale is not None:
-        return _desc_of(*shape, PA_KV_FP8_E4M3)
-    desc = cache_desc(k_cache)
-    _scales(desc, k_scale, v_scale)
-    return desc
-
-
-def _ptr(t, name, dtype, device: int):
-    """Address of a contiguous tensor of ``dtype`` on CUDA device ``device``;
-    None for an absent one."""
-    if t is None:
-        return None
-    try:
-        if t.get_device() == device >= 0 and t.dtype is dtype and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or device < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, other tensors are on cuda:{device}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _call(device: int, fn: str, args, stream) -> None:
-    """Calls library function ``fn`` with the tensors' device current and, by
-    default, on that device's current stream."""
-    if device != torch._C._cuda_getDevice():
-        with torch.cuda.device(device):
-            return _call(device, fn, args, stream)
-    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    status = getattr(_lib.lib(), fn)(*args, raw)
-    if status:
-        _lib.check(status)
-
-
-def _head_rows(t: torch.Tensor, name: str, device: int):
-    """Pointer and token stride of a [tokens, heads, head_dim] tensor whose
-    tokens may lie apart (a slice of a projection's output)."""
-    if t.get_device() != device or device < 0 or t.dtype is not _BF16:
-        _ptr(t, name, _BF16, device)  # raises
-    n, h, d = t.shape
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
-        raise ValueError(f"{name}: a token's heads and channels must be contiguous")
-    return t.data_ptr(), (s0 if n > 1 else h * d)
-
+# The block-sparse step's calls: their arguments are checked and handed over
+# by the compiled binding (csrc/binding.cpp).
 
 def rope_and_cache(q_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
                    k_scale=None, v_scale=None, sections=None, sections_in_turn=False,
@@ -413,52 +339,11 @@ def rope_and_cache(q_out, query, key, value, k_cache, v_cache, slot_mapping, pos
     Tokens of query, key and value may lie apart.  ``positions``: [N] or
     [axes, N] int32; ``cos_sin``: [max_position, rot_dim] fp32, cosines then
     sines; ``sections``: pairs turned by each axis."""
-    desc = _caches(k_cache, v_cache, k_scale, v_scale)
-    _, _, kv_heads, d = k_cache.shape
-    n = slot_mapping.numel()
-    want = (n, kv_heads, d)
-    if key.shape != want or value.shape != want:
-        raise ValueError(f"key and value must be {list(want)} (one row per slot), "
-                         f"got {list(key.shape)} and {list(value.shape)}")
-    q_shape = query.shape
-    if len(q_shape) != 3 or q_shape[0] != n or q_shape[2] != d or q_out.shape != q_shape:
-        raise ValueError(f"query and q_out must be [{n}, num_heads, {d}], "
-                         f"got {list(query.shape)} and {list(q_out.shape)}")
-    p_shape = positions.shape
-    if len(p_shape) not in (1, 2) or p_shape[-1] != n:
-        raise ValueError(f"positions must be [{n}] or [axes, {n}], got {list(positions.shape)}")
-    axes = 1 if len(p_shape) == 1 else p_shape[0]
-    t_shape = cos_sin.shape
-    if len(t_shape) != 2:
-        raise ValueError("cos_sin must be [max_position, rot_dim]")
-    sections = (t_shape[1] // 2,) if sections is None and axes == 1 else tuple(sections or ())
-    if len(sections) != axes:
-        raise ValueError(f"sections must have one entry for each of the {axes} position axes")
-    if axes > 4:
-        raise ValueError("at most 4 position axes")
-    rope = _rope_of(t_shape[1], t_shape[0], axes, sections, bool(sections_in_turn),
-                    bool(adjacent_pairs))
-    dev = k_cache.get_device()
-    kv = k_cache.dtype
-    q, q_stride = _head_rows(query, "query", dev)
-    k, k_stride = _head_rows(key, "key", dev)
-    v, v_stride = _head_rows(value, "value", dev)
-    _call(dev, "pa_rope_and_cache", (
-        _ptr(q_out, "q_out", _BF16, dev), q, q_stride, q_shape[1], k, k_stride, v, v_stride,
-        _ptr(k_cache, "k_cache", kv, dev), _ptr(v_cache, "v_cache", kv, dev), desc,
-        _ptr(slot_mapping, "slot_mapping", _I32, dev), _ptr(positions, "positions", _I32, dev),
-        _ptr(cos_sin, "cos_sin", _F32, dev), rope, n, _ptr(k_scale, "k_scale", _F32, dev),
-        _ptr(v_scale, "v_scale", _F32, dev)), stream)
-
-
-def _check_ranges(desc, codes, scales):
-    if codes.shape != (desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim):
-        raise ValueError(f"codes must be [num_blocks, num_kv_heads, 2, head_dim] = "
-                         f"{[desc.num_blocks, desc.num_kv_heads, 2, desc.head_dim]}, "
-                         f"got {list(codes.shape)}")
-    if scales.shape != codes.shape[:2]:
-        raise ValueError(f"scales must be [num_blocks, num_kv_heads] = "
-                         f"{[desc.num_blocks, desc.num_kv_heads]}, got {list(scales.shape)}")
+    status = (_lib._binding or _lib.binding()).rope_and_cache(
+        q_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, k_scale,
+        v_scale, sections, sections_in_turn, adjacent_pairs, stream)
+    if status:
+        _lib.check(status)
 
 
 def alloc_block_ranges(k_cache):
@@ -474,36 +359,10 @@ def alloc_block_ranges(k_cache):
 def summarize_blocks(k_cache, slot_mapping, codes, scales, stream=None) -> None:
     """Keys' range per channel, in 8 bits, of every block whose last slot is
     in ``slot_mapping`` (the step's writes, already done on the stream)."""
-    if k_cache.dim() != 4 or not (k_cache.dtype is _BF16 or k_cache.dtype in _FP8_DTYPES):
-        cache_desc(k_cache)  # raises
-    desc = _desc_of(*k_cache.shape, PA_KV_BF16 if k_cache.dtype is _BF16 else PA_KV_FP8_E4M3)
-    _check_ranges(desc, codes, scales)
-    dev = k_cache.get_device()
-    _call(dev, "pa_summarize_blocks", (
-        _ptr(k_cache, "k_cache", k_cache.dtype, dev), desc,
-        _ptr(slot_mapping, "slot_mapping", _I32, dev), slot_mapping.numel(),
-        _ptr(codes, "codes", _I8, dev), _ptr(scales, "scales", _F32, dev)), stream)
-
-
-def _check_rows(q, block_tables, context_lens, row_seqs, selected, num_kv_heads, head_dim):
-    """Sizes shared by the calls over query rows; (rows, heads, sequences, top)."""
-    if q.dim() != 3:
-        raise ValueError("q must be [num_rows, num_heads, head_dim]")
-    rows, heads, d = q.shape
-    t_shape, s_shape = block_tables.shape, selected.shape
-    if len(t_shape) != 2 or (row_seqs is None and t_shape[0] != rows):
-        raise ValueError(f"block_tables must be [{'num_seqs' if row_seqs is not None else rows}, "
-                         f"max_blocks_per_seq], got {list(block_tables.shape)}")
-    if context_lens.numel() != rows:
-        raise ValueError(f"context_lens needs {rows} entries, got {context_lens.numel()}")
-    if row_seqs is not None and row_seqs.numel() != rows:
-        raise ValueError(f"row_seqs needs {rows} entries, got {row_seqs.numel()}")
-    if len(s_shape) != 3 or s_shape[0] != rows or s_shape[1] != num_kv_heads:
-        raise ValueError(f"selected must be [{rows}, {num_kv_heads}, top], "
-                         f"got {list(selected.shape)}")
-    if d != head_dim:
-        raise ValueError(f"q's head_dim {d} differs from the cache's {head_dim}")
-    return rows, heads, t_shape[0], t_shape[1], s_shape[2]
+    status = (_lib._binding or _lib.binding()).summarize_blocks(k_cache, slot_mapping, codes,
+                                                                scales, stream)
+    if status:
+        _lib.check(status)
 
 
 def select_blocks(selected, q, codes, scales, block_tables, context_lens, block_size, sink=1,
@@ -512,20 +371,11 @@ def select_blocks(selected, q, codes, scales, block_tables, context_lens, block_
     [num_rows, H_kv, top] int32 (rising logical block indices, then -1) and
     returns it.  ``row_seqs`` [num_rows] names each row's sequence when there
     are several queries to one."""
-    if codes.dim() != 4 or codes.shape[2] != 2:
-        raise ValueError("codes must be [num_blocks, num_kv_heads, 2, head_dim]")
-    nb, hkv, _, d = codes.shape
-    desc = _desc_of(nb, int(block_size), hkv, d, PA_KV_BF16)
-    _check_ranges(desc, codes, scales)
-    rows, heads, seqs, max_blocks, top = _check_rows(q, block_tables, context_lens, row_seqs,
-                                                     selected, hkv, d)
-    dev = codes.get_device()
-    _call(dev, "pa_select_blocks", (
-        _ptr(selected, "selected", _I32, dev), _ptr(q, "q", _BF16, dev),
-        _ptr(codes, "codes", _I8, dev), _ptr(scales, "scales", _F32, dev), desc,
-        _ptr(block_tables, "block_tables", _I32, dev), max_blocks,
-        _ptr(context_lens, "context_lens", _I32, dev), _ptr(row_seqs, "row_seqs", _I32, dev), rows,
-        seqs, heads, top, sink, recent), stream)
+    status = (_lib._binding or _lib.binding()).select_blocks(
+        selected, q, codes, scales, block_tables, context_lens, block_size, sink, recent, row_seqs,
+        stream)
+    if status:
+        _lib.check(status)
     return selected
 
 
@@ -533,21 +383,11 @@ def decode_selected(out, q, k_cache, v_cache, block_tables, context_lens, select
                     k_scale=None, v_scale=None, row_seqs=None, stream=None):
     """``decode`` over the blocks listed in ``selected`` [num_rows, H_kv, top];
     writes ``out`` [num_rows, H_q, d] bf16 and returns it."""
-    desc = _caches(k_cache, v_cache, k_scale, v_scale)
-    if out.shape != q.shape:
-        raise ValueError("q and out must both be [num_rows, num_heads, head_dim]")
-    _, _, kv_heads, d = k_cache.shape
-    rows, heads, seqs, max_blocks, top = _check_rows(q, block_tables, context_lens, row_seqs,
-                                                     selected, kv_heads, d)
-    dev = k_cache.get_device()
-    kv = k_cache.dtype
-    _call(dev, "pa_decode_selected", (
-        _ptr(out, "out", _BF16, dev), _ptr(q, "q", _BF16, dev), _ptr(k_cache, "k_cache", kv, dev),
-        _ptr(v_cache, "v_cache", kv, dev), desc, _ptr(block_tables, "block_tables", _I32, dev),
-        max_blocks, _ptr(context_lens, "context_lens", _I32, dev),
-        _ptr(row_seqs, "row_seqs", _I32, dev), _ptr(selected, "selected", _I32, dev), rows, seqs,
-        heads, top, scale, _ptr(k_scale, "k_scale", _F32, dev),
-        _ptr(v_scale, "v_scale", _F32, dev)), stream)
+    status = (_lib._binding or _lib.binding()).decode_selected(
+        out, q, k_cache, v_cache, block_tables, context_lens, selected, scale, k_scale, v_scale,
+        row_seqs, stream)
+    if status:
+        _lib.check(status)
     return out
 
 

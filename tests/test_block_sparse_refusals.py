@@ -169,6 +169,38 @@ def test_binding_checks_the_rotating_write():
             ops.rope_and_cache(**{**good, **kw})
 
 
+def test_binding_refuses_what_is_no_tensor_or_number():
+    kc = _z(NB, B, HKV, D)
+    codes, scales = ops.alloc_block_ranges(kc)
+    slots = _z(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="slot_mapping must be a CUDA tensor"):
+        ops.summarize_blocks(kc, [0, 1], codes, scales)
+    with pytest.raises(ValueError, match="cache must be"):
+        ops.summarize_blocks(kc[0], slots, codes, scales)
+    with pytest.raises(ValueError, match="cache dtype"):
+        ops.summarize_blocks(kc.float(), slots, codes, scales)
+    i32 = torch.int32
+    sel = dict(selected=_z(3, HKV, 4, dtype=i32), q=_z(3, H, D), codes=codes, scales=scales,
+               block_tables=_z(3, 7, dtype=i32), context_lens=_z(3, dtype=i32))
+    with pytest.raises(ValueError, match="block_size must be an integer"):
+        ops.select_blocks(block_size=None, **sel)
+    with pytest.raises(ValueError, match="recent does not fit"):
+        ops.select_blocks(block_size=B, recent=2 ** 40, **sel)
+    with pytest.raises(ValueError, match="scale must be a number"):
+        ops.decode_selected(out=_z(3, H, D), q=_z(3, H, D), k_cache=kc, v_cache=kc.clone(),
+                            block_tables=sel["block_tables"], context_lens=sel["context_lens"],
+                            selected=sel["selected"], scale="0.1")
+    rope = dict(q_out=_z(3, H, D), query=_z(3, H, D), key=_z(3, HKV, D), value=_z(3, HKV, D),
+                k_cache=kc, v_cache=kc.clone(), slot_mapping=slots,
+                positions=_z(2, 3, dtype=i32), cos_sin=_z(9, D, dtype=torch.float32))
+    with pytest.raises(ValueError, match="sections"):
+        ops.rope_and_cache(sections=[16, "16"], **rope)
+    with pytest.raises(ValueError, match="sections"):
+        ops.rope_and_cache(sections=32, **rope)
+    with pytest.raises(ValueError, match="sections_in_turn"):
+        ops.rope_and_cache(sections=[16, 16], sections_in_turn=torch.zeros(2), **rope)
+
+
 def test_binding_checks_ranges_and_selections():
     kc = _z(NB, B, HKV, D)
     codes, scales = ops.alloc_block_ranges(kc)
