@@ -103,12 +103,11 @@ __device__ __forceinline__ uint32_t widen(uint16_t codes) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ float load_peer(const float* own, uint32_t rank) {
+// Writes a word of another CTA's shared memory.
+__device__ __forceinline__ void store_peer(float* own, uint32_t rank, float v) {
   uint32_t a;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(a) : "r"(smem_u32(own)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(a) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(a), "f"(v) : "memory");
 }
 
 // The factor of a part whose running max is m under the whole's max; 1 where
@@ -152,34 +151,71 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads)
   using C = Cfg<D, FP8>;
   constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   constexpr int kSteps = D / 16;  // k16 steps of q . k; m16 tiles of O^T
+  constexpr int kEarly = 2;       // list entries per thread in the first loads
   extern __shared__ __align__(128) uint8_t smem[];
   // listed entries of this CTA's share: first slot of the block, tokens in use
   int2* s_entry = reinterpret_cast<int2*>(smem + C::kRing);
   __shared__ int s_last;
-  __shared__ float s_out[G][D];        // the CTA's result, for the cluster
-  __shared__ float s_m[8], s_l[8];
+  // what the cluster's CTAs hand this one: their sums of its share of the
+  // outputs, and every head's max and sum
+  __shared__ float s_part[G * D + kLargeCluster];
+  __shared__ float s_state[kLargeCluster][G][2];
+  // the first half of a cluster barrier: peers may be written to once all run
+  if (clusters > 1) asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory");
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int g = lane / 4, c = lane % 4;  // MMA fragment coordinates
   const int unit = blockIdx.x / clusters, rank = blockIdx.x % clusters;
   const int row = unit / p.num_kv_heads, kvh = unit - row * p.num_kv_heads;
-  const int seq = p.row_seqs ? p.row_seqs[row] : row;
   const int lb = p.log2_block_size, block = 1 << lb;
-  int64_t n = p.context_lens[row];
-  n = min(n, (int64_t)p.max_blocks << lb);
-  if ((unsigned)seq >= (unsigned)p.num_seqs) n = 0;
+
+  // What depends on nothing is loaded first: the list's first entries, the
+  // length, the queries; then the entries' physical blocks.
   const int32_t* list = p.selected + (int64_t)unit * p.top;
-  const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks;
+  int j_early[kEarly], phys_early[kEarly];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) {
+    const int i = k * kThreads + tid;
+    j_early[k] = i < p.top ? list[i] : -1;
+  }
+  const int seq = p.row_seqs ? p.row_seqs[row] : row;
+  int64_t n = p.context_lens[row];
+  const bool known = (unsigned)seq < (unsigned)p.num_seqs;
+  const int32_t* table = p.block_tables + (known ? (int64_t)seq * p.max_blocks : 0);
+  constexpr int kColHeads = G <= 4 ? 4 : 8;
+  const int qh = g % kColHeads;  // the query head of this lane's MMA column
+  uint2 qw[kSteps];              // its channels, as operand B takes them
+  {
+    const __nv_bfloat16* q = p.q + ((int64_t)unit * G + qh) * D;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      qw[k] = make_uint2(0, 0);
+      if (qh < G) {
+        if (FP8) {
+          qw[k] = *reinterpret_cast<const uint2*>(q + 16 * k + 4 * c);
+        } else {
+          qw[k].x = *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c);
+          qw[k].y = *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 + 2 * c);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    phys_early[k] = known && (unsigned)j_early[k] < (unsigned)p.max_blocks ? table[j_early[k]] : -1;
+  n = known ? min(n, (int64_t)p.max_blocks << lb) : 0;
 
   // entries up to the last that names a block below the context's end
+  auto inside = [&](int j) { return j >= 0 && ((int64_t)j << lb) < n; };
   if (tid == 0) s_last = 0;
   __syncthreads();
   int last = 0;
-  for (int i = tid; i < p.top; i += kThreads) {
-    const int j = list[i];
-    if (j >= 0 && ((int64_t)j << lb) < n) last = i + 1;
-  }
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (inside(j_early[k])) last = k * kThreads + tid + 1;
+  for (int i = kEarly * kThreads + tid; i < p.top; i += kThreads)
+    if (inside(list[i])) last = i + 1;
   last = __reduce_max_sync(0xffffffffu, last);
   if (lane == 0 && last) atomicMax(&s_last, last);
   __syncthreads();
@@ -192,52 +228,45 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads)
   const int slot0 = c0 * kChunk;  // in list order
   const int e0 = slot0 >> lb;
   const int e1 = chunks ? min(last, ((slot0 + chunks * kChunk - 1) >> lb) + 1) : e0;
-  for (int i = e0 + tid; i < e1; i += kThreads) {
+  auto enter = [&](int i, int j, int phys) {
+    if (i < e0 || i >= e1) return;
+    s_entry[i - e0] = inside(j) && (unsigned)phys < (unsigned)p.num_blocks
+                          ? make_int2(phys << lb, (int)min((int64_t)block, n - ((int64_t)j << lb)))
+                          : make_int2(0, 0);
+  };
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k) enter(k * kThreads + tid, j_early[k], phys_early[k]);
+  for (int i = max(e0, kEarly * kThreads) + tid; i < e1; i += kThreads) {
     const int j = list[i];
-    int2 e = make_int2(0, 0);
-    if (j >= 0 && ((int64_t)j << lb) < n) {
-      const int phys = table[j];
-      if ((unsigned)phys < (unsigned)p.num_blocks)
-        e = make_int2(phys << lb, (int)min((int64_t)block, n - ((int64_t)j << lb)));
-    }
-    s_entry[i - e0] = e;
+    enter(i, j, inside(j) ? table[j] : -1);
   }
 
   // q as MMA operand B: column `col` is query head col (mod 4 when G <= 4)
-  constexpr int kColHeads = G <= 4 ? 4 : 8;
-  const int qh = g % kColHeads;
   uint32_t qb[kSteps][2];
   float q_scale = 1.f;  // FP8: what q's columns were divided by
-  {
-    const __nv_bfloat16* q = p.q + ((int64_t)(row * p.num_kv_heads + kvh) * G + qh) * D;
-    const bool real = qh < G;
-    if constexpr (FP8) {
-      uint2 w[kSteps];
-      float amax = 0.f;
+  if constexpr (FP8) {
+    float amax = 0.f;
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        w[k] = real ? *reinterpret_cast<const uint2*>(q + 16 * k + 4 * c) : make_uint2(0, 0);
-        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(w[k].x)), fabsf(bf16_hi(w[k].x))),
-                                 fmaxf(fabsf(bf16_lo(w[k].y)), fabsf(bf16_hi(w[k].y)))));
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // 2^floor(log2 amax); kept within the normal floats so that its
-      // reciprocal is exact (an infinite or NaN q stays what it is)
-      const int e = min(max((int)(__float_as_uint(amax) >> 23), 1), 253) - 127;
-      q_scale = __int_as_float((127 + e) << 23);
-      const float inv = __int_as_float((127 - e) << 23);
+    for (int k = 0; k < kSteps; ++k)
+      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(qw[k].x)), fabsf(bf16_hi(qw[k].x))),
+                               fmaxf(fabsf(bf16_lo(qw[k].y)), fabsf(bf16_hi(qw[k].y)))));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // 2^floor(log2 amax); kept within the normal floats so that its
+    // reciprocal is exact (an infinite or NaN q stays what it is)
+    const int e = min(max((int)(__float_as_uint(amax) >> 23), 1), 253) - 127;
+    q_scale = __int_as_float((127 + e) << 23);
+    const float inv = __int_as_float((127 - e) << 23);
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        qb[k][0] = pack2<true>(bf16_lo(w[k].x) * inv, bf16_hi(w[k].x) * inv);
-        qb[k][1] = pack2<true>(bf16_lo(w[k].y) * inv, bf16_hi(w[k].y) * inv);
-      }
-    } else {
+    for (int k = 0; k < kSteps; ++k) {
+      qb[k][0] = pack2<true>(bf16_lo(qw[k].x) * inv, bf16_hi(qw[k].x) * inv);
+      qb[k][1] = pack2<true>(bf16_lo(qw[k].y) * inv, bf16_hi(qw[k].y) * inv);
+    }
+  } else {
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        qb[k][0] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 2 * c) : 0u;
-        qb[k][1] = real ? *reinterpret_cast<const uint32_t*>(q + 16 * k + 8 + 2 * c) : 0u;
-      }
+    for (int k = 0; k < kSteps; ++k) {
+      qb[k][0] = qw[k].x;
+      qb[k][1] = qw[k].y;
     }
   }
   // the logit factors of this lane's two accumulator columns 2c, 2c + 1
@@ -428,7 +457,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads)
     w[3] = l1;
   }
   __syncthreads();
-  // every CTA of the cluster: its own result, unnormalised
+  // the CTA's own result, unnormalised; in a cluster each CTA owns a share of
+  // the outputs and is handed the others' parts of it
+  const int share = (G * D + clusters - 1) / clusters;
+  if (clusters > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
   for (int i = tid; i < G * D; i += kThreads) {
     const int h = i / D, d = i % D;
     float mm = -INFINITY;
@@ -443,32 +475,33 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads)
       acc += a * x;
       l += a * ml[(w * 8 + h) * 2 + 1];
     }
-    __nv_bfloat16* out = p.out + ((int64_t)(row * p.num_kv_heads + kvh) * G + h) * D + d;
     if (clusters == 1) {
-      *out = quotient(acc * v_scale, l);
+      p.out[(int64_t)unit * G * D + i] = quotient(acc * v_scale, l);
     } else {
-      s_out[h][d] = acc;
-      if (d == 0) {
-        s_m[h] = mm;
-        s_l[h] = l;
+      const int owner = i / share;
+      store_peer(&s_part[rank * share + i - owner * share], owner, acc);
+      if (d < clusters) {
+        store_peer(&s_state[rank][h][0], d, mm);
+        store_peer(&s_state[rank][h][1], d, l);
       }
     }
   }
   if (clusters == 1) return;
-  cluster_sync();
-  for (int i = rank * kThreads + tid; i < G * D; i += clusters * kThreads) {
-    const int h = i / D, d = i % D;
+  cluster_sync();  // all parts have arrived; peers' memory is not touched again
+  for (int i = tid; i < share; i += kThreads) {
+    const int o = rank * share + i;
+    if (o >= G * D) break;
+    const int h = o / D;
     float mm = -INFINITY;
-    for (int r = 0; r < clusters; ++r) mm = fmaxf(mm, load_peer(&s_m[h], r));
+    for (int r = 0; r < clusters; ++r) mm = fmaxf(mm, s_state[r][h][0]);
     float acc = 0.f, l = 0.f;
     for (int r = 0; r < clusters; ++r) {
-      const float a = weight(load_peer(&s_m[h], r), mm);
-      acc += a * load_peer(&s_out[h][d], r);
-      l += a * load_peer(&s_l[h], r);
+      const float a = weight(s_state[r][h][0], mm);
+      acc += a * s_part[r * share + i];
+      l += a * s_state[r][h][1];
     }
-    p.out[((int64_t)(row * p.num_kv_heads + kvh) * G + h) * D + d] = quotient(acc * v_scale, l);
+    p.out[(int64_t)unit * G * D + o] = quotient(acc * v_scale, l);
   }
-  cluster_sync();  // no CTA leaves while a peer may read its memory
 }
 
 template <int D, int G, bool FP8>
