@@ -363,6 +363,24 @@ def test_select_odd_values():
     _check_select(rng, lens, 2, 2, 64, 16, 45, q=q, codes=(c, s), tables=tables)
 
 
+@pytest.mark.parametrize("G,d", [(1, 128), (4, 128), (8, 128), (8, 64)])
+def test_select_largest_codes(G, d):
+    # sums at the ends of their range, a unit apart: no rounding may show
+    rng = np.random.default_rng(40)
+    lens = [16 * 60] * 3
+    q = torch.full((3, 2 * G, d), 127.0, device=DEV, dtype=torch.bfloat16)
+    q[1] = -127.0
+    q[2, :, ::2] = -127.0
+    c = np.empty((90, 2, 2, d), np.int8)
+    c[:, :, 0], c[:, :, 1] = 127, 126
+    c[30:60, :, 0], c[30:60, :, 1] = -126, -127
+    for b in range(90):  # each block a unit or two from the next
+        c[b, :, :, rng.integers(0, d, b % 7)] -= 1 if b < 30 or b >= 60 else -1
+    c[:, :, 1] = np.minimum(c[:, :, 0], c[:, :, 1])
+    s = np.ones((90, 2), np.float32)
+    _check_select(rng, lens, G, 2, d, 16, 13, q=q, codes=(c, s), NB=90)
+
+
 def test_select_rows_of_one_sequence_and_cut_lengths():
     rng = np.random.default_rng(9)
     lens = [700, 701, 702, 33, 34, 10 ** 9, 2 ** 31 - 1, 50, 60]
