@@ -52,7 +52,8 @@ cudaError_t launch_dependent(dim3 grid, dim3 block, size_t smem, cudaStream_t st
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, Kernel, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  const cudaError_t last = cudaGetLastError();  // a refused launch leaves no error behind
+  return e != cudaSuccess ? e : last;
 }
 
 }  // namespace pa

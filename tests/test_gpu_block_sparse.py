@@ -15,6 +15,10 @@ Tolerances, from the arithmetic (u = 2^-24, half a step of fp32):
   two-part rounding and 2^-21 for exp2.  Numerator and denominator both:
   under 2^-11 sum p |v| / sum p in all; then half a step of bf16.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -689,6 +693,31 @@ def test_steps_captured_and_replayed(kv):
         s.stage()
         g.replay()
         s.check()
+
+
+def test_first_use_inside_a_capture():
+    # a fresh process whose first call of each kernel is captured: the rows are
+    # few and the context long, so that the clustered variants are among them
+    code = """
+import torch
+from tests.test_gpu_block_sparse import _Step
+s = _Step.__new__(_Step)
+_Step._prefill = lambda self: None
+_Step.__init__(s, "bf16", 5)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    s.run()
+s.lens = s.lens * 0
+for _ in range(20):
+    s.stage()
+    g.replay()
+s.check()
+print("captured first")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert "captured first" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_batches_on_two_streams():
