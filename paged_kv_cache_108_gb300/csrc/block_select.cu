@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(32 * kSumWarps, FP8 ? 2 : 4)
 // Order of floats as unsigned integers.
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x);
-  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+  return min(b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u), 0xfffffffeu);  // (a NaN's is cut)
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -383,6 +383,7 @@ struct Scorer<D, G, false> {
 };
 
 constexpr int kMaxCluster = 8;  // CTAs that share a unit
+constexpr int kHeld = 8;        // keys a lane holds where one warp finds the cut
 constexpr int kStages = 2;      // steps of 16 rows in a warp's ring (3 and 4: no faster)
 
 // One cluster of CTAs per (query row, KV head).  Each CTA scores an equal
@@ -541,6 +542,58 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
       }
     }
   }
+  // Few candidates: one warp holds their keys in registers and halves the
+  // range in which the cut lies until the keys from `mid` on are as many as
+  // wanted (or one value is left, shared by some that are not).
+  if (clusters == 1 && count <= 32 * kHeld) {
+    sync();
+    if (warp > 0) return;
+    uint32_t key[kHeld];
+    uint32_t low = 0xffffffffu, high = 0;
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) {
+      key[r] = 0;  // behind the last: never counted, mid is above the least key
+      if (r * 32 < count) {
+        const bool in = r * 32 + lane < count;
+        if (in) key[r] = s_key[r * 32 + lane];
+        low = min(low, in ? key[r] : 0xffffffffu);
+        high = max(high, key[r]);
+      }
+    }
+    low = __reduce_min_sync(0xffffffffu, low);  // more than wanted are >= low
+    high = __reduce_max_sync(0xffffffffu, high) + 1;  // fewer are >= high
+    uint32_t over = 0;  // keys >= high
+    while (high - low > 1) {
+      const uint32_t mid = low + (high - low) / 2;
+      uint32_t n = 0;
+#pragma unroll
+      for (int r = 0; r < kHeld; ++r)
+        if (r * 32 < count) n += key[r] >= mid;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (n > want) {
+        low = mid;
+      } else {
+        high = mid;
+        over = n;
+        if (n == want) break;
+      }
+    }
+    uint32_t ties = want - over;  // of the keys equal to low, the first ones
+    int at = first;
+    const uint32_t before = (1u << lane) - 1;
+#pragma unroll
+    for (int r = 0; r < kHeld; ++r) {
+      if (r * 32 >= count) break;
+      const uint32_t equal = __ballot_sync(0xffffffffu, r * 32 + lane < count && key[r] == low);
+      const bool take = key[r] >= high || ((equal >> lane & 1) && __popc(equal & before) < ties);
+      const uint32_t taken = __ballot_sync(0xffffffffu, take);
+      if (take) out[at + __popc(taken & before)] = first + r * 32 + lane;
+      at += __popc(taken);
+      ties -= min(ties, (uint32_t)__popc(equal));
+    }
+    return;
+  }
+
   kmin = __reduce_min_sync(0xffffffffu, kmin);
   kmax = __reduce_max_sync(0xffffffffu, kmax);
   if constexpr (NT > 32) {
@@ -713,21 +766,24 @@ cudaError_t launch_select_nt(const SelectParams& p, int c, cudaStream_t stream) 
 }
 
 // CTAs per unit and threads per CTA (us at 128 channels, 16-token blocks):
-//  - few units share theirs among up to 8 CTAs while that leaves each 256
-//    blocks and at most two to an SM: 16 units of 4000 blocks 30.4 alone,
-//    12.0 by 8; 64 of 2000 18.0, 12.4 by 4; 128 of 500 8.0, 9.5 by 2;
+//  - few units share theirs among up to 8 CTAs while that leaves each 100
+//    blocks and one to an SM, or 256 blocks and two to an SM: 16 units of 4000
+//    blocks 33.1 alone, 11.3 by 8; 16 of 500 7.7, 6.5 by 4; 64 of 2000 18.9,
+//    12.1 by 4, 18.4 by 8; 128 of 500 8.2, 9.1 by 2;
 //  - a unit's chain of waits is shortest with 8 warps, while all fit: 256
-//    units of 180 blocks 6.5 with 256 threads, 7.1 with 128; 512 of 180 11.9
-//    and 8.9; 1024 of 180 19.2, 13.7, and 12.7 with 64;
+//    units of 180 blocks 6.6 with 256 threads, 7.0 with 128; 512 of 180 10.8
+//    and 8.6; 1024 of 180 19.6, 13.3, and 12.7 with 64;
 //  - with more than 8 to an SM and few query heads a warp each is best, as
 //    long as many keep their keys on an SM: 8192 units of 180 blocks, one
-//    query head, 73 with 64 threads, 57 with 32 (four query heads, 2048
-//    units: 24 and 28).
+//    query head, 63.0 with 64 threads, 56.6 with 32 (four query heads, 2048
+//    units: 23.3 and 27.6).
 template <int D, int G>
 cudaError_t launch_select(const SelectParams& p, int num_sms, cudaStream_t stream) {
   const int64_t units = (int64_t)p.num_rows * p.num_kv_heads;
   int c = 1;
-  while (c < kMaxCluster && units * 2 * c <= 2 * num_sms && p.max_blocks / (2 * c) >= 256) c *= 2;
+  while (c < kMaxCluster && units * 2 * c <= 2 * num_sms &&
+         p.max_blocks / (2 * c) >= (units * 2 * c <= num_sms ? 100 : 256))
+    c *= 2;
   while (c < kMaxCluster && p.max_blocks > c * (kSelectMaxBlocks / kMaxCluster)) c *= 2;
   if (c > 1 || units <= 2 * num_sms) return launch_select_nt<D, G, 256>(p, c, stream);
   if (units <= 4 * num_sms || p.max_blocks > 4096) return launch_select_nt<D, G, 128>(p, c, stream);

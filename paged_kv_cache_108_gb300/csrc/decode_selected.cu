@@ -127,8 +127,8 @@ struct Cfg {
   static constexpr int kTile = kChunk * kRow;  // K (or V) bytes of a chunk
   // A warp's stage is 8 KB of bf16 or 4 KB of e4m3 (D = 128), and e4m3 has
   // twice the instructions a byte, so twice the warps to hide them behind
-  // (8 rows of 8192 tokens: 34.8 us with 4 warps of 3 stages, 28.5 with 8 of
-  // 2; 64 rows of 1024 tokens in bf16: 46.4 with 4 of 3, 56.8 with 8 of 2).
+  // (8 rows of 8192 tokens: 33.3 us with 4 warps of 3 stages, 28.4 with 8 of
+  // 2; 64 rows of 1024 tokens in bf16: 46.5 with 4 of 3, 56.1 with 8 of 2).
   static constexpr int kWarps = FP8 ? 8 : 4;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = FP8 ? 2 : 3;
@@ -510,12 +510,12 @@ cudaError_t launch_one(const SelectedParams& p, int num_sms, cudaStream_t stream
   const int64_t units = (int64_t)p.num_rows * p.num_kv_heads;
   const int64_t tokens = (int64_t)p.top << p.log2_block_size;  // of a unit, at most
   // CTAs per unit: as many as run at two to an SM, while each has a chunk for
-  // every warp (8 rows of 8 heads, 8192 tokens each in e4m3: 55.6 us with 1,
-  // 32.9 with 2, 28.5 with 4, and 41.5 with 5, which no longer run at once)
+  // every warp (8 rows of 8 heads, 8192 tokens each in e4m3: 51.9 us with 1,
+  // 31.1 with 2, 28.4 with 4, and 40.7 with 5, which no longer run at once).
   // Up to 8, and 12 where these few units' lists leave each CTA four chunks a
   // warp and the SMs are not yet full (one row of 8 heads in bf16: 2048 blocks
-  // 57.1 us with 8, 40.9 with 12, 63.5 with 16; 256 blocks 11.2, 10.0, 9.5; 64
-  // blocks 6.0, 6.5; 4 rows of 256 blocks 16.4, 25.1).
+  // 58.0 us with 8, 41.5 with 12, 63.6 with 16; 256 blocks 10.1, 8.6, 7.9; 64
+  // blocks 5.1, 5.2, 5.1; 4 rows of 256 blocks 15.5, 22.2, 27.2).
   const int64_t chunks = tokens / (kChunk * C::kWarps);  // for every warp of a CTA
   const bool large = units * kLargeCluster <= 3 * num_sms / 2 && chunks >= 4 * kLargeCluster;
   int64_t c = 2 * num_sms / units;
