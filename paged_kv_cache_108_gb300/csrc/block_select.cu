@@ -552,13 +552,11 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
     uint32_t low = 0xffffffffu, high = 0;
 #pragma unroll
     for (int r = 0; r < kHeld; ++r) {
-      key[r] = 0;  // behind the last: never counted, mid is above the least key
-      if (r * 32 < count) {
-        const bool in = r * 32 + lane < count;
-        if (in) key[r] = s_key[r * 32 + lane];
-        low = min(low, in ? key[r] : 0xffffffffu);
-        high = max(high, key[r]);
-      }
+      // behind the last 0: never counted, mid is above the least key
+      const bool in = r * 32 + lane < count;
+      key[r] = in ? s_key[r * 32 + lane] : 0u;
+      low = min(low, in ? key[r] : 0xffffffffu);
+      high = max(high, key[r]);
     }
     low = __reduce_min_sync(0xffffffffu, low);  // more than wanted are >= low
     high = __reduce_max_sync(0xffffffffu, high) + 1;  // fewer are >= high
@@ -567,8 +565,7 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
       const uint32_t mid = low + (high - low) / 2;
       uint32_t n = 0;
 #pragma unroll
-      for (int r = 0; r < kHeld; ++r)
-        if (r * 32 < count) n += key[r] >= mid;
+      for (int r = 0; r < kHeld; ++r) n += key[r] >= mid;
       n = __reduce_add_sync(0xffffffffu, n);
       if (n > want) {
         low = mid;
@@ -583,7 +580,6 @@ __global__ void __launch_bounds__(NT, NT == 32 ? 24 : 1)
     const uint32_t before = (1u << lane) - 1;
 #pragma unroll
     for (int r = 0; r < kHeld; ++r) {
-      if (r * 32 >= count) break;
       const uint32_t equal = __ballot_sync(0xffffffffu, r * 32 + lane < count && key[r] == low);
       const bool take = key[r] >= high || ((equal >> lane & 1) && __popc(equal & before) < ties);
       const uint32_t taken = __ballot_sync(0xffffffffu, take);
