@@ -18,6 +18,7 @@ Tolerances, from the arithmetic (u = 2^-24, half a step of fp32):
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -332,6 +333,14 @@ def test_select_launch_shapes(G, rows, Hkv, blocks):
     _check_select(rng, lens, G, Hkv, 64, 16, 11, NB=211)
 
 
+def test_select_from_the_widest_table():
+    rng = np.random.default_rng(41)
+    _check_select(rng, [196608 * 16 - 5], 1, 1, 64, 16, 300, NB=500)
+    # a wide table of short rows, enough rows that a CTA is two warps
+    tables = rng.integers(0, 97, (700, 4000)).astype(np.int32)
+    _check_select(rng, [16 * (r % 30) + 3 for r in range(700)], 1, 1, 64, 16, 9, tables=tables)
+
+
 @pytest.mark.parametrize("rows,blocks", [(1, 4096), (70, 150)])
 def test_select_ties_go_to_the_lowest_index(rows, blocks):
     rng = np.random.default_rng(7)
@@ -476,6 +485,14 @@ def test_decode_selected_shared_by_a_cluster(rows, blocks, top, kv):
     rng = np.random.default_rng(blocks)
     lens = [blocks * 16 - 5 - 9 * r for r in range(rows)]
     _check_attend(rng, lens, _lists(rng, lens, 2, 16, top), 4, 2, 128, 16, kv)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("B,rows,G", [(1, 2, 4), (4, 1, 8), (2, 7, 1)])
+def test_decode_selected_longest_lists(B, rows, G, kv):
+    rng = np.random.default_rng(42)
+    lens = [4500 * B - 3 * r for r in range(rows)]
+    _check_attend(rng, lens, _lists(rng, lens, 1, B, 4096), G, 1, 64, B, kv)
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
@@ -731,6 +748,34 @@ def test_two_batches_on_two_streams():
                 s.run()
         torch.cuda.synchronize()
         a.check(), b.check()
+
+
+def test_two_host_threads():
+    steps = [_Step("bf16", seed=6), _Step("fp8", seed=7)]
+    for s in steps:
+        s.stage()
+        s.run()
+    torch.cuda.synchronize()
+    want = [(s.q.clone(), s.sel.clone(), s.out.clone()) for s in steps]
+    failed = []
+
+    def work(s, w):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(200):
+                    s.run()
+                torch.cuda.current_stream().synchronize()
+            for got, ref in zip((s.q, s.sel, s.out), w):
+                assert torch.equal(got, ref)
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=x) for x in zip(steps, want)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not failed, failed
+    for s in steps:
+        s.check()
 
 
 def test_selection_finds_the_block_that_matters():
