@@ -20,10 +20,15 @@
 // operand layout by movmatrix.  With G <= 4 the columns 4..7 repeat the
 // heads of columns 0..3 and carry what rounding takes from P (p - round(p)),
 // so P V keeps about 16 bits of P at no cost; with G = 8 a second MMA does.
+// (The sum of the weights is of P before that rounding; 2^-17 of a weight is
+// far below the outputs' half step, 2^-9.)
 // An e4m3 cache is widened to f16 in registers (exact); q then enters in f16
 // under a power-of-two scale per head that puts its largest channel in
 // [1, 2) (f16 keeps 11 bits, bf16 q has 8, so channels down to 2^-16 of the
-// largest stay exact).
+// largest stay exact).  f16 ends at 2^-24, so its P is 2^14 2^(s - m), below
+// its largest value 65504: what is lost of a weight is below 2^-39 of the
+// largest, and 2^22 listed tokens lose less than 2^-17 together (2^(s - m)
+// itself would drop each weight below 2^-25, 2^-3 together).
 // The warps' results meet in shared memory, those of the CTAs that share a
 // (row, KV head) in a cluster's distributed shared memory: no workspace, no
 // second kernel, and sums in a fixed order.
@@ -380,9 +385,10 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads)
       m0 = n0;
       m1 = n1;
     }
+    constexpr float kRaise = FP8 ? 16384.f : 1.f;  // the factor that P and its sum carry
     const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-    const float p00 = fast_exp2(x00 - z0), p01 = fast_exp2(x01 - z1);
-    const float p10 = fast_exp2(x10 - z0), p11 = fast_exp2(x11 - z1);
+    const float p00 = fast_exp2(x00 - z0) * kRaise, p01 = fast_exp2(x01 - z1) * kRaise;
+    const float p10 = fast_exp2(x10 - z0) * kRaise, p11 = fast_exp2(x11 - z1) * kRaise;
     l0 += p00 + p10;
     l1 += p01 + p11;
     uint32_t hi0 = pack2<FP8>(p00, p01), hi1 = pack2<FP8>(p10, p11);

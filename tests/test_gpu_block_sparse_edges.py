@@ -1,0 +1,42 @@
+"""Block-sparse decode step on a GPU: values at the ends of their range, sizes
+at the ends of theirs, and how tensors' memory is written.
+
+Tolerances are those derived in test_gpu_block_sparse.py; where bits have to
+be equal the test says so.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_sparse as bs
+from paged_kv_cache_108_gb300 import ops
+from tests.test_gpu_block_sparse import DEV, _dev, _np
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------- decode_selected
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("G,top", [(1, 70), (4, 70), (8, 70), (4, 3)])
+def test_weights_far_below_the_largest_count(G, top, kv):
+    # The first token outweighs each of the others by up to 2^26 and has a zero
+    # value, so that the output is what the others add up to.
+    B, d, n = 16, 64, 16 * top - 5
+    q = torch.zeros(1, G, d, device=DEV, dtype=torch.bfloat16)
+    q[0, :, 0] = torch.linspace(0.75, 1.0, G, device=DEV).to(torch.bfloat16)
+    k = torch.zeros(top, B, 1, d, device=DEV)
+    k[0, 0, 0, 0] = 1.0
+    v = torch.ones(top, B, 1, d, device=DEV)
+    v[:, :, 0, 1::2] = 0.5
+    v[0, 0] = 0.0
+    kc, vc = ((x.to(torch.bfloat16) if kv == "bf16" else x.to(torch.float8_e4m3fn).view(torch.uint8))
+              for x in (k, v))
+    one = None if kv == "bf16" else _dev([1.0], torch.float32)
+    table, sel = _dev(np.arange(top)[None]), _dev(np.arange(top)[None, None])
+    scale = 26 * float(np.log(2.0))
+    out = torch.empty_like(q)
+    ops.decode_selected(out, q, kc, vc, table, _dev([n]), sel, scale, one, one)
+    want, mag = bs.decode_selected(_np(q)[0], _np(k), _np(v), np.arange(top), n, sel[0].cpu().numpy(), scale)
+    assert want.min() > 0.4 * (n - 1) * 2.0 ** -26
+    assert (np.abs(_np(out)[0] - want) <= 2 ** -8 * np.abs(want) + 2 ** -11 * mag).all()
