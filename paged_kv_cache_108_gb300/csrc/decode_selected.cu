@@ -120,9 +120,11 @@ __device__ __forceinline__ void store_peer(float* own, uint32_t rank, float v) {
 __device__ __forceinline__ float weight(float m, float whole) {
   return whole == -INFINITY ? 1.f : fast_exp2(m - whole);
 }
-// o / l, and zero for a row without tokens.
-__device__ __forceinline__ __nv_bfloat16 quotient(float o, float l) {
-  return __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+// (o / l) scale, and zero for a row without tokens.  The division first: o is
+// a sum over up to 2^22 tokens, and scale may bring it past the largest float
+// where the result is in range.
+__device__ __forceinline__ __nv_bfloat16 quotient(float o, float l, float scale) {
+  return __float2bfloat16_rn(l == 0.f ? 0.f : o / l * scale);
 }
 
 template <int D, bool FP8>
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads)
       l += a * ml[(w * 8 + h) * 2 + 1];
     }
     if (clusters == 1) {
-      p.out[(int64_t)unit * G * D + i] = quotient(acc * v_scale, l);
+      p.out[(int64_t)unit * G * D + i] = quotient(acc, l, v_scale);
     } else {
       const int owner = i / share;
       store_peer(&s_part[rank * share + i - owner * share], owner, acc);
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads)
       acc += a * s_part[r * share + i];
       l += a * s_state[r][h][1];
     }
-    p.out[(int64_t)unit * G * D + o] = quotient(acc * v_scale, l);
+    p.out[(int64_t)unit * G * D + o] = quotient(acc, l, v_scale);
   }
 }
 

@@ -10,7 +10,7 @@ import torch
 
 from oracle import block_sparse as bs
 from paged_kv_cache_108_gb300 import ops
-from tests.test_gpu_block_sparse import DEV, _dev, _np
+from tests.test_gpu_block_sparse import DEV, _bf16, _dev, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,19 @@ def test_weights_far_below_the_largest_count(G, top, kv):
     want, mag = bs.decode_selected(_np(q)[0], _np(k), _np(v), np.arange(top), n, sel[0].cpu().numpy(), scale)
     assert want.min() > 0.4 * (n - 1) * 2.0 ** -26
     assert (np.abs(_np(out)[0] - want) <= 2 ** -8 * np.abs(want) + 2 ** -11 * mag).all()
+
+
+@pytest.mark.parametrize("rows", [1, 80])
+def test_value_scales_near_the_ends_of_fp32(rows):
+    # the result is in range although the sum of the values under the scale is not
+    B, d, top = 16, 64, 64
+    rng = np.random.default_rng(53)
+    q = _bf16(rng, rows, 4, d)
+    codes = torch.full((top, B, 2, d), 448.0, device=DEV).to(torch.float8_e4m3fn).view(torch.uint8)
+    table, sel = _dev(np.tile(np.arange(top), (rows, 1))), _dev(np.tile(np.arange(top), (rows, 2, 1)))
+    for e in (112, -120):
+        out = torch.empty_like(q)
+        ops.decode_selected(out, q, codes, codes, table, _dev([B * top] * rows), sel, 1e-3,
+                            _dev([1e-3], torch.float32), _dev([2.0 ** e], torch.float32))
+        want = 448.0 * 2.0 ** e  # the mean of equal values; the weights' errors cancel but for 2^-11
+        assert (np.abs(_np(out) - want) <= (2 ** -8 + 2 ** -11) * want).all()
