@@ -50,14 +50,16 @@ __device__ __forceinline__ int axis_of_pair(const RopeParams& p, int i) {
   return a;
 }
 
+// Stores a piece: rounded from f, or, for a bf16 destination whose channels
+// are not rotated, as it was loaded, so that a NaN keeps its bits.
 __device__ __forceinline__ void store_piece(void* cache, int64_t elem, const float* f, bool fp8,
-                                            float scale) {
+                                            float scale, const uint4& loaded, bool rotated) {
   if (!fp8) {
     uint4 w;
-    w.x = pack_bf16x2_rn(f[0], f[1]);
-    w.y = pack_bf16x2_rn(f[2], f[3]);
-    w.z = pack_bf16x2_rn(f[4], f[5]);
-    w.w = pack_bf16x2_rn(f[6], f[7]);
+    w.x = rotated ? pack_bf16x2_rn(f[0], f[1]) : loaded.x;
+    w.y = rotated ? pack_bf16x2_rn(f[2], f[3]) : loaded.y;
+    w.z = rotated ? pack_bf16x2_rn(f[4], f[5]) : loaded.z;
+    w.w = rotated ? pack_bf16x2_rn(f[6], f[7]) : loaded.w;
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + elem) = w;
   } else {
     uint32_t h[4];
@@ -148,7 +150,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
       float x[8], y[8];
       Unpack16<false>::run(a[u], x);
       Unpack16<false>::run(b[u], y);
-      if (h < v0 && turned) {
+      const bool turns = h < v0 && turned;
+      if (turns) {
         const float4* cs = reinterpret_cast<const float4*>(&s_cs[t][8 * c]);
         if (p.adjacent) {
 #pragma unroll
@@ -170,8 +173,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
       }
       if (h < kv0) {
         const int64_t row = ((tok0 + t) * kv0 + h) * D;
-        store_piece(p.q_out, row + e0, x, false, 1.f);
-        store_piece(p.q_out, row + e1, y, false, 1.f);
+        store_piece(p.q_out, row + e0, x, false, 1.f, a[u], turns);
+        store_piece(p.q_out, row + e1, y, false, 1.f, b[u], turns);
       } else {
         const int slot = s_slot[t];
         if (slot < 0 || slot >= p.num_slots) continue;  // padding token or bad slot
@@ -179,8 +182,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
         const int64_t row = ((int64_t)slot * p.num_kv_heads + h - (is_v ? v0 : kv0)) * D;
         void* cache = is_v ? p.v_cache : p.k_cache;
         const float scale = is_v ? vs : ks;
-        store_piece(cache, row + e0, x, FP8, scale);
-        store_piece(cache, row + e1, y, FP8, scale);
+        store_piece(cache, row + e0, x, FP8, scale, a[u], turns);
+        store_piece(cache, row + e1, y, FP8, scale, b[u], turns);
       }
     }
   }

@@ -10,7 +10,7 @@ import torch
 
 from oracle import block_sparse as bs
 from paged_kv_cache_108_gb300 import ops
-from tests.test_gpu_block_sparse import DEV, _bf16, _dev, _np
+from tests.test_gpu_block_sparse import DEV, _bf16, _dev, _np, _rope_case, _rope_run
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +56,29 @@ def test_value_scales_near_the_ends_of_fp32(rows):
                             _dev([1e-3], torch.float32), _dev([2.0 ** e], torch.float32))
         want = 448.0 * 2.0 ** e  # the mean of equal values; the weights' errors cancel but for 2^-11
         assert (np.abs(_np(out) - want) <= (2 ** -8 + 2 ** -11) * want).all()
+
+
+# ------------------------------------------------------------ rope_and_cache
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("tokens,H,Hkv,d,rot,adjacent", [(41, 4, 2, 64, 32, False), (41, 8, 2, 128, 48, True),
+                                                        (2500, 16, 4, 128, 64, False), (2501, 6, 3, 64, 16, True)])
+def test_what_is_not_rotated_keeps_its_bits(tokens, H, Hkv, d, rot, adjacent, kv):
+    # values, and the channels from rot_dim on, NaN of every kind among them
+    c = _rope_case(tokens, H, Hkv, d, rot, None, False, adjacent, kv, seed=54)
+    rng = np.random.default_rng(55)
+    bits = lambda t: t.view(torch.int16)  # noqa: E731
+    for name, first in (("q", rot), ("k", rot), ("v", 0)):
+        t = c[name] = c[name].contiguous()
+        odd = torch.from_numpy(rng.integers(-2 ** 15, 2 ** 15, t[..., first:].shape).astype(np.int16)).to(DEV)
+        odd[:, :, ::5] = torch.from_numpy(rng.choice(np.array([0x7f81, 0x7fff, -1, -127, 0x7f80, -128, -32768, 1], np.int16),
+                                                     tuple(odd[:, :, ::5].shape))).to(DEV)
+        bits(t)[..., first:] = odd
+    kc, vc = c["kc"].clone(), c["vc"].clone()
+    out = _rope_run(c)
+    assert torch.equal(bits(out)[..., rot:], bits(c["q"])[..., rot:])
+    ops.reshape_and_cache(c["k"], c["v"], kc, vc, _dev(c["slots"]), c["ks"], c["vs"])  # the plain write
+    raw = lambda t: t.view(torch.uint8)  # noqa: E731
+    w = kc.element_size()
+    assert torch.equal(raw(c["vc"]), raw(vc))
+    assert torch.equal(raw(c["kc"])[..., rot * w:], raw(kc)[..., rot * w:])
