@@ -174,8 +174,10 @@ __global__ void __launch_bounds__(32 * kSumWarps, FP8 ? 2 : 4)
         ch[k] = cl[k] = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          ch[k] |= ((uint32_t)__float2int_ru(h[4 * k + i] * inv) & 255u) << (8 * i);
-          cl[k] |= ((uint32_t)__float2int_rd(l[4 * k + i] * inv) & 255u) << (8 * i);
+          // (the products too are rounded outward: exact but below the smallest
+          // float, where a tiny key beside a huge one would become 0)
+          ch[k] |= ((uint32_t)__float2int_ru(__fmul_ru(h[4 * k + i], inv)) & 255u) << (8 * i);
+          cl[k] |= ((uint32_t)__float2int_rd(__fmul_rd(l[4 * k + i], inv)) & 255u) << (8 * i);
         }
       }
       if (in) {

@@ -15,6 +15,28 @@ from tests.test_gpu_block_sparse import DEV, _bf16, _dev, _np, _rope_case, _rope
 pytestmark = pytest.mark.gpu
 
 
+# ---------------------------------------------------------- summarize_blocks
+
+def test_ranges_bound_tiny_keys_beside_huge_ones():
+    # k / u below the smallest float must still round outward
+    rng = np.random.default_rng(50)
+    B, Hkv, d = 16, 2, 128
+    k = torch.zeros(4, B, Hkv, d, dtype=torch.float32)
+    k[:, :, :, 0] = torch.tensor([2.0 ** 23, 2.0 ** 30, 2.0 ** 50, 2.0 ** 60])[:, None, None]
+    tiny = 2.0 ** rng.integers(-133, -100, (4, B, Hkv, 40)) * rng.choice([-1.0, 1.0], (4, 1, Hkv, 40))
+    k[:, :, :, 1:41] = torch.from_numpy(tiny).float()
+    kc = k.to(DEV).to(torch.bfloat16)
+    values = _np(kc)
+    assert (values[:, :, :, 1:41] == tiny).all()  # bf16 holds them
+    codes, scales = ops.alloc_block_ranges(kc)
+    ops.summarize_blocks(kc, _dev(np.arange(4) * B + B - 1), codes, scales)
+    for b in range(4):
+        want, u = bs.block_range(values[b])
+        assert np.array_equal(scales[b].cpu().numpy(), u)
+        assert np.array_equal(codes[b].cpu().numpy(), want)
+        assert set(np.abs(want[:, :, 1:41]).max(1).ravel()) == {1}
+
+
 # ----------------------------------------------------------- decode_selected
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
