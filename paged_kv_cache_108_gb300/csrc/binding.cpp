@@ -81,15 +81,22 @@ class OnDevice {
       throw Refused(std::string(name) + " must have dtype " + c10::toString(type) + ", got " +
                     c10::toString(t.scalar_type()));
   }
+  // What a call reads.
   template <typename T = void>
-  T* ptr(const at::Tensor& t, const char* name, at::ScalarType type) const {
-    check(t, name, type);
-    if (!t.is_contiguous()) throw Refused(std::string(name) + " must be contiguous");
-    return static_cast<T*>(const_cast<void*>(t.const_data_ptr()));
+  const T* in(const at::Tensor& t, const char* name, at::ScalarType type) const {
+    whole(t, name, type);
+    return static_cast<const T*>(t.const_data_ptr());
   }
   template <typename T = void>
-  T* optional(PyObject* o, const char* name, at::ScalarType type) const {
-    return o == Py_None ? nullptr : ptr<T>(tensor(o, name), name, type);
+  const T* optional(PyObject* o, const char* name, at::ScalarType type) const {
+    return o == Py_None ? nullptr : in<T>(tensor(o, name), name, type);
+  }
+  // What a call writes: a lazy clone gets memory of its own here, so these
+  // are taken before the addresses of inputs, which may be views of them.
+  template <typename T = void>
+  T* out(const at::Tensor& t, const char* name, at::ScalarType type) const {
+    whole(t, name, type);
+    return static_cast<T*>(t.mutable_data_ptr());
   }
   // Rows [heads, d] of a [tokens, heads, d] tensor whose tokens may lie apart.
   const void* rows(const at::Tensor& t, const char* name, int64_t* stride) const {
@@ -126,6 +133,10 @@ class OnDevice {
   }
 
  private:
+  void whole(const at::Tensor& t, const char* name, at::ScalarType type) const {
+    check(t, name, type);
+    if (!t.is_contiguous()) throw Refused(std::string(name) + " must be contiguous");
+  }
   c10::DeviceIndex device_;
 };
 
@@ -266,16 +277,16 @@ PyObject* rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     rope.sections_in_turn = flag(a[12], "sections_in_turn");
     rope.adjacent_pairs = flag(a[13], "adjacent_pairs");
     const OnDevice on(kc, "k_cache");
+    void* o = on.out(q_out, "q_out", at::kBFloat16);
+    void *kp = on.out(kc, "k_cache", kc.scalar_type()), *vp = on.out(vc, "v_cache", kc.scalar_type());
     int64_t q_stride, k_stride, v_stride;
     const void *q = on.rows(query, "query", &q_stride), *k = on.rows(key, "key", &k_stride),
                *v = on.rows(value, "value", &v_stride);
-    void* o = on.ptr(q_out, "q_out", at::kBFloat16);
-    void *kp = on.ptr(kc, "k_cache", kc.scalar_type()), *vp = on.ptr(vc, "v_cache", kc.scalar_type());
-    const auto* sp = on.ptr<const int32_t>(slots, "slot_mapping", at::kInt);
-    const auto* pp = on.ptr<const int32_t>(pos, "positions", at::kInt);
-    const auto* cs = on.ptr<const float>(table, "cos_sin", at::kFloat);
-    const auto* ks = on.optional<const float>(a[9], "k_scale", at::kFloat);
-    const auto* vs = on.optional<const float>(a[10], "v_scale", at::kFloat);
+    const auto* sp = on.in<int32_t>(slots, "slot_mapping", at::kInt);
+    const auto* pp = on.in<int32_t>(pos, "positions", at::kInt);
+    const auto* cs = on.in<float>(table, "cos_sin", at::kFloat);
+    const auto* ks = on.optional<float>(a[9], "k_scale", at::kFloat);
+    const auto* vs = on.optional<float>(a[10], "v_scale", at::kFloat);
     const int32_t heads = to_int32(qs[1], "num_heads"), tokens = to_int32(n, "num_tokens");
     return on.run(a[14], [&](pa_stream_t stream) {
       return pa_rope_and_cache(o, q, q_stride, heads, k, k_stride, v, v_stride, kp, vp, d, sp, pp,
@@ -292,10 +303,10 @@ PyObject* summarize_blocks(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const pa_cache_desc d = describe(kc);
     check_ranges(d, codes, scales);
     const OnDevice on(kc, "k_cache");
-    const void* kp = on.ptr(kc, "k_cache", kc.scalar_type());
-    const auto* sp = on.ptr<const int32_t>(slots, "slot_mapping", at::kInt);
-    auto* cp = on.ptr<int8_t>(codes, "codes", at::kChar);
-    auto* up = on.ptr<float>(scales, "scales", at::kFloat);
+    auto* cp = on.out<int8_t>(codes, "codes", at::kChar);
+    auto* up = on.out<float>(scales, "scales", at::kFloat);
+    const void* kp = on.in(kc, "k_cache", kc.scalar_type());
+    const auto* sp = on.in<int32_t>(slots, "slot_mapping", at::kInt);
     const int32_t tokens = to_int32(slots.numel(), "num_tokens");
     return on.run(a[4], [&](pa_stream_t stream) {
       return pa_summarize_blocks(kp, d, sp, tokens, cp, up, stream);
@@ -320,13 +331,13 @@ PyObject* select_blocks(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     const Rows r = check_rows(q, tables, lens, a[9], selected, d);
     const int32_t sink = integer(a[7], "sink"), recent = integer(a[8], "recent");
     const OnDevice on(codes, "codes");
-    auto* out = on.ptr<int32_t>(selected, "selected", at::kInt);
-    const void* qp = on.ptr(q, "q", at::kBFloat16);
-    const auto* cp = on.ptr<const int8_t>(codes, "codes", at::kChar);
-    const auto* up = on.ptr<const float>(scales, "scales", at::kFloat);
-    const auto* tp = on.ptr<const int32_t>(tables, "block_tables", at::kInt);
-    const auto* lp = on.ptr<const int32_t>(lens, "context_lens", at::kInt);
-    const auto* rp = on.optional<const int32_t>(a[9], "row_seqs", at::kInt);
+    auto* out = on.out<int32_t>(selected, "selected", at::kInt);
+    const void* qp = on.in(q, "q", at::kBFloat16);
+    const auto* cp = on.in<int8_t>(codes, "codes", at::kChar);
+    const auto* up = on.in<float>(scales, "scales", at::kFloat);
+    const auto* tp = on.in<int32_t>(tables, "block_tables", at::kInt);
+    const auto* lp = on.in<int32_t>(lens, "context_lens", at::kInt);
+    const auto* rp = on.optional<int32_t>(a[9], "row_seqs", at::kInt);
     return on.run(a[10], [&](pa_stream_t stream) {
       return pa_select_blocks(out, qp, cp, up, d, tp, r.max_blocks, lp, rp, r.rows, r.seqs,
                               r.heads, r.top, sink, recent, stream);
@@ -352,16 +363,16 @@ PyObject* decode_selected(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       throw Refused("scale must be a number");
     }
     const OnDevice on(kc, "k_cache");
-    void* op = on.ptr(out, "out", at::kBFloat16);
-    const void* qp = on.ptr(q, "q", at::kBFloat16);
-    const void *kp = on.ptr(kc, "k_cache", kc.scalar_type()),
-               *vp = on.ptr(vc, "v_cache", kc.scalar_type());
-    const auto* tp = on.ptr<const int32_t>(tables, "block_tables", at::kInt);
-    const auto* lp = on.ptr<const int32_t>(lens, "context_lens", at::kInt);
-    const auto* sp = on.ptr<const int32_t>(selected, "selected", at::kInt);
-    const auto* ks = on.optional<const float>(a[8], "k_scale", at::kFloat);
-    const auto* vs = on.optional<const float>(a[9], "v_scale", at::kFloat);
-    const auto* rp = on.optional<const int32_t>(a[10], "row_seqs", at::kInt);
+    void* op = on.out(out, "out", at::kBFloat16);
+    const void* qp = on.in(q, "q", at::kBFloat16);
+    const void *kp = on.in(kc, "k_cache", kc.scalar_type()),
+               *vp = on.in(vc, "v_cache", kc.scalar_type());
+    const auto* tp = on.in<int32_t>(tables, "block_tables", at::kInt);
+    const auto* lp = on.in<int32_t>(lens, "context_lens", at::kInt);
+    const auto* sp = on.in<int32_t>(selected, "selected", at::kInt);
+    const auto* ks = on.optional<float>(a[8], "k_scale", at::kFloat);
+    const auto* vs = on.optional<float>(a[9], "v_scale", at::kFloat);
+    const auto* rp = on.optional<int32_t>(a[10], "row_seqs", at::kInt);
     return on.run(a[11], [&](pa_stream_t stream) {
       return pa_decode_selected(op, qp, kp, vp, d, tp, r.max_blocks, lp, rp, sp, r.rows, r.seqs,
                                 r.heads, r.top, (float)scale, ks, vs, stream);

@@ -104,3 +104,47 @@ def test_what_is_not_rotated_keeps_its_bits(tokens, H, Hkv, d, rot, adjacent, kv
     w = kc.element_size()
     assert torch.equal(raw(c["vc"]), raw(vc))
     assert torch.equal(raw(c["kc"])[..., rot * w:], raw(kc)[..., rot * w:])
+
+
+# ----------------------------------------------------------- tensors' memory
+
+def test_outputs_that_are_lazy_clones_are_written_alone():
+    # a tensor that shares its memory until it is written: the other keeps what it held
+    rng = np.random.default_rng(56)
+    c = _rope_case(40, 4, 2, 64, 32, None, False, False, "bf16", seed=57)
+    shared = {x: c[x].clone() for x in ("kc", "vc")}
+    kept = {x: t.clone() for x, t in shared.items()}
+    want_q = _rope_run(c)
+    k_want, v_want = c["kc"], c["vc"]
+    c["kc"], c["vc"] = (torch._lazy_clone(shared[x]) for x in ("kc", "vc"))
+    base = torch.full_like(want_q, 3.0)
+    out = torch._lazy_clone(base)
+    _rope_run(c, out=out)
+    same = lambda a, b: torch.equal(a.view(torch.uint8), b.view(torch.uint8))  # noqa: E731
+    assert same(out, want_q) and same(c["kc"], k_want) and same(c["vc"], v_want)
+    assert (base == 3.0).all() and all(same(shared[x], kept[x]) for x in shared)
+    # in place on a lazy clone: the queries are its own
+    q0 = c["q"].contiguous()
+    q = torch._lazy_clone(q0)
+    before = q0.clone()
+    _rope_run(c, out=q, q=q)
+    assert same(q, want_q) and same(q0, before)
+
+    NB, B, top = 12, 16, 5
+    kc, vc = _bf16(rng, NB, B, 2, 64), _bf16(rng, NB, B, 2, 64)
+    codes0, scales0 = ops.alloc_block_ranges(kc)
+    codes, scales = torch._lazy_clone(codes0), torch._lazy_clone(scales0)
+    ops.summarize_blocks(kc, _dev(np.arange(NB) * B + B - 1), codes, scales)
+    assert (codes0 == 0).all() and (scales0 == 0).all() and (scales > 0).all()
+    q = _bf16(rng, 1, 4, 64)
+    table, lens = _dev(np.arange(NB)[None]), _dev([NB * B])
+    sel0 = torch.full((1, 2, top), -5, device=DEV, dtype=torch.int32)
+    sel = torch._lazy_clone(sel0)
+    ops.select_blocks(sel, q, codes, scales, table, lens, B)
+    assert (sel0 == -5).all() and (sel >= 0).all()
+    out0 = torch.full_like(q, 9.0)
+    out = torch._lazy_clone(out0)
+    ops.decode_selected(out, q, kc, vc, table, lens, sel, 0.125)
+    want, mag = bs.decode_selected(_np(q)[0], _np(kc), _np(vc), np.arange(NB), NB * B, sel[0].cpu().numpy(), 0.125)
+    assert (out0 == 9.0).all()
+    assert (np.abs(_np(out)[0] - want) <= 2 ** -8 * np.abs(want) + 2 ** -11 * mag).all()
