@@ -812,8 +812,9 @@ cudaError_t launch_summarize(const SummaryParams& p, cudaStream_t stream) {
   const unsigned groups = (unsigned)((p.num_tokens + per - 1) / per);
   const dim3 b(32 * kSumWarps);
   if (block < 64) {
-    const dim3 grid(groups, (unsigned)((columns * (per == 1 ? 1 : (32 + block - 1) / block) +
-                                        kSumWarps - 1) / kSumWarps));
+    // (a grid's y ends at 65535; CTAs stride over what is left)
+    const int y = (columns * (per == 1 ? 1 : (32 + block - 1) / block) + kSumWarps - 1) / kSumWarps;
+    const dim3 grid(groups, (unsigned)(y < 65535 ? y : 65535));
     return launch_dependent<summarize_kernel<D, FP8, 1>>(grid, b, 0, stream, 1, p, per);
   }
   return launch_dependent<summarize_kernel<D, FP8, 8>>(dim3(groups, (unsigned)columns), b, 0,

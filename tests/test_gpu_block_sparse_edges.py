@@ -37,6 +37,23 @@ def test_ranges_bound_tiny_keys_beside_huge_ones():
         assert set(np.abs(want[:, :, 1:41]).max(1).ravel()) == {1}
 
 
+@pytest.mark.parametrize("heads", [32767, 32768])
+def test_ranges_of_the_most_heads_and_the_smallest_blocks(heads):
+    rng = np.random.default_rng(51)
+    kc = _bf16(rng, 3, 1, heads, 128)
+    slots = np.full(1025, -1)
+    slots[[7, 1000, 1024]] = [2, 0, 1]
+    codes, scales = ops.alloc_block_ranges(kc)
+    ops.summarize_blocks(kc, _dev(slots), codes, scales)
+    some = [0, 1, 255, 256, 8191, heads // 2, heads - 257, heads - 2, heads - 1]
+    values = _np(kc[:, :, some])
+    for b in range(3):
+        want, u = bs.block_range(values[b])
+        assert np.array_equal(scales[b, some].cpu().numpy(), u)
+        assert np.array_equal(codes[b, some].cpu().numpy(), want)
+    assert (scales > 0).all()
+
+
 # ----------------------------------------------------------- decode_selected
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
