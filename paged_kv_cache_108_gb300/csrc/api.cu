@@ -914,7 +914,7 @@ pa_status pa_rope_and_cache(void* q_out, const void* query, int64_t q_stride, in
     const char* q0 = static_cast<const char*>(query);
     const char* o0 = static_cast<const char*>(q_out);
     const int64_t q_bytes = 2 * ((num_tokens - 1) * q_stride + q_row);
-    const int64_t o_bytes = 2 * num_tokens * q_row;
+    const int64_t o_bytes = 2 * (int64_t)num_tokens * q_row;
     if (o0 < q0 + q_bytes && q0 < o0 + o_bytes)
       return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: q_out overlaps query in another layout");
   }
