@@ -533,10 +533,11 @@ typedef struct {
  *
  *  q_out         device, [num_tokens, num_heads, head_dim] bf16, written.
  *                May be `query` itself if q_stride is num_heads * head_dim;
- *                must not overlap it otherwise.
+ *                must not overlap it otherwise, nor key, value or a cache
+ *                (PA_ERR_INVALID).
  *  query, key, value  device bf16; token t's [heads, head_dim] row starts
  *                q_stride / k_stride / v_stride elements after token t - 1's
- *                (multiples of 8, at least heads * head_dim; slices of one
+ *                (multiples of 8 from heads * head_dim to 2^40; slices of one
  *                projection's output qualify).  16-byte aligned.
  *  num_heads     query heads, from 0 (then q_out, query: NULL) up to
  *                num_heads + 2 num_kv_heads = 32768.

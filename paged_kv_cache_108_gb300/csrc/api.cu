@@ -32,6 +32,15 @@ int ilog2(int64_t x) {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether one of n rows of `row` bytes, `stride` apart from `base` on, meets
+// [o0, o1).
+bool rows_meet(const void* base, int64_t stride, int64_t row, int64_t n, const char* o0,
+               const char* o1) {
+  const int64_t b = reinterpret_cast<intptr_t>(base), lo = reinterpret_cast<intptr_t>(o0);
+  const int64_t t = lo < b + row ? 0 : (lo - b - row) / stride + 1;  // the first to end behind o0
+  return t < n && b + t * stride < reinterpret_cast<intptr_t>(o1);
+}
+
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -897,10 +906,13 @@ pa_status pa_rope_and_cache(void* q_out, const void* query, int64_t q_stride, in
   const int64_t kv_row = (int64_t)cache.num_kv_heads * cache.head_dim;
   if ((int64_t)num_heads + 2 * (int64_t)cache.num_kv_heads > 32768)
     return pa_fail(PA_ERR_UNSUPPORTED, "pa_rope_and_cache: more than 32768 heads in all");
-  if ((num_heads && (q_stride < q_row || q_stride % 8)) || k_stride < kv_row || k_stride % 8 ||
-      v_stride < kv_row || v_stride % 8)
+  constexpr int64_t kMaxStride = int64_t(1) << 40;  // addresses stay within 64 bits
+  if ((num_heads && (q_stride < q_row || q_stride % 8 || q_stride > kMaxStride)) ||
+      k_stride < kv_row || k_stride % 8 || k_stride > kMaxStride || v_stride < kv_row ||
+      v_stride % 8 || v_stride > kMaxStride)
     return pa_fail(PA_ERR_INVALID,
-                   "pa_rope_and_cache: strides must be multiples of 8 and hold a token's heads");
+                   "pa_rope_and_cache: strides must be multiples of 8, hold a token's heads and be "
+                   "at most 2^40");
   if (num_tokens == 0) return PA_OK;
   if ((num_heads && (!q_out || !query)) || !key || !value || !k_cache || !v_cache ||
       !slot_mapping || !positions || !cos_sin)
@@ -909,14 +921,20 @@ pa_status pa_rope_and_cache(void* q_out, const void* query, int64_t q_stride, in
       !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 4) ||
       !aligned(positions, 4) || !aligned(cos_sin, 4))
     return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: misaligned pointer");
-  if (num_heads && !(q_out == query && q_stride == q_row)) {
-    // another layout over the same bytes would be read after it is written
-    const char* q0 = static_cast<const char*>(query);
-    const char* o0 = static_cast<const char*>(q_out);
-    const int64_t q_bytes = 2 * ((num_tokens - 1) * q_stride + q_row);
-    const int64_t o_bytes = 2 * (int64_t)num_tokens * q_row;
-    if (o0 < q0 + q_bytes && q0 < o0 + o_bytes)
+  if (num_heads) {
+    // what is read after a part of q_out is written must lie elsewhere
+    const auto* o0 = static_cast<const char*>(q_out);
+    const char* o1 = o0 + 2 * (int64_t)num_tokens * q_row;
+    if (!(q_out == query && q_stride == q_row) &&
+        rows_meet(query, q_stride * 2, q_row * 2, num_tokens, o0, o1))
       return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: q_out overlaps query in another layout");
+    if (rows_meet(key, k_stride * 2, kv_row * 2, num_tokens, o0, o1) ||
+        rows_meet(value, v_stride * 2, kv_row * 2, num_tokens, o0, o1))
+      return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: q_out overlaps key or value");
+    const int64_t pool = (int64_t)cache.num_blocks * cache.block_size * kv_row *
+                         (cache.dtype == PA_KV_BF16 ? 2 : 1);
+    if (rows_meet(k_cache, pool, pool, 1, o0, o1) || rows_meet(v_cache, pool, pool, 1, o0, o1))
+      return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: q_out overlaps a cache");
   }
   pa::RopeParams p = {};
   p.q_out = static_cast<__nv_bfloat16*>(q_out);
