@@ -123,7 +123,7 @@ def lib():
         if _lib is None:
             if not os.path.exists(LIB_PATH):
                 from . import build as _build
-                _build.build()
+                _build.build_library()
             if not os.path.exists(LIB_PATH):
                 raise RuntimeError(f"libpa.so not found at {LIB_PATH}; run build()")
             handle = ctypes.CDLL(LIB_PATH)

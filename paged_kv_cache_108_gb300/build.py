@@ -3,8 +3,9 @@ _binding.so (csrc/binding.cpp, the compiled part of the torch binding).
 
 Each translation unit is compiled in parallel into _build/ at the repository
 root, then linked into paged_kv_cache_108_gb300/libpa.so (static CUDA runtime);
-_binding.so links against it and the installed torch.  A rebuild happens only
-when a source or header is newer than the libraries.
+_binding.so links against it and the installed torch, and is left out where
+there is none.  Each is rebuilt only when a source or header of its own is
+newer.
 Run ``python -m paged_kv_cache_108_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -36,11 +37,9 @@ def _nvcc() -> str:
     return cand
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch not found: the binding is compiled against its headers")
-    return spec.submodule_search_locations[0]
+    return spec.submodule_search_locations[0] if spec else None
 
 
 def sources():
@@ -49,19 +48,28 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + cpp)
 
 
-def _deps():
-    return [*sources(), BINDING_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
-        os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "pa.h"), __file__]
+def _newer_than_all(out: str, deps) -> bool:
+    if not os.path.exists(out):
+        return False
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def library_up_to_date() -> bool:
+    headers = [h for e in ("*.h", "*.cuh") for h in glob.glob(os.path.join(CSRC, e))]
+    return _newer_than_all(LIB, [*sources(), *headers, os.path.join(INCLUDE, "pa.h"), __file__])
+
+
+def binding_up_to_date() -> bool:
+    return _newer_than_all(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "pa.h"), __file__])
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and (binding_up_to_date() or _torch_dir() is None)
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
+    os.makedirs(BUILD, exist_ok=True)
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     if src.endswith(".cu"):
         cmd = [_nvcc(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -86,20 +94,44 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
-    """Compile and link libpa.so; returns its path."""
-    if not force and not verbose_ptxas and up_to_date():
+    """Build what is stale of libpa.so and, where torch is installed, of
+    _binding.so; returns libpa.so's path."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # the binding beside the library
+        obj = None
+        if _torch_dir() is not None and (force or not binding_up_to_date()):
+            obj = ex.submit(_compile, BINDING_SRC, False)
+        build_library(force, verbose_ptxas, jobs)
+        if obj is not None:
+            _link_binding(obj.result())
+    return LIB
+
+
+def build_library(force: bool = False, verbose_ptxas: bool = False,
+                  jobs: int | None = None) -> str:
+    """Compile and link libpa.so (needs the CUDA toolkit alone); returns its path."""
+    if not force and not verbose_ptxas and library_up_to_date():
         return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    srcs = [*sources(), BINDING_SRC]
+    srcs = sources()
     jobs = jobs or min(len(srcs), os.cpu_count() or 4)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        *objs, binding = ex.map(lambda s: _compile(s, verbose_ptxas), srcs)
+        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
     _link([_nvcc(), *ARCH, "-shared"], [*objs, "-lpthread"], LIB)
+    return LIB
+
+
+def build_binding() -> str:
+    """Compile _binding.so and link it against libpa.so, which it leaves as it is."""
+    if _torch_dir() is None:
+        raise RuntimeError("torch not found: the binding is compiled against its headers")
+    _link_binding(_compile(BINDING_SRC, False))
+    return BINDING
+
+
+def _link_binding(obj: str) -> None:
     torch_lib = os.path.join(_torch_dir(), "lib")
     _link(["g++", "-shared"],
-          [binding, "-L", PKG, "-l:libpa.so", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
+          [obj, "-L", PKG, "-l:libpa.so", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"], BINDING)
-    return LIB
 
 
 def _link(cmd, inputs, out: str) -> None:

@@ -1,0 +1,70 @@
+"""What build.py builds, with what is installed (compiler and linker faked)."""
+import os
+
+import pytest
+
+from paged_kv_cache_108_gb300 import build as b
+
+
+@pytest.fixture
+def made(tmp_path, monkeypatch):
+    """Outputs in a folder of their own; compiles and links are recorded."""
+    log = []
+    monkeypatch.setattr(b, "BUILD", str(tmp_path / "o"))
+    monkeypatch.setattr(b, "LIB", str(tmp_path / "libpa.so"))
+    monkeypatch.setattr(b, "BINDING", str(tmp_path / "_binding.so"))
+
+    def compile_(src, verbose):
+        log.append(("compile", os.path.basename(src)))
+        return src + ".o"
+
+    def link(cmd, inputs, out):
+        log.append(("link", os.path.basename(out)))
+        open(out, "w").close()
+
+    monkeypatch.setattr(b, "_compile", compile_)
+    monkeypatch.setattr(b, "_link", link)
+    return log
+
+
+def _without_torch(monkeypatch):
+    find = b.importlib.util.find_spec
+    monkeypatch.setattr(b.importlib.util, "find_spec", lambda n, *a: None if n == "torch" else find(n, *a))
+
+
+def test_the_library_is_built_without_torch(made, monkeypatch):
+    _without_torch(monkeypatch)
+    assert b.build() == b.LIB
+    assert ("link", "libpa.so") in made and ("compile", "binding.cpp") not in made
+    assert b.up_to_date()
+    with pytest.raises(RuntimeError, match="torch not found"):
+        b.build_binding()
+
+
+def test_a_binding_that_does_not_compile_leaves_the_library(made, monkeypatch):
+    compile_ = b._compile
+
+    def fails(src, verbose):
+        if src == b.BINDING_SRC:
+            raise RuntimeError("compile failed: no Python.h")
+        return compile_(src, verbose)
+
+    monkeypatch.setattr(b, "_compile", fails)
+    with pytest.raises(RuntimeError, match="Python.h"):
+        b.build()
+    assert os.path.exists(b.LIB) and not os.path.exists(b.BINDING)
+
+
+def test_each_is_built_when_it_is_stale(made):
+    b.build()
+    assert made[-1] == ("link", "_binding.so") and ("link", "libpa.so") in made
+    made.clear()
+    b.build()
+    assert not made
+    os.remove(b.BINDING)
+    b.build()
+    assert made == [("compile", "binding.cpp"), ("link", "_binding.so")]
+    made.clear()
+    os.remove(b.LIB)
+    b.build()
+    assert ("link", "libpa.so") in made and ("link", "_binding.so") not in made
