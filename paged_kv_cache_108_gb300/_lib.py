@@ -140,8 +140,8 @@ def binding():
     global _binding
     if _binding is None:
         lib()
-        if not os.path.exists(os.path.join(_HERE, "_binding.so")):
-            from . import build as _build
+        from . import build as _build
+        if not _build.binding_fits():  # another torch's or Python's layouts must not be loaded
             _build.build()
         import torch  # noqa: F401  (its libraries are what the binding links against)
 

@@ -5,7 +5,7 @@ Each translation unit is compiled in parallel into _build/ at the repository
 root, then linked into paged_kv_cache_108_gb300/libpa.so (static CUDA runtime);
 _binding.so links against it and the installed torch, and is left out where
 there is none.  Each is rebuilt only when a source or header of its own is
-newer.
+newer, the binding also when torch or Python is another than it was built for.
 Run ``python -m paged_kv_cache_108_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -14,6 +14,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -27,6 +28,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpa.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_binding.so")
+BUILT_FOR = os.path.join(PKG, "_binding.built_for")  # the torch and Python that BINDING is for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -40,6 +42,22 @@ def _nvcc() -> str:
 def _torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")
     return spec.submodule_search_locations[0] if spec else None
+
+
+def _built_for() -> str:
+    """The installed torch's version and this Python's ABI, by which the
+    layouts that the binding's code relies on go."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        version = re.search(r"__version__\s*=\s*['\"](.+?)['\"]", f.read())
+    return f"torch {version.group(1) if version else '?'} {sysconfig.get_config_var('SOABI')}\n"
+
+
+def binding_fits() -> bool:
+    """Whether there is a binding, built for this torch and Python."""
+    if _torch_dir() is None or not os.path.exists(BINDING) or not os.path.exists(BUILT_FOR):
+        return False
+    with open(BUILT_FOR) as f:
+        return f.read() == _built_for()
 
 
 def sources():
@@ -61,11 +79,12 @@ def library_up_to_date() -> bool:
 
 
 def binding_up_to_date() -> bool:
-    return _newer_than_all(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "pa.h"), __file__])
+    return (_newer_than_all(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "pa.h"), __file__])
+            and binding_fits())
 
 
 def up_to_date() -> bool:
-    return library_up_to_date() and (binding_up_to_date() or _torch_dir() is None)
+    return library_up_to_date() and (_torch_dir() is None or binding_up_to_date())
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
@@ -132,6 +151,8 @@ def _link_binding(obj: str) -> None:
     _link(["g++", "-shared"],
           [obj, "-L", PKG, "-l:libpa.so", "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_lib}"], BINDING)
+    with open(BUILT_FOR, "w") as f:
+        f.write(_built_for())
 
 
 def _link(cmd, inputs, out: str) -> None:

@@ -13,6 +13,7 @@ def made(tmp_path, monkeypatch):
     monkeypatch.setattr(b, "BUILD", str(tmp_path / "o"))
     monkeypatch.setattr(b, "LIB", str(tmp_path / "libpa.so"))
     monkeypatch.setattr(b, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(b, "BUILT_FOR", str(tmp_path / "_binding.built_for"), raising=False)
 
     def compile_(src, verbose):
         log.append(("compile", os.path.basename(src)))
@@ -68,3 +69,40 @@ def test_each_is_built_when_it_is_stale(made):
     os.remove(b.LIB)
     b.build()
     assert ("link", "libpa.so") in made and ("link", "_binding.so") not in made
+
+
+@pytest.mark.parametrize("what", ["torch", "python", "record"])
+def test_a_binding_for_another_torch_or_python_is_built_again(made, monkeypatch, what):
+    b.build()
+    assert b.binding_up_to_date() and b.binding_fits()
+    if what == "torch":
+        with open(b.BUILT_FOR) as f:
+            old = f.read()
+        with open(b.BUILT_FOR, "w") as f:
+            f.write(old.replace("torch ", "torch 1."))
+    elif what == "python":
+        monkeypatch.setattr(b.sysconfig, "get_config_var", lambda n: "cpython-399")
+    else:
+        os.remove(b.BUILT_FOR)
+    assert not b.binding_fits() and not b.up_to_date()
+    made.clear()
+    b.build()
+    assert made == [("compile", "binding.cpp"), ("link", "_binding.so")]
+    assert b.binding_fits() and b.up_to_date()
+
+
+def test_the_record_names_the_torch_that_is_imported():
+    import torch
+
+    assert f"torch {torch.__version__} " in b._built_for()
+
+
+def test_the_loader_builds_a_binding_that_does_not_fit(monkeypatch):
+    from paged_kv_cache_108_gb300 import _lib
+
+    built = []
+    monkeypatch.setattr(_lib, "_binding", None)
+    monkeypatch.setattr(b, "binding_fits", lambda: bool(built))
+    for f in ("build", "build_binding"):
+        monkeypatch.setattr(b, f, lambda *a, **k: built.append(1))
+    assert _lib.binding().__name__.endswith("_binding") and built == [1]
