@@ -138,14 +138,18 @@ def lib():
 def binding():
     """The compiled binding of the block-sparse step's calls (_binding.so)."""
     global _binding
-    if _binding is None:
-        lib()
-        from . import build as _build
-        if not _build.binding_fits():  # another torch's or Python's layouts must not be loaded
-            _build.build()
-        import torch  # noqa: F401  (its libraries are what the binding links against)
+    if _binding is not None:
+        return _binding
+    lib()
+    with _lock:
+        if _binding is None:
+            from . import build as _build
+            if not _build.binding_fits():  # another torch's or Python's layouts must not be loaded
+                # (libpa.so stays: the binding has to meet the one loaded above)
+                _build.build_binding()
+            import torch  # noqa: F401  (its libraries are what the binding links against)
 
-        _binding = importlib.import_module("._binding", __package__)
+            _binding = importlib.import_module("._binding", __package__)
     return _binding
 
 

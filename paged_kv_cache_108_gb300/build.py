@@ -11,6 +11,8 @@ Run ``python -m paged_kv_cache_108_gb300.build`` or call ``build()``.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
+import fcntl
 import glob
 import importlib.util
 import os
@@ -88,7 +90,6 @@ def up_to_date() -> bool:
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
-    os.makedirs(BUILD, exist_ok=True)
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     if src.endswith(".cu"):
         cmd = [_nvcc(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -115,11 +116,11 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
     """Build what is stale of libpa.so and, where torch is installed, of
     _binding.so; returns libpa.so's path."""
-    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # the binding beside the library
+    with _alone(), cf.ThreadPoolExecutor(max_workers=1) as ex:  # the binding beside the library
         obj = None
         if _torch_dir() is not None and (force or not binding_up_to_date()):
             obj = ex.submit(_compile, BINDING_SRC, False)
-        build_library(force, verbose_ptxas, jobs)
+        _library(force, verbose_ptxas, jobs)
         if obj is not None:
             _link_binding(obj.result())
     return LIB
@@ -128,6 +129,11 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
 def build_library(force: bool = False, verbose_ptxas: bool = False,
                   jobs: int | None = None) -> str:
     """Compile and link libpa.so (needs the CUDA toolkit alone); returns its path."""
+    with _alone():
+        return _library(force, verbose_ptxas, jobs)
+
+
+def _library(force: bool, verbose_ptxas: bool, jobs: int | None) -> str:
     if not force and not verbose_ptxas and library_up_to_date():
         return LIB
     srcs = sources()
@@ -139,11 +145,24 @@ def build_library(force: bool = False, verbose_ptxas: bool = False,
 
 
 def build_binding() -> str:
-    """Compile _binding.so and link it against libpa.so, which it leaves as it is."""
+    """Build _binding.so if it is stale and link it against libpa.so, which it
+    leaves as it is: a process that has libpa.so loaded goes on with that one."""
     if _torch_dir() is None:
         raise RuntimeError("torch not found: the binding is compiled against its headers")
-    _link_binding(_compile(BINDING_SRC, False))
+    with _alone():
+        if not binding_up_to_date():
+            _link_binding(_compile(BINDING_SRC, False))
     return BINDING
+
+
+@contextlib.contextmanager
+def _alone():
+    """One build at a time, over the threads and processes of this machine:
+    they share object files and outputs."""
+    os.makedirs(BUILD, exist_ok=True)
+    with open(os.path.join(BUILD, "lock"), "w") as f:
+        fcntl.flock(f, fcntl.LOCK_EX)
+        yield
 
 
 def _link_binding(obj: str) -> None:

@@ -1,5 +1,9 @@
 """What build.py builds, with what is installed (compiler and linker faked)."""
 import os
+import subprocess
+import sys
+import threading
+import time
 
 import pytest
 
@@ -106,3 +110,66 @@ def test_the_loader_builds_a_binding_that_does_not_fit(monkeypatch):
     for f in ("build", "build_binding"):
         monkeypatch.setattr(b, f, lambda *a, **k: built.append(1))
     assert _lib.binding().__name__.endswith("_binding") and built == [1]
+
+
+def _in_threads(n, f):
+    got = []
+    threads = [threading.Thread(target=lambda: got.append(f())) for _ in range(n)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    return got
+
+
+def test_threads_whose_first_call_finds_no_binding_build_it_once(monkeypatch):
+    from paged_kv_cache_108_gb300 import _lib
+
+    built = []
+
+    def build_binding():
+        time.sleep(0.05)
+        built.append("binding")
+
+    monkeypatch.setattr(_lib, "_binding", None)
+    monkeypatch.setattr(b, "binding_fits", lambda: bool(built))
+    monkeypatch.setattr(b, "build_binding", build_binding)
+    # the library, which is loaded, is not linked anew
+    for f in ("build", "build_library"):
+        monkeypatch.setattr(b, f, lambda *a, **k: built.append("library"))
+    got = _in_threads(8, _lib.binding)
+    assert len(set(got)) == 1 and len(got) == 8 and built == ["binding"]
+
+
+@pytest.mark.parametrize("what", ["build", "build_binding"])
+def test_builds_at_the_same_time_run_one_after_another(made, monkeypatch, what):
+    if what == "build_binding":
+        b.build_library()
+        made.clear()
+    compile_, running, most = b._compile, [], []
+
+    def slow(src, verbose):
+        if src == b.BINDING_SRC:
+            running.append(1)
+            most.append(len(running))
+            time.sleep(0.02)
+            running.pop()
+        return compile_(src, verbose)
+
+    monkeypatch.setattr(b, "_compile", slow)
+    _in_threads(4, getattr(b, what))
+    assert most == [1] and made.count(("link", "_binding.so")) == 1
+    assert made.count(("link", "libpa.so")) == (what == "build")
+
+
+def test_the_binding_and_the_loader_share_one_library():
+    # what the binding's call fails with is what the loader reads
+    from paged_kv_cache_108_gb300 import _lib
+
+    code = """
+from paged_kv_cache_108_gb300 import _lib
+_lib.lib(), _lib.binding()
+with open("/proc/self/maps") as f:
+    print(sorted({l.split()[-1] for l in f if "libpa.so" in l}))
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120,
+                       cwd=b.ROOT)
+    assert r.stdout.strip() == str([_lib.LIB_PATH]), r.stderr[-500:]
