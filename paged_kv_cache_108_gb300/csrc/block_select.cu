@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(32 * kSumWarps, FP8 ? 2 : 4)
     for (int t0 = part; t0 < block; t0 += kLoads * kSplit) {
       uint4 v[kLoads];
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i)  // past the end the run's first token: no effect
+      for (int i = 0; i < kLoads; ++i)  // (those past the block's end are not looked at below)
         if (i == 0 || t0 + i * kSplit < block) v[i] = base[(int64_t)(t0 + i * kSplit) * pieces];
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
@@ -249,7 +249,8 @@ struct __align__(16) QueryCodes {
   float u[G];
 };
 
-// A warp codes one head, D / 32 channels a lane in its registers w.
+// A warp codes one head, four channels (the registers w) to each of the first
+// D / 4 lanes.
 template <int D, int G>
 __device__ __forceinline__ void code_query(QueryCodes<D, G>& q, int head, int lane, uint2 w) {
   float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)}, amax = 0.f;
