@@ -116,6 +116,8 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
     """Build what is stale of libpa.so and, where torch is installed, of
     _binding.so; returns libpa.so's path."""
+    if not force and not verbose_ptxas and up_to_date():
+        return LIB  # (nothing is written, not the lock either)
     with _alone(), cf.ThreadPoolExecutor(max_workers=1) as ex:  # the binding beside the library
         obj = None
         if _torch_dir() is not None and (force or not binding_up_to_date()):
@@ -129,6 +131,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = N
 def build_library(force: bool = False, verbose_ptxas: bool = False,
                   jobs: int | None = None) -> str:
     """Compile and link libpa.so (needs the CUDA toolkit alone); returns its path."""
+    if not force and not verbose_ptxas and library_up_to_date():
+        return LIB
     with _alone():
         return _library(force, verbose_ptxas, jobs)
 

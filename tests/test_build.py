@@ -173,3 +173,10 @@ with open("/proc/self/maps") as f:
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120,
                        cwd=b.ROOT)
     assert r.stdout.strip() == str([_lib.LIB_PATH]), r.stderr[-500:]
+
+
+def test_nothing_is_written_where_nothing_is_stale(made, monkeypatch):
+    b.build()
+    made.clear()
+    monkeypatch.setattr(b, "_alone", None)  # a tree that cannot be written to
+    assert b.build() == b.LIB and b.build_library() == b.LIB and not made
