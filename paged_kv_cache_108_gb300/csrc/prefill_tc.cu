@@ -733,12 +733,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             ptx::tc_fence_before();
           }
           l *= alpha;
-        } else if (cm > m_ref + kRescaleLog2) {
-          if (m_ref != -INFINITY) {
-            // rescale this half of the row of O (earlier chunks): after their PV
-            const float alpha = fast_exp2(m_ref - cm);
+        } else {
+          float alpha = 1.f;
+          if (cm > m_ref + kRescaleLog2) {
+            if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - cm);
+            m_ref = cm;
+          }
+          // Tensor-memory accesses are the whole warp's: if one of its rows
+          // rescales, all its lanes read and write back their rows (by 1 where
+          // a row keeps its reference), after the earlier chunks' PV.
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
             const long long L = ck - 1;
             wait_bar(sm, sm.bar(B_O_FULL + (int)(L & 1)), (uint32_t)(L >> 1) & 1, p.err, 24);
+            __syncwarp();
             ptx::tc_fence_after();
 #pragma unroll
             for (int q2 = 0; q2 < 2; ++q2) {
@@ -752,9 +759,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
-            l *= alpha;
           }
-          m_ref = cm;
+          l *= alpha;
         }
         const float msafe = m_ref == -INFINITY ? 0.f : m_ref;
         // ---- P (and the V rows past the item's last key) ----
