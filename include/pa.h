@@ -50,7 +50,10 @@ typedef enum {
   PA_ERR_UNSUPPORTED = 4  /* valid, but a shape this build has no kernel for */
 } pa_status;
 
-typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1 } pa_kv_dtype;
+/* PA_KV_INT8: 8-bit rows, whole numbers -127 .. 127 under a unit of their own
+ * for each token and head, [num_blocks, block_size, num_kv_heads] fp32 beside
+ * the cache; taken by the scored step's calls alone. */
+typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_INT8 = 2 } pa_kv_dtype;
 
 /* Shape of one K (or V) cache tensor.  Supported: head_dim in {64, 128};
  * block_size >= 1; num_kv_heads >= 1; dtype a pa_kv_dtype. */
@@ -645,6 +648,137 @@ pa_status pa_decode_selected(void* out, const void* q, const void* k_cache, cons
                              const int32_t* row_seqs, const int32_t* selected, int32_t num_rows,
                              int32_t num_seqs, int32_t num_heads, int32_t top, float scale,
                              const float* k_scale, const float* v_scale, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Scored step.  The pages' attention is plain causal softmax over a bf16 or
+ * e4m3 cache; these calls are this library's additions for layers that
+ * normalise each head's queries and keys and change the scores between q . k
+ * and the softmax, and for caches of 8-bit rows.  In stream order:
+ *     pa_norm_rope_and_cache -> pa_decode_scored    (a new token each)
+ *                            -> pa_varlen_scored    (prompts, chunks)
+ *     pa_gather_cache reads a cache back as bf16 rows: contexts of 8-bit rows
+ *     for prompts' tiles, a prefix for another pool or layout.
+ *
+ * 8-bit rows (PA_KV_INT8).  A token's d channels x of one head are held as
+ * whole numbers c under a unit u, u = max |x| / 127 and c = round(x / u) (ties
+ * to even; both quotients in fp32), and stand for c u.  k_scale and v_scale
+ * then name the units, [num_blocks, block_size, num_kv_heads] fp32 at the
+ * cache's slots, 4-byte aligned.  A row of zeros (or whose u underflows to 0)
+ * has u = 0, c = 0; one that holds an infinity or a NaN reads back as NaNs.
+ * The units of an attended token must not be negative.
+ * ---------------------------------------------------------------------- */
+
+/* pa_norm_rope_and_cache -- pa_rope_and_cache into any cache, with each query
+ * and key head normalised first:
+ *     x <- x / sqrt(mean(x^2) + eps) * weight     (over the head's channels)
+ * in fp32, then rotated, then rounded once (queries to bf16, keys to the
+ * cache's elements).  Values are written as they are.
+ *
+ *  q_weight, k_weight  device, [head_dim] fp32; both NULL: no norm.
+ *  eps           finite, >= 0.
+ *  rope          as pa_rope_and_cache, or rot_dim 0: no rotation (its other
+ *                fields, positions and cos_sin are then not used: NULL).
+ *  k_scale, v_scale  e4m3: device scalars, read.  int8: the units, written.
+ *                bf16: NULL.
+ *  Other arguments, limits and refusals as pa_rope_and_cache; nor may q_out
+ *  overlap the units. */
+pa_status pa_norm_rope_and_cache(void* q_out, const void* query, int64_t q_stride,
+                                 int32_t num_heads, const void* key, int64_t k_stride,
+                                 const void* value, int64_t v_stride, void* k_cache, void* v_cache,
+                                 pa_cache_desc cache, const int32_t* slot_mapping,
+                                 const int32_t* positions, const float* cos_sin, pa_rope_desc rope,
+                                 const float* q_weight, const float* k_weight, float eps,
+                                 int32_t num_tokens, float* k_scale, float* v_scale,
+                                 pa_stream_t stream);
+
+/* pa_gather_cache -- reads tokens first_tokens[i] .. context_lens[i] - 1 of
+ * every sequence back, into rows out_start_loc[i], out_start_loc[i] + 1, ...
+ * of k_out and v_out, up to row out_start_loc[i + 1] - 1.  bf16 elements keep
+ * their bits; others are multiplied by their scale in fp32 and rounded to
+ * bf16.  Rows that no token falls to (behind a sequence's last, behind the
+ * last sequence, of a block outside the pool) are left as they were.
+ *
+ *  k_out, v_out  device, [num_rows, num_kv_heads, head_dim] bf16, 16-byte
+ *                aligned; must not overlap each other or the cache.  With
+ *                starts at multiples of a block size these are a bf16 cache
+ *                whose block tables count upwards.
+ *  context_lens  device, [num_seqs] int32, as pa_decode.
+ *  first_tokens  device, [num_seqs] int32, or NULL: 0.  A negative one reads
+ *                nothing.
+ *  out_start_loc device, [num_seqs + 1] int32, non-decreasing.
+ *  Up to 32768 KV heads.  num_rows == 0 is valid and launches nothing. */
+pa_status pa_gather_cache(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                          pa_cache_desc cache, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* context_lens,
+                          const int32_t* first_tokens, const int32_t* out_start_loc,
+                          int32_t num_seqs, int32_t num_rows, const float* k_scale,
+                          const float* v_scale, pa_stream_t stream);
+
+/* What happens to a score s = scale q . k of the query at position i and the
+ * key at position j, in this order:
+ *  cap     > 0: s <- cap tanh(s / cap) (from 1e-6 to 1e6).  0: none.
+ *  slopes  device, [num_heads] fp32: s <- s - slopes[h] |i - j|.  NULL: none.
+ *  window  > 0: only keys with i - j < window are seen.  0: all.
+ * Blocks that lie wholly before the window of every query are not read, nor
+ * are their block table entries. */
+typedef struct {
+  float cap;
+  int32_t window;
+  const float* slopes;
+} pa_score_desc;
+
+/* Workspace bytes of pa_decode_scored (num_rows: sequences) and
+ * pa_varlen_scored (num_rows: new tokens), on the current device; 0 for bad
+ * sizes.  A workspace that is large enough serves calls of any sizes that
+ * need no more, on one stream; calls that share one must not overlap on the
+ * GPU.  It needs no initialisation. */
+size_t pa_scored_workspace_size(int32_t num_rows, int32_t num_heads, int32_t num_kv_heads,
+                                int32_t head_dim);
+
+/* pa_decode_scored -- pa_decode with changed scores, over any cache.  A
+ * sequence's query is at position context_lens[i] - 1.  Any finite scale.
+ *  workspace     >= pa_scored_workspace_size(num_seqs, ...) bytes, 256-byte
+ *                aligned.
+ *  Limits: num_heads / num_kv_heads in {1, 2, 4, 8}; max_blocks_per_seq *
+ *  block_size up to 2^30; num_seqs * num_kv_heads up to 2^27; else
+ *  PA_ERR_UNSUPPORTED.  A block outside the pool is passed over.
+ *  num_seqs == 0 is valid and launches nothing.
+ *  Other arguments as pa_decode. */
+pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           pa_cache_desc cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens,
+                           int32_t num_seqs, int32_t num_heads, float scale, pa_score_desc score,
+                           const float* k_scale, const float* v_scale, void* workspace,
+                           size_t workspace_bytes, pa_stream_t stream);
+
+/* pa_varlen_scored -- pa_varlen_attention with changed scores, over any cache:
+ * a new token at position i sees keys 0 .. i, and, if i < prefix_lens[r], all
+ * keys below that (a prefix whose tokens see each other); a window applies to
+ * the keys before it.
+ *
+ *  prefix_lens   device, [num_seqs] int32, or NULL; what is over seq_lens[r]
+ *                is cut.
+ *  workspace     >= pa_scored_workspace_size(num_tokens, ...) bytes, 256-byte
+ *                aligned.
+ *  Steps with more than 2 new tokens per request on average run on the
+ *  tensor-core prefill tiles, for a bf16 or e4m3 cache with head_dim 128,
+ *  block_size >= 8, at most 256 requests and 65535 new tokens; a request that
+ *  sees more than max_blocks_per_seq * block_size keys then gets zero rows,
+ *  and workspace word 0 (int32) is set to a nonzero code if a bounded wait
+ *  expired or a block id was out of range; the library never clears it.  All
+ *  other steps are computed row by row, each new token reading its keys (long
+ *  prompts over 8-bit rows are better gathered first).
+ *  A request whose new tokens exceed its seq_len gets zero rows.  Rows of out
+ *  before query_start_loc[0] or behind query_start_loc[num_seqs] are left as
+ *  they were.
+ *  Limits and other arguments as pa_decode_scored and pa_varlen_attention. */
+pa_status pa_varlen_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           pa_cache_desc cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                           const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                           int32_t num_heads, float scale, pa_score_desc score,
+                           const int32_t* prefix_lens, const float* k_scale, const float* v_scale,
+                           void* workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Host-side block pool (off the hot path; not thread-safe: one owner).

@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(_HERE, "libpa.so")
 
 PA_OK, PA_ERR_INVALID, PA_ERR_OOM, PA_ERR_CUDA, PA_ERR_UNSUPPORTED = range(5)
 PA_DECODE_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # include/pa.h
-PA_KV_BF16, PA_KV_FP8_E4M3 = 0, 1
+PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_INT8 = 0, 1, 2
 
 
 class CacheDesc(ctypes.Structure):
@@ -33,6 +33,10 @@ class RopeDesc(ctypes.Structure):
     _fields_ = [("rot_dim", ctypes.c_int32), ("max_position", ctypes.c_int32),
                 ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
                 ("sections_in_turn", ctypes.c_int32), ("adjacent_pairs", ctypes.c_int32)]
+
+
+class ScoreDesc(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p)]
 
 
 class PaError(RuntimeError):
@@ -92,6 +96,14 @@ SIGNATURES = {
                                P]),
     "pa_decode_selected": (I32, [P, P, P, P, CacheDesc, P, I32, P, P, P, I32, I32, I32, I32,
                                  ctypes.c_float, P, P, P]),
+    "pa_norm_rope_and_cache": (I32, [P, P, I64, I32, P, I64, P, I64, P, P, CacheDesc, P, P, P,
+                                     RopeDesc, P, P, ctypes.c_float, I32, P, P, P]),
+    "pa_gather_cache": (I32, [P, P, P, P, CacheDesc, P, I32, P, P, P, I32, I32, P, P, P]),
+    "pa_scored_workspace_size": (SIZE, [I32, I32, I32, I32]),
+    "pa_decode_scored": (I32, [P, P, P, P, CacheDesc, P, I32, P, I32, I32, ctypes.c_float,
+                               ScoreDesc, P, P, P, SIZE, P]),
+    "pa_varlen_scored": (I32, [P, P, P, P, CacheDesc, P, I32, P, P, I32, I32, I32, ctypes.c_float,
+                               ScoreDesc, P, P, P, P, SIZE, P]),
     "pa_slot_mapping": (I32, [PI32, I32, I32, I32, PI32, PI32, I32, PI32]),
     "pa_pool_create": (P, [I32]),
     "pa_pool_create_ordered": (P, [I32, PI32]),
@@ -136,7 +148,7 @@ def lib():
 
 
 def binding():
-    """The compiled binding of the block-sparse step's calls (_binding.so)."""
+    """The compiled binding of the block-sparse and scored steps' calls (_binding.so)."""
     global _binding
     if _binding is not None:
         return _binding

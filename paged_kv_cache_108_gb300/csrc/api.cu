@@ -22,6 +22,10 @@ constexpr int kMaxPartition = 65536;
 // take the tensor-core prefill tiles
 constexpr int kTileMinTokens = 16;
 
+// pa_varlen_scored: up to this many new tokens per request on average each
+// is a row of its own, with more the tensor-core tiles serve them
+constexpr int kRowsPerRequest = 2;
+
 bool is_pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
 int ilog2(int64_t x) {
@@ -126,6 +130,57 @@ pa_status check_scales(const pa_cache_desc& c, const float* ks, const float* vs,
   return PA_OK;
 }
 
+// check_cache and check_scales of the calls that also take 8-bit rows.
+pa_status check_any_cache(pa_cache_desc c, const float* ks, const float* vs, const char* fn) {
+  const bool rows = c.dtype == PA_KV_INT8;
+  if (rows) c.dtype = PA_KV_FP8_E4M3;  // the same limits
+  const pa_status st = check_cache(c, fn);
+  if (st != PA_OK) return st;
+  if (rows && (!ks || !vs || !aligned(ks, 4) || !aligned(vs, 4)))
+    return pa_fail(PA_ERR_INVALID,
+                   (std::string(fn) + ": an int8 cache needs k_scale and v_scale, 4-byte aligned").c_str());
+  return rows ? PA_OK : check_scales(c, ks, vs, fn);
+}
+
+pa::KvFormat format_of(const pa_cache_desc& c) {
+  return c.dtype == PA_KV_BF16 ? pa::kBf16 : c.dtype == PA_KV_INT8 ? pa::kInt8 : pa::kE4m3;
+}
+
+// What changes the scores, checked, in the kernels' units.
+pa_status check_score(const pa_score_desc& s, float scale, int32_t max_blocks, int32_t block_size,
+                      const char* fn, pa::ScoreMod* mod) {
+  char buf[192];
+  if (!std::isfinite(scale)) {
+    snprintf(buf, sizeof buf, "%s: scale must be finite", fn);
+    return pa_fail(PA_ERR_INVALID, buf);
+  }
+  if (!(s.cap >= 0.f) || !std::isfinite(s.cap) || s.window < 0 || !aligned(s.slopes, 4)) {
+    snprintf(buf, sizeof buf,
+             "%s: cap must be finite and not negative, window not negative, slopes 4-byte aligned",
+             fn);
+    return pa_fail(PA_ERR_INVALID, buf);
+  }
+  // 2 / cap, and tanh of it times any logit, stay in range
+  if (s.cap > 0.f && (s.cap < 1e-6f || s.cap > 1e6f)) {
+    snprintf(buf, sizeof buf, "%s: cap unsupported (0, or 1e-6 to 1e6)", fn);
+    return pa_fail(PA_ERR_UNSUPPORTED, buf);
+  }
+  if ((int64_t)max_blocks * block_size > (1 << 30)) {
+    snprintf(buf, sizeof buf, "%s: max_blocks_per_seq * block_size above 2^30", fn);
+    return pa_fail(PA_ERR_UNSUPPORTED, buf);
+  }
+  *mod = {};
+  mod->cap_log2 = s.cap * 1.4426950408889634f;
+  mod->inv_cap_log2 = s.cap > 0.f ? 2.f / s.cap : 0.f;
+  mod->slopes = s.slopes;
+  mod->window = s.window;
+  return PA_OK;
+}
+
+// The scored calls' workspace: the tiles' error word and work counter, then
+// what split units need.
+constexpr size_t kScoredHead = 256;
+
 // What the calls over query rows share: row r belongs to sequence
 // row_seqs[r], or r.
 pa_status check_rows(const pa_cache_desc& c, int32_t max_blocks, const int32_t* row_seqs,
@@ -157,6 +212,182 @@ pa_status cuda_status(cudaError_t e, const char* fn) {
   char buf[256];
   snprintf(buf, sizeof buf, "%s: %s", fn, cudaGetErrorString(e));
   return pa_fail(PA_ERR_CUDA, buf);
+}
+
+// What the two rotating writes share: their checks and parameters.  `norm`:
+// the call that also normalises, and may leave the rotation out.
+pa_status rope_params(const char* fn, void* q_out, const void* query, int64_t q_stride,
+                      int32_t num_heads, const void* key, int64_t k_stride, const void* value,
+                      int64_t v_stride, void* k_cache, void* v_cache, const pa_cache_desc& cache,
+                      const int32_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+                      pa_rope_desc rope, int32_t num_tokens, pa::RopeParams* params,
+                      bool norm = false) {
+  auto fail = [&](pa_status st, const char* msg) {
+    return pa_fail(st, (std::string(fn) + ": " + msg).c_str());
+  };
+  if (num_tokens < 0 || num_heads < 0)
+    return fail(PA_ERR_INVALID, "num_tokens or num_heads < 0");
+  const bool rotates = !norm || rope.rot_dim != 0;
+  if (!rotates) rope = {};
+  const int32_t pairs = rope.rot_dim / 2;
+  if (rotates && (rope.max_position <= 0 || rope.num_axes < 1))
+    return fail(PA_ERR_INVALID, "max_position and num_axes must be positive");
+  if (rotates && (rope.rot_dim <= 0 || rope.rot_dim % 16 || rope.rot_dim > cache.head_dim || rope.num_axes > 4))
+    return fail(PA_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16 up to head_dim, num_axes at most 4");
+  if (rope.num_axes > 1) {
+    int64_t sum = 0;
+    for (int a = 0; a < rope.num_axes; ++a) {
+      const int64_t n = rope.sections[a];
+      if (n < 0) return fail(PA_ERR_INVALID, "negative section");
+      sum += n;
+      if (rope.sections_in_turn && a > 0 && n > 0 && a + rope.num_axes * (n - 1) >= pairs)
+        return fail(PA_ERR_INVALID, "a section in turn runs past rot_dim / 2");
+    }
+    if (sum != pairs)
+      return fail(PA_ERR_INVALID, "sections must sum to rot_dim / 2");
+  }
+  const int64_t q_row = (int64_t)num_heads * cache.head_dim;
+  const int64_t kv_row = (int64_t)cache.num_kv_heads * cache.head_dim;
+  if ((int64_t)num_heads + 2 * (int64_t)cache.num_kv_heads > 32768)
+    return fail(PA_ERR_UNSUPPORTED, "more than 32768 heads in all");
+  constexpr int64_t kMaxStride = int64_t(1) << 40;  // addresses stay within 64 bits
+  if ((num_heads && (q_stride < q_row || q_stride % 8 || q_stride > kMaxStride)) ||
+      k_stride < kv_row || k_stride % 8 || k_stride > kMaxStride || v_stride < kv_row ||
+      v_stride % 8 || v_stride > kMaxStride)
+    return fail(PA_ERR_INVALID, "strides must be multiples of 8, hold a token's heads and be "
+                   "at most 2^40");
+  if (num_tokens == 0) return PA_OK;
+  if ((num_heads && (!q_out || !query)) || !key || !value || !k_cache || !v_cache ||
+      !slot_mapping || (rotates && (!positions || !cos_sin)))
+    return fail(PA_ERR_INVALID, "NULL pointer");
+  if (!aligned(q_out, 16) || !aligned(query, 16) || !aligned(key, 16) || !aligned(value, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 4) ||
+      !aligned(positions, 4) || !aligned(cos_sin, 4))
+    return fail(PA_ERR_INVALID, "misaligned pointer");
+  if (num_heads) {
+    // what is read after a part of q_out is written must lie elsewhere
+    const auto* o0 = static_cast<const char*>(q_out);
+    const char* o1 = o0 + 2 * (int64_t)num_tokens * q_row;
+    if (!(q_out == query && q_stride == q_row) &&
+        rows_meet(query, q_stride * 2, q_row * 2, num_tokens, o0, o1))
+      return fail(PA_ERR_INVALID, "q_out overlaps query in another layout");
+    if (rows_meet(key, k_stride * 2, kv_row * 2, num_tokens, o0, o1) ||
+        rows_meet(value, v_stride * 2, kv_row * 2, num_tokens, o0, o1))
+      return fail(PA_ERR_INVALID, "q_out overlaps key or value");
+    const int64_t pool = (int64_t)cache.num_blocks * cache.block_size * kv_row *
+                         (cache.dtype == PA_KV_BF16 ? 2 : 1);
+    if (rows_meet(k_cache, pool, pool, 1, o0, o1) || rows_meet(v_cache, pool, pool, 1, o0, o1))
+      return fail(PA_ERR_INVALID, "q_out overlaps a cache");
+  }
+  pa::RopeParams& p = *params;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.query = static_cast<const __nv_bfloat16*>(query);
+  p.key = static_cast<const __nv_bfloat16*>(key);
+  p.value = static_cast<const __nv_bfloat16*>(value);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.slot_mapping = slot_mapping;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.num_slots = (int64_t)cache.num_blocks * cache.block_size;
+  p.num_tokens = num_tokens;
+  p.num_heads = num_heads;
+  p.num_kv_heads = cache.num_kv_heads;
+  p.rot_dim = rope.rot_dim;
+  p.max_position = rope.max_position;
+  p.num_axes = rope.num_axes;
+  for (int a = 0; a < 4; ++a) p.sections[a] = rope.sections[a];
+  p.in_turn = rope.sections_in_turn != 0;
+  p.adjacent = rope.adjacent_pairs != 0;
+  return PA_OK;
+}
+
+// Decode with changed scores for one row of each sequence, or (`starts` given)
+// for several: by tiles where they apply, else row by row.
+pa_status scored_rows(const char* fn, void* out, const void* q, const void* k_cache,
+                      const void* v_cache, const pa_cache_desc& cache, const int32_t* block_tables,
+                      int32_t max_blocks, const int32_t* lens, const int32_t* starts,
+                      int32_t num_rows, int32_t num_seqs, int32_t num_heads, float scale,
+                      const pa_score_desc& score, const int32_t* prefix_lens, const float* k_scale,
+                      const float* v_scale, void* workspace, size_t workspace_bytes,
+                      pa_stream_t stream) {
+  auto fail = [&](pa_status st, const char* msg) {
+    return pa_fail(st, (std::string(fn) + ": " + msg).c_str());
+  };
+  pa_status st = check_any_cache(cache, k_scale, v_scale, fn);
+  if (st != PA_OK) return st;
+  // (with starts a row's sequence is known on the device alone)
+  if ((st = check_rows(cache, max_blocks, starts, num_rows, num_seqs, num_heads, fn)) != PA_OK)
+    return st;
+  pa::ScoreMod mod;
+  if ((st = check_score(score, scale, max_blocks, cache.block_size, fn, &mod)) != PA_OK) return st;
+  mod.prefix_lens = prefix_lens;
+  if (num_rows == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !lens || !workspace)
+    return fail(PA_ERR_INVALID, "NULL pointer");
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_tables, 4) || !aligned(lens, 4) || !aligned(workspace, 256))
+    return fail(PA_ERR_INVALID, "misaligned pointer");
+  const size_t need =
+      pa_scored_workspace_size(num_rows, num_heads, cache.num_kv_heads, cache.head_dim);
+  if (workspace_bytes < need)
+    return fail(PA_ERR_INVALID, ("workspace of " + std::to_string(need) + " bytes needed").c_str());
+  const int group = num_heads / cache.num_kv_heads;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (starts && cache.dtype != PA_KV_INT8 && num_rows > kRowsPerRequest * (int64_t)num_seqs &&
+      num_rows <= 65535 &&
+      pa::prefill_supported(cache.head_dim, group, cache.dtype == PA_KV_FP8_E4M3, num_seqs,
+                            cache.block_size)) {
+    pa::PrefillLaunch a{};
+    a.out = out;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_tables = block_tables;
+    a.seq_lens = lens;
+    a.query_start_loc = starts;
+    a.workspace = workspace;
+    a.num_seqs = num_seqs;
+    a.num_tokens = num_rows;
+    a.num_heads = num_heads;
+    a.num_kv_heads = cache.num_kv_heads;
+    a.max_blocks = max_blocks;
+    a.num_blocks = cache.num_blocks;
+    a.block_size = cache.block_size;
+    a.num_ctas = num_sms();
+    a.scale = scale;
+    a.fp8 = cache.dtype == PA_KV_FP8_E4M3;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.scored = true;
+    a.mod = mod;
+    return cuda_status(pa::launch_prefill_tc(a, s), fn);
+  }
+  pa::ScoredParams p = {};
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.lens = lens;
+  p.starts = starts;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.num_rows = num_rows;
+  p.num_seqs = num_seqs;
+  p.num_kv_heads = cache.num_kv_heads;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks;
+  p.log2_block_size = ilog2(cache.block_size);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.mod = mod;
+  return cuda_status(
+      pa::launch_decode_scored(p, static_cast<char*>(workspace) + kScoredHead, cache.head_dim,
+                               group, format_of(cache), num_sms(), s),
+      fn);
 }
 
 }  // namespace
@@ -882,88 +1113,157 @@ pa_status pa_rope_and_cache(void* q_out, const void* query, int64_t q_stride, in
   pa_status st = check_cache(cache, fn);
   if (st != PA_OK) return st;
   if ((st = check_scales(cache, k_scale, v_scale, fn)) != PA_OK) return st;
-  if (num_tokens < 0 || num_heads < 0)
-    return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: num_tokens or num_heads < 0");
-  const int32_t pairs = rope.rot_dim / 2;
-  if (rope.max_position <= 0 || rope.num_axes < 1)
-    return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: max_position and num_axes must be positive");
-  if (rope.rot_dim <= 0 || rope.rot_dim % 16 || rope.rot_dim > cache.head_dim || rope.num_axes > 4)
-    return pa_fail(PA_ERR_UNSUPPORTED,
-                   "pa_rope_and_cache: rot_dim must be a multiple of 16 up to head_dim, num_axes at most 4");
-  if (rope.num_axes > 1) {
-    int64_t sum = 0;
-    for (int a = 0; a < rope.num_axes; ++a) {
-      const int64_t n = rope.sections[a];
-      if (n < 0) return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: negative section");
-      sum += n;
-      if (rope.sections_in_turn && a > 0 && n > 0 && a + rope.num_axes * (n - 1) >= pairs)
-        return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: a section in turn runs past rot_dim / 2");
-    }
-    if (sum != pairs)
-      return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: sections must sum to rot_dim / 2");
-  }
-  const int64_t q_row = (int64_t)num_heads * cache.head_dim;
-  const int64_t kv_row = (int64_t)cache.num_kv_heads * cache.head_dim;
-  if ((int64_t)num_heads + 2 * (int64_t)cache.num_kv_heads > 32768)
-    return pa_fail(PA_ERR_UNSUPPORTED, "pa_rope_and_cache: more than 32768 heads in all");
-  constexpr int64_t kMaxStride = int64_t(1) << 40;  // addresses stay within 64 bits
-  if ((num_heads && (q_stride < q_row || q_stride % 8 || q_stride > kMaxStride)) ||
-      k_stride < kv_row || k_stride % 8 || k_stride > kMaxStride || v_stride < kv_row ||
-      v_stride % 8 || v_stride > kMaxStride)
-    return pa_fail(PA_ERR_INVALID,
-                   "pa_rope_and_cache: strides must be multiples of 8, hold a token's heads and be "
-                   "at most 2^40");
-  if (num_tokens == 0) return PA_OK;
-  if ((num_heads && (!q_out || !query)) || !key || !value || !k_cache || !v_cache ||
-      !slot_mapping || !positions || !cos_sin)
-    return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: NULL pointer");
-  if (!aligned(q_out, 16) || !aligned(query, 16) || !aligned(key, 16) || !aligned(value, 16) ||
-      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 4) ||
-      !aligned(positions, 4) || !aligned(cos_sin, 4))
-    return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: misaligned pointer");
-  if (num_heads) {
-    // what is read after a part of q_out is written must lie elsewhere
-    const auto* o0 = static_cast<const char*>(q_out);
-    const char* o1 = o0 + 2 * (int64_t)num_tokens * q_row;
-    if (!(q_out == query && q_stride == q_row) &&
-        rows_meet(query, q_stride * 2, q_row * 2, num_tokens, o0, o1))
-      return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: q_out overlaps query in another layout");
-    if (rows_meet(key, k_stride * 2, kv_row * 2, num_tokens, o0, o1) ||
-        rows_meet(value, v_stride * 2, kv_row * 2, num_tokens, o0, o1))
-      return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: q_out overlaps key or value");
-    const int64_t pool = (int64_t)cache.num_blocks * cache.block_size * kv_row *
-                         (cache.dtype == PA_KV_BF16 ? 2 : 1);
-    if (rows_meet(k_cache, pool, pool, 1, o0, o1) || rows_meet(v_cache, pool, pool, 1, o0, o1))
-      return pa_fail(PA_ERR_INVALID, "pa_rope_and_cache: q_out overlaps a cache");
-  }
   pa::RopeParams p = {};
-  p.q_out = static_cast<__nv_bfloat16*>(q_out);
-  p.query = static_cast<const __nv_bfloat16*>(query);
-  p.key = static_cast<const __nv_bfloat16*>(key);
-  p.value = static_cast<const __nv_bfloat16*>(value);
-  p.q_stride = q_stride;
-  p.k_stride = k_stride;
-  p.v_stride = v_stride;
-  p.k_cache = k_cache;
-  p.v_cache = v_cache;
-  p.slot_mapping = slot_mapping;
-  p.positions = positions;
-  p.cos_sin = cos_sin;
+  st = rope_params(fn, q_out, query, q_stride, num_heads, key, k_stride, value, v_stride, k_cache,
+                   v_cache, cache, slot_mapping, positions, cos_sin, rope, num_tokens, &p);
+  if (st != PA_OK || num_tokens == 0) return st;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
-  p.num_slots = (int64_t)cache.num_blocks * cache.block_size;
-  p.num_tokens = num_tokens;
-  p.num_heads = num_heads;
-  p.num_kv_heads = cache.num_kv_heads;
-  p.rot_dim = rope.rot_dim;
-  p.max_position = rope.max_position;
-  p.num_axes = rope.num_axes;
-  for (int a = 0; a < 4; ++a) p.sections[a] = rope.sections[a];
-  p.in_turn = rope.sections_in_turn != 0;
-  p.adjacent = rope.adjacent_pairs != 0;
   return cuda_status(pa::launch_rope_and_cache(p, cache.head_dim, cache.dtype == PA_KV_FP8_E4M3,
                                                num_sms(), reinterpret_cast<cudaStream_t>(stream)),
                      fn);
+}
+
+pa_status pa_norm_rope_and_cache(void* q_out, const void* query, int64_t q_stride,
+                                 int32_t num_heads, const void* key, int64_t k_stride,
+                                 const void* value, int64_t v_stride, void* k_cache, void* v_cache,
+                                 pa_cache_desc cache, const int32_t* slot_mapping,
+                                 const int32_t* positions, const float* cos_sin, pa_rope_desc rope,
+                                 const float* q_weight, const float* k_weight, float eps,
+                                 int32_t num_tokens, float* k_scale, float* v_scale,
+                                 pa_stream_t stream) {
+  const char* fn = "pa_norm_rope_and_cache";
+  pa_status st = check_any_cache(cache, k_scale, v_scale, fn);
+  if (st != PA_OK) return st;
+  if (!q_weight != !k_weight)
+    return pa_fail(PA_ERR_INVALID,
+                   "pa_norm_rope_and_cache: q_weight and k_weight are given together or not at all");
+  if (!aligned(q_weight, 4) || !aligned(k_weight, 4))
+    return pa_fail(PA_ERR_INVALID, "pa_norm_rope_and_cache: misaligned weights");
+  if (q_weight && !(eps >= 0.f && std::isfinite(eps)))
+    return pa_fail(PA_ERR_INVALID, "pa_norm_rope_and_cache: eps must be finite and not negative");
+  pa::RopeParams p = {};
+  st = rope_params(fn, q_out, query, q_stride, num_heads, key, k_stride, value, v_stride, k_cache,
+                   v_cache, cache, slot_mapping, positions, cos_sin, rope, num_tokens, &p, true);
+  if (st != PA_OK || num_tokens == 0) return st;
+  if (cache.dtype == PA_KV_INT8) {
+    const int64_t units = (int64_t)cache.num_blocks * cache.block_size * cache.num_kv_heads * 4;
+    const auto* o0 = static_cast<const char*>(q_out);
+    const char* o1 = o0 + 2 * (int64_t)num_tokens * num_heads * cache.head_dim;
+    if (num_heads && (rows_meet(k_scale, units, units, 1, o0, o1) ||
+                      rows_meet(v_scale, units, units, 1, o0, o1)))
+      return pa_fail(PA_ERR_INVALID, "pa_norm_rope_and_cache: q_out overlaps k_scale or v_scale");
+    p.k_units = k_scale;
+    p.v_units = v_scale;
+  } else {
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+  }
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  return cuda_status(pa::launch_norm_rope_and_cache(p, cache.head_dim, format_of(cache), num_sms(),
+                                                    reinterpret_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+pa_status pa_gather_cache(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                          pa_cache_desc cache, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* context_lens,
+                          const int32_t* first_tokens, const int32_t* out_start_loc,
+                          int32_t num_seqs, int32_t num_rows, const float* k_scale,
+                          const float* v_scale, pa_stream_t stream) {
+  const char* fn = "pa_gather_cache";
+  const pa_status st = check_any_cache(cache, k_scale, v_scale, fn);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || num_rows < 0 || max_blocks_per_seq <= 0)
+    return pa_fail(PA_ERR_INVALID, "pa_gather_cache: bad sizes");
+  if (cache.num_kv_heads > 32768)
+    return pa_fail(PA_ERR_UNSUPPORTED, "pa_gather_cache: num_kv_heads above 32768");
+  if (num_rows == 0 || num_seqs == 0) return PA_OK;
+  if (!k_out || !v_out || !k_cache || !v_cache || !block_tables || !context_lens || !out_start_loc)
+    return pa_fail(PA_ERR_INVALID, "pa_gather_cache: NULL pointer");
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(first_tokens, 4) ||
+      !aligned(out_start_loc, 4))
+    return pa_fail(PA_ERR_INVALID, "pa_gather_cache: misaligned pointer");
+  // what is read while a part of the outputs is written must lie elsewhere
+  const int64_t elems = (int64_t)cache.num_kv_heads * cache.head_dim;
+  const int64_t slots = (int64_t)cache.num_blocks * cache.block_size;
+  const int64_t out_bytes = num_rows * elems * 2;
+  const int64_t pool = slots * elems * (cache.dtype == PA_KV_BF16 ? 2 : 1);
+  const int64_t units = cache.dtype == PA_KV_INT8 ? slots * cache.num_kv_heads * 4 : 4;
+  const void* const outs[] = {k_out, v_out};
+  for (const void* o : outs) {
+    const auto* o0 = static_cast<const char*>(o);
+    const char* o1 = o0 + out_bytes;
+    if (rows_meet(k_cache, pool, pool, 1, o0, o1) || rows_meet(v_cache, pool, pool, 1, o0, o1) ||
+        (k_scale && rows_meet(k_scale, units, units, 1, o0, o1)) ||
+        (v_scale && rows_meet(v_scale, units, units, 1, o0, o1)))
+      return pa_fail(PA_ERR_INVALID, "pa_gather_cache: an output overlaps the cache");
+  }
+  if (rows_meet(k_out, out_bytes, out_bytes, 1, static_cast<const char*>(v_out),
+                static_cast<const char*>(v_out) + out_bytes))
+    return pa_fail(PA_ERR_INVALID, "pa_gather_cache: the outputs overlap");
+  pa::GatherParams p = {};
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.first_tokens = first_tokens;
+  p.out_start_loc = out_start_loc;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.num_seqs = num_seqs;
+  p.num_rows = num_rows;
+  p.num_kv_heads = cache.num_kv_heads;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks_per_seq;
+  p.log2_block_size = ilog2(cache.block_size);
+  return cuda_status(pa::launch_gather_cache(p, cache.head_dim, format_of(cache), num_sms(),
+                                             reinterpret_cast<cudaStream_t>(stream)),
+                     fn);
+}
+
+size_t pa_scored_workspace_size(int32_t num_rows, int32_t num_heads, int32_t num_kv_heads,
+                                int32_t head_dim) {
+  if (num_rows < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
+      head_dim <= 0)
+    return 0;
+  return kScoredHead +
+         pa::scored_workspace_bytes(num_rows, num_heads, num_kv_heads, head_dim, num_sms());
+}
+
+pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           pa_cache_desc cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens,
+                           int32_t num_seqs, int32_t num_heads, float scale, pa_score_desc score,
+                           const float* k_scale, const float* v_scale, void* workspace,
+                           size_t workspace_bytes, pa_stream_t stream) {
+  return scored_rows("pa_decode_scored", out, q, k_cache, v_cache, cache, block_tables,
+                     max_blocks_per_seq, context_lens, nullptr, num_seqs, num_seqs, num_heads,
+                     scale, score, nullptr, k_scale, v_scale, workspace, workspace_bytes, stream);
+}
+
+pa_status pa_varlen_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           pa_cache_desc cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                           const int32_t* query_start_loc, int32_t num_seqs, int32_t num_tokens,
+                           int32_t num_heads, float scale, pa_score_desc score,
+                           const int32_t* prefix_lens, const float* k_scale, const float* v_scale,
+                           void* workspace, size_t workspace_bytes, pa_stream_t stream) {
+  const char* fn = "pa_varlen_scored";
+  if (num_tokens > 0 && num_seqs == 0)
+    return pa_fail(PA_ERR_INVALID, "pa_varlen_scored: tokens without requests");
+  if (num_tokens > 0 && !query_start_loc)
+    return pa_fail(PA_ERR_INVALID, "pa_varlen_scored: NULL pointer");
+  if (!aligned(query_start_loc, 4) || !aligned(prefix_lens, 4))
+    return pa_fail(PA_ERR_INVALID, "pa_varlen_scored: misaligned pointer");
+  return scored_rows(fn, out, q, k_cache, v_cache, cache, block_tables, max_blocks_per_seq,
+                     seq_lens, query_start_loc, num_tokens, num_seqs, num_heads, scale, score,
+                     prefix_lens, k_scale, v_scale, workspace, workspace_bytes, stream);
 }
 
 pa_status pa_summarize_blocks(const void* k_cache, pa_cache_desc cache,

@@ -1,4 +1,4 @@
-// Launch helper shared by the block-sparse step's kernels.
+// Launch helpers shared by the kernels of the later steps.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -95,4 +95,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// About one step of fp32.
+__device__ __forceinline__ float fast_reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
 }  // namespace pa

@@ -75,6 +75,15 @@ cudaError_t launch_decode_tc(const TcLaunch& a, cudaStream_t stream);
 // (16 for group 1, else 8); any block size (head-major tiles for blocks of
 // at least 128 / that many tokens, token-major below).
 // Takes the same TcLaunch (fp8, tokens_per_seq and non_causal unused).
+// What changes a score before the softmax (log2 units where named so).
+struct ScoreMod {
+  float cap_log2;      // > 0: s2 -> cap_log2 tanh(s2 / cap_log2)
+  float inv_cap_log2;  // 2 log2(e) / cap_log2
+  const float* slopes;          // [H] or null
+  const int32_t* prefix_lens;   // [S] or null
+  int32_t window;               // > 0: keys of the last `window` positions only
+};
+
 // Causal varlen attention for prefill chunks on the tensor cores
 // (prefill_tc.cu): bf16 cache, head_dim 128, GQA group 1, 2, 4 or 8, at most
 // 256 requests, blocks of at least 8 tokens.  workspace word 0 is the error
@@ -95,6 +104,8 @@ struct PrefillLaunch {
   bool fp8;                // e4m3 cache: k_scale / v_scale are device scalars
   const float* k_scale;
   const float* v_scale;
+  bool scored;  // with changed scores
+  ScoreMod mod;
 };
 bool prefill_supported(int head_dim, int group, bool fp8, int num_seqs, int block_size);
 cudaError_t launch_prefill_tc(const PrefillLaunch& a, cudaStream_t stream);
@@ -140,7 +151,10 @@ cudaError_t launch_copy_blocks(void* k_cache, void* v_cache,
                                const int32_t* pairs, int num_pairs,
                                cudaStream_t stream);
 
-// Rotation and cache write (rope_cache.cu).  Strides in elements.
+// How a cache's elements are held: pa_kv_dtype's values.
+enum KvFormat { kBf16 = 0, kE4m3 = 1, kInt8 = 2 };
+
+// Norm, rotation and cache write (rope_cache.cu).  Strides in elements.
 struct RopeParams {
   __nv_bfloat16* q_out;        // [N, H, D]
   const __nv_bfloat16* query;  // N rows of [H, D], q_stride apart
@@ -154,6 +168,11 @@ struct RopeParams {
   const float* cos_sin;         // [max_position, rot_dim]: cosines, then sines
   const float* k_scale;         // fp8 only
   const float* v_scale;
+  const float* q_weight;        // [D]: the norm's weights; both null: no norm
+  const float* k_weight;
+  float* k_units;               // int8: [num_slots, Hkv], written
+  float* v_units;
+  float eps;
   int64_t num_slots;
   int64_t num_tokens;
   int32_t num_heads, num_kv_heads;
@@ -164,6 +183,50 @@ struct RopeParams {
 };
 cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, int num_sms,
                                   cudaStream_t stream);
+// With the norm (where its weights are given) and into any cache; rot_dim may
+// be 0 (no positions then, num_axes 0).
+cudaError_t launch_norm_rope_and_cache(RopeParams p, int head_dim, KvFormat format, int num_sms,
+                                       cudaStream_t stream);
+
+// Reading a cache back (gather_cache.cu).
+struct GatherParams {
+  __nv_bfloat16* k_out;  // [num_rows, Hkv, D]
+  __nv_bfloat16* v_out;
+  const void* k_cache;  // [NB, B, Hkv, D]
+  const void* v_cache;
+  const int32_t* block_tables;   // [S, max_blocks]
+  const int32_t* context_lens;   // [S]
+  const int32_t* first_tokens;   // [S] or null (zeros)
+  const int32_t* out_start_loc;  // [S + 1]
+  const float* k_scale;          // e4m3: scalars; int8: [num_slots, Hkv]
+  const float* v_scale;
+  int32_t num_seqs, num_rows, num_kv_heads, num_blocks, max_blocks, log2_block_size;
+};
+cudaError_t launch_gather_cache(const GatherParams& p, int head_dim, KvFormat format, int num_sms,
+                                cudaStream_t stream);
+
+// Decode with changed scores (decode_scored.cu).
+struct ScoredParams {
+  __nv_bfloat16* out;  // [R, H, D]
+  const __nv_bfloat16* q;
+  const void* k_cache;  // [NB, B, Hkv, D]
+  const void* v_cache;
+  const int32_t* block_tables;  // [S, max_blocks]
+  const int32_t* lens;          // [S]
+  const int32_t* starts;        // [S + 1] first row of each sequence; null: one row each
+  const float* k_scale;         // e4m3: scalars; int8: [num_slots, Hkv]
+  const float* v_scale;
+  unsigned long long* counters;  // [units]: arrivals of a split unit's pieces
+  float* parts;                  // [CTAs][2][G][D + 2]: partial sums
+  unsigned long long epoch;
+  int32_t num_rows, num_seqs, num_kv_heads, num_blocks, max_blocks, log2_block_size;
+  float scale_log2;  // scale * log2(e)
+  ScoreMod mod;
+};
+size_t scored_workspace_bytes(int64_t num_rows, int64_t num_heads, int64_t num_kv_heads,
+                              int head_dim, int num_sms);
+cudaError_t launch_decode_scored(ScoredParams p, void* workspace, int head_dim, int group,
+                                 KvFormat format, int num_sms, cudaStream_t stream);
 
 // Key ranges of full blocks and block selection (block_select.cu).
 struct SummaryParams {

@@ -1,4 +1,5 @@
-// Rotary position embedding fused with the cache write.
+// Rotary position embedding fused with the cache write; optionally behind an
+// RMS norm of each query and key head, and into a cache of 8-bit rows.
 //
 // For the pair (x, y) that pair index i < rot_dim / 2 names in a head, with
 // p the token's position on that pair's axis and (c, s) = (cos, sin) from
@@ -16,6 +17,12 @@
 // these are in flight the tokens' cosines and sines -- shared by all heads --
 // are gathered into shared memory, one (pair, axis) per thread, which serves
 // every assignment of axes to pairs alike.
+//
+// The norm, x / sqrt(mean x^2 + eps) * w per head, and the 8-bit rows' unit,
+// max |x| / 127 per token and head, are sums and maxima over a head, which
+// d / 16 neighbouring threads hold between them: three shuffles (two at 64
+// channels) each, in fp32, and no further pass over memory.  A code is
+// x / unit rounded to the nearest whole number (IEEE division, ties to even).
 #include <cuda_bf16.h>
 
 #include "launch.cuh"
@@ -50,17 +57,37 @@ __device__ __forceinline__ int axis_of_pair(const RopeParams& p, int i) {
   return a;
 }
 
+// x / unit as a code: whole numbers up to 127, ties to even.  A row's largest
+// |x| gives 127 exactly.  (A row of zeros has unit 0; one that holds an
+// infinity or a NaN an infinite or NaN one, whose product with 0 is NaN: their
+// codes are 0.)
+__device__ __forceinline__ uint32_t code_of(float x, float unit) {
+  const float r = rintf(__fdiv_rn(x, unit));
+  return (uint32_t)(int)fminf(fmaxf(r, -127.f), 127.f) & 255;
+}
+
 // Stores a piece: rounded from f, or, for a bf16 destination whose channels
-// are not rotated, as it was loaded, so that a NaN keeps its bits.
-__device__ __forceinline__ void store_piece(void* cache, int64_t elem, const float* f, bool fp8,
-                                            float scale, const uint4& loaded, bool rotated) {
-  if (!fp8) {
+// are unchanged, as it was loaded, so that a NaN keeps its bits.
+template <KvFormat F>
+__device__ __forceinline__ void store_piece(void* cache, int64_t elem, const float* f, float scale,
+                                            const uint4& loaded, bool changed) {
+  if constexpr (F == kBf16) {
     uint4 w;
-    w.x = rotated ? pack_bf16x2_rn(f[0], f[1]) : loaded.x;
-    w.y = rotated ? pack_bf16x2_rn(f[2], f[3]) : loaded.y;
-    w.z = rotated ? pack_bf16x2_rn(f[4], f[5]) : loaded.z;
-    w.w = rotated ? pack_bf16x2_rn(f[6], f[7]) : loaded.w;
+    w.x = changed ? pack_bf16x2_rn(f[0], f[1]) : loaded.x;
+    w.y = changed ? pack_bf16x2_rn(f[2], f[3]) : loaded.y;
+    w.z = changed ? pack_bf16x2_rn(f[4], f[5]) : loaded.z;
+    w.w = changed ? pack_bf16x2_rn(f[6], f[7]) : loaded.w;
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + elem) = w;
+  } else if constexpr (F == kInt8) {
+    uint2 w = make_uint2(0, 0);
+    if (scale > 0.f && scale < INFINITY) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w.x |= code_of(f[i], scale) << (8 * i);
+        w.y |= code_of(f[4 + i], scale) << (8 * i);
+      }
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + elem) = w;
   } else {
     uint32_t h[4];
 #pragma unroll
@@ -77,14 +104,31 @@ __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
   x = u;
 }
 
-template <int D, bool FP8, int kUnroll>
+// Over the kCols neighbouring threads that hold a head between them.
+template <int kCols>
+__device__ __forceinline__ float head_sum(float x) {
+#pragma unroll
+  for (int d = 1; d < kCols; d *= 2) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+template <int kCols>
+__device__ __forceinline__ uint32_t head_max(uint32_t x) {
+#pragma unroll
+  for (int d = 1; d < kCols; d *= 2) x = max(x, __shfl_xor_sync(0xffffffffu, x, d));
+  return x;
+}
+
+template <int D, KvFormat F, bool NORM, int kUnroll>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
     rope_and_cache_kernel(const __grid_constant__ RopeParams p) {
+  constexpr bool FP8 = F == kE4m3;
+  constexpr bool kTogether = NORM || F == kInt8;  // a head's threads exchange: none leaves early
   constexpr int kCols = D / 16;  // items (two 8-element pieces) per head
   constexpr int kRows = kRopeThreads / kCols;  // heads the CTA takes at a time
   __shared__ __align__(16) float2 s_cs[kRopeMaxTokens][D / 2];
   __shared__ int s_slot[kRopeMaxTokens];
   __shared__ int s_ok[kRopeMaxTokens];
+  __shared__ __align__(16) float s_weight[NORM ? 2 : 1][NORM ? D : 4];  // queries', keys'
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x;
@@ -129,6 +173,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
           ok &= (unsigned)p.positions[x * p.num_tokens + tok] < (unsigned)p.max_position;
         s_ok[tid] = ok;
       }
+      if constexpr (NORM) {
+        for (int i = tid; i < 2 * D; i += kRopeThreads)
+          s_weight[i / D][i % D] = (i < D ? p.q_weight : p.k_weight)[i % D];
+      }
       for (int i = tid; i < ntok * half; i += kRopeThreads) {
         const int t = ntok == 1 ? 0 : i / half, pair = i - t * half;
         const int pos = p.positions[axis_of_pair(p, pair) * p.num_tokens + tok0 + t];
@@ -144,13 +192,32 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int r = base + u * kRows + first;
-      if (r >= rows) continue;
-      const int t = (int)__umulhi((unsigned)r, p.heads_inverse), h = r - t * heads;
-      if (!s_ok[t]) continue;
+      if (!kTogether && r >= rows) continue;
+      const bool there = r < rows;
+      const int t = there ? (int)__umulhi((unsigned)r, p.heads_inverse) : 0;
+      const int h = there ? r - t * heads : 0;
+      if (!kTogether && !s_ok[t]) continue;
+      if (kTogether && !there) a[u] = b[u] = make_uint4(0, 0, 0, 0);
       float x[8], y[8];
       Unpack16<false>::run(a[u], x);
       Unpack16<false>::run(b[u], y);
       const bool turns = h < v0 && turned;
+      const bool changed = turns || (NORM && h < v0);
+      if constexpr (NORM) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += x[i] * x[i] + y[i] * y[i];
+        ss = head_sum<kCols>(ss);
+        if (h < v0) {
+          const float f = 1.f / sqrtf(ss * (1.f / D) + p.eps);
+          const float* w = s_weight[h >= kv0];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] = x[i] * f * w[e0 + i];
+            y[i] = y[i] * f * w[e1 + i];
+          }
+        }
+      }
       if (turns) {
         const float4* cs = reinterpret_cast<const float4*>(&s_cs[t][8 * c]);
         if (p.adjacent) {
@@ -171,31 +238,41 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas)
           }
         }
       }
+      float unit = 0.f;
+      if constexpr (F == kInt8) {
+        // |x| as bits orders like |x|, infinities and then NaNs above all
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          m = max(m, max(__float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(y[i]) & 0x7fffffffu));
+        unit = __fdiv_rn(__uint_as_float(head_max<kCols>(m)), 127.f);
+      }
+      if (kTogether && (!there || !s_ok[t])) continue;
       if (h < kv0) {
         const int64_t row = ((tok0 + t) * kv0 + h) * D;
-        store_piece(p.q_out, row + e0, x, false, 1.f, a[u], turns);
-        store_piece(p.q_out, row + e1, y, false, 1.f, b[u], turns);
+        store_piece<kBf16>(p.q_out, row + e0, x, 1.f, a[u], changed);
+        store_piece<kBf16>(p.q_out, row + e1, y, 1.f, b[u], changed);
       } else {
         const int slot = s_slot[t];
         if (slot < 0 || slot >= p.num_slots) continue;  // padding token or bad slot
         const bool is_v = h >= v0;
-        const int64_t row = ((int64_t)slot * p.num_kv_heads + h - (is_v ? v0 : kv0)) * D;
+        const int64_t at = (int64_t)slot * p.num_kv_heads + h - (is_v ? v0 : kv0);
+        const int64_t row = at * D;
         void* cache = is_v ? p.v_cache : p.k_cache;
-        const float scale = is_v ? vs : ks;
-        store_piece(cache, row + e0, x, FP8, scale, a[u], turns);
-        store_piece(cache, row + e1, y, FP8, scale, b[u], turns);
+        const float scale = F == kInt8 ? unit : (is_v ? vs : ks);
+        store_piece<F>(cache, row + e0, x, scale, a[u], changed);
+        store_piece<F>(cache, row + e1, y, scale, b[u], changed);
+        if (F == kInt8 && c == 0) (is_v ? p.v_units : p.k_units)[at] = unit;
       }
     }
   }
 }
 
-}  // namespace
-
-cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, int num_sms,
-                                  cudaStream_t stream) {
+template <int D, KvFormat F, bool NORM>
+cudaError_t launch(RopeParams p, int num_sms, cudaStream_t stream) {
   // tokens per CTA: enough items for every thread's loads in flight
   const int heads = p.num_heads + 2 * p.num_kv_heads;
-  const int64_t per_token = (int64_t)heads * (head_dim / 16);
+  const int64_t per_token = (int64_t)heads * (D / 16);
   int64_t t = kRopeThreads * kRopeUnroll / per_token;
   t = t < 1 ? 1 : (t > kRopeMaxTokens ? kRopeMaxTokens : t);
   // A long call's CTAs take two tokens at least: the wait for positions, then
@@ -215,23 +292,45 @@ cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, int num_
   // item: less work behind each wait (1 token of 48 heads: 2.96 us alone, 1.98
   // by 3; 64 in e4m3 3.63, 2.66; 300 4.04, 3.70; 600 4.95, 5.62, where the
   // CTAs no longer run at once).
-  const int at_once = kRopeThreads / (head_dim / 16);  // heads of a CTA
+  const int at_once = kRopeThreads / (D / 16);  // heads of a CTA
   const int64_t parts = (t * heads + at_once - 1) / at_once;
-  if (ctas * parts <= 6 * num_sms) {
-    const dim3 g(ctas, (unsigned)parts);
-    if (head_dim == 128)
-      return fp8 ? launch_dependent<rope_and_cache_kernel<128, true, 1>>(g, b, 0, stream, 1, p)
-                 : launch_dependent<rope_and_cache_kernel<128, false, 1>>(g, b, 0, stream, 1, p);
-    return fp8 ? launch_dependent<rope_and_cache_kernel<64, true, 1>>(g, b, 0, stream, 1, p)
-               : launch_dependent<rope_and_cache_kernel<64, false, 1>>(g, b, 0, stream, 1, p);
-  }
-  const dim3 g(ctas);
-  constexpr int U = kRopeUnroll;
+  if (ctas * parts <= 6 * num_sms)
+    return launch_dependent<rope_and_cache_kernel<D, F, NORM, 1>>(dim3(ctas, (unsigned)parts), b, 0,
+                                                                  stream, 1, p);
+  return launch_dependent<rope_and_cache_kernel<D, F, NORM, kRopeUnroll>>(dim3(ctas), b, 0, stream,
+                                                                          1, p);
+}
+
+template <int D, KvFormat F>
+cudaError_t launch_norm(const RopeParams& p, int num_sms, cudaStream_t stream) {
+  return p.q_weight ? launch<D, F, true>(p, num_sms, stream) : launch<D, F, false>(p, num_sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_and_cache(RopeParams p, int head_dim, bool fp8, int num_sms,
+                                  cudaStream_t stream) {
   if (head_dim == 128)
-    return fp8 ? launch_dependent<rope_and_cache_kernel<128, true, U>>(g, b, 0, stream, 1, p)
-               : launch_dependent<rope_and_cache_kernel<128, false, U>>(g, b, 0, stream, 1, p);
-  return fp8 ? launch_dependent<rope_and_cache_kernel<64, true, U>>(g, b, 0, stream, 1, p)
-             : launch_dependent<rope_and_cache_kernel<64, false, U>>(g, b, 0, stream, 1, p);
+    return fp8 ? launch<128, kE4m3, false>(p, num_sms, stream)
+               : launch<128, kBf16, false>(p, num_sms, stream);
+  return fp8 ? launch<64, kE4m3, false>(p, num_sms, stream)
+             : launch<64, kBf16, false>(p, num_sms, stream);
+}
+
+cudaError_t launch_norm_rope_and_cache(RopeParams p, int head_dim, KvFormat format, int num_sms,
+                                       cudaStream_t stream) {
+  switch (format) {
+    case kBf16:
+      return head_dim == 128 ? launch_norm<128, kBf16>(p, num_sms, stream)
+                             : launch_norm<64, kBf16>(p, num_sms, stream);
+    case kE4m3:
+      return head_dim == 128 ? launch_norm<128, kE4m3>(p, num_sms, stream)
+                             : launch_norm<64, kE4m3>(p, num_sms, stream);
+    case kInt8:
+      return head_dim == 128 ? launch_norm<128, kInt8>(p, num_sms, stream)
+                             : launch_norm<64, kInt8>(p, num_sms, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace pa

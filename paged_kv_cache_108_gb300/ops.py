@@ -391,6 +391,101 @@ def decode_selected(out, q, k_cache, v_cache, block_tables, context_lens, select
     return out
 
 
+# The scored step's calls, by the compiled binding too.
+
+def alloc_cache_units(k_cache):
+    """(k_scale, v_scale) of an int8 cache [num_blocks, block_size, H_kv, d]:
+    zeroed fp32 [num_blocks, block_size, H_kv] on its device, the units that
+    ``norm_rope_and_cache`` writes."""
+    if k_cache.dim() != 4 or k_cache.dtype != torch.int8:
+        raise ValueError("cache must be int8 [num_blocks, block_size, num_kv_heads, head_dim]")
+    return tuple(torch.zeros(k_cache.shape[:3], dtype=torch.float32, device=k_cache.device)
+                 for _ in range(2))
+
+
+def norm_rope_and_cache(q_out, query, key, value, k_cache, v_cache, slot_mapping, positions=None,
+                        cos_sin=None, q_weight=None, k_weight=None, eps=1e-6, k_scale=None,
+                        v_scale=None, sections=None, sections_in_turn=False, adjacent_pairs=False,
+                        stream=None) -> None:
+    """``rope_and_cache`` with each query and key head normalised first (RMS,
+    weights fp32 [d]; none given: no norm), into a bf16, e4m3 or int8 cache.
+    Without ``positions`` and ``cos_sin`` nothing is rotated.  For an int8
+    cache ``k_scale`` and ``v_scale`` are its units (``alloc_cache_units``),
+    written here."""
+    status = (_lib._binding or _lib.binding()).norm_rope_and_cache(
+        q_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
+        k_weight, eps, k_scale, v_scale, sections, sections_in_turn, adjacent_pairs, stream)
+    if status:
+        _lib.check(status)
+
+
+def gather_cache(k_out, v_out, k_cache, v_cache, block_tables, context_lens, out_start_loc,
+                 first_tokens=None, k_scale=None, v_scale=None, stream=None) -> None:
+    """Reads a cache back: tokens ``first_tokens[i]`` (0) up to
+    ``context_lens[i]`` of sequence i into the rows of ``k_out`` and ``v_out``
+    [num_rows, H_kv, d] (bf16) from ``out_start_loc[i]`` up to
+    ``out_start_loc[i + 1]``.  Rows without a token stay as they were."""
+    status = (_lib._binding or _lib.binding()).gather_cache(
+        k_out, v_out, k_cache, v_cache, block_tables, context_lens, out_start_loc, first_tokens,
+        k_scale, v_scale, stream)
+    if status:
+        _lib.check(status)
+
+
+def scored_workspace_size(num_rows: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(_lib.lib().pa_scored_workspace_size(num_rows, num_heads, num_kv_heads, head_dim))
+
+
+def alloc_scored_workspace(num_rows, num_heads, num_kv_heads, head_dim, device=None):
+    """A caller-owned device workspace for ``decode_scored`` (``num_rows``
+    sequences) or ``varlen_scored`` (``num_rows`` new tokens)."""
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):  # the size goes by the device's SMs
+        n = scored_workspace_size(num_rows, num_heads, num_kv_heads, head_dim)
+        return torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+
+
+def _scored_workspace(workspace, q, k_cache, stream):
+    if workspace is not None or not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+        return workspace  # (what is wrong is refused by the binding)
+    if stream is None:
+        side = torch.cuda.current_stream(q.device)
+    else:  # allocated on the stream that uses it, so that its memory is not handed on before
+        side = (stream if isinstance(stream, torch.cuda.Stream)
+                else torch.cuda.ExternalStream(int(stream), device=q.device))
+    with torch.cuda.stream(side):
+        return alloc_scored_workspace(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2],
+                                      q.device)
+
+
+def decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, scale, cap=0.0, window=0,
+                  slopes=None, k_scale=None, v_scale=None, workspace=None, stream=None):
+    """``decode`` with changed scores, over a bf16, e4m3 or int8 cache: capped
+    by ``cap`` tanh(s / ``cap``), less ``slopes`` (fp32 [H_q]) times the
+    distance, over the last ``window`` tokens; writes ``out`` [B_s, H_q, d]
+    bf16 and returns it."""
+    status = (_lib._binding or _lib.binding()).decode_scored(
+        out, q, k_cache, v_cache, block_tables, context_lens, scale, cap, window, slopes, k_scale,
+        v_scale, _scored_workspace(workspace, q, k_cache, stream), stream)
+    if status:
+        _lib.check(status)
+    return out
+
+
+def varlen_scored(out, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale,
+                  cap=0.0, window=0, slopes=None, prefix_lens=None, k_scale=None, v_scale=None,
+                  workspace=None, stream=None):
+    """``varlen_attention`` with ``decode_scored``'s scores; new tokens below
+    ``prefix_lens[i]`` of their sequence also see every token below it."""
+    status = (_lib._binding or _lib.binding()).varlen_scored(
+        out, q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, scale, cap, window,
+        slopes, prefix_lens, k_scale, v_scale, _scored_workspace(workspace, q, k_cache, stream),
+        stream)
+    if status:
+        _lib.check(status)
+    return out
+
+
 class StepGraph:
     """One decode step captured once as a CUDA graph over fixed buffers.
 
