@@ -740,8 +740,8 @@ size_t pa_scored_workspace_size(int32_t num_rows, int32_t num_heads, int32_t num
  *  workspace     >= pa_scored_workspace_size(num_seqs, ...) bytes, 256-byte
  *                aligned.
  *  Limits: num_heads / num_kv_heads in {1, 2, 4, 8}; max_blocks_per_seq *
- *  block_size up to 2^30; num_seqs * num_kv_heads up to 2^27; else
- *  PA_ERR_UNSUPPORTED.  A block outside the pool is passed over.
+ *  block_size up to 2^30; num_kv_heads up to 32768; num_seqs * num_kv_heads
+ *  up to 2^27; else PA_ERR_UNSUPPORTED.  A block outside the pool is passed over.
  *  num_seqs == 0 is valid and launches nothing.
  *  Other arguments as pa_decode. */
 pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const void* v_cache,

@@ -322,6 +322,7 @@ pa_status scored_rows(const char* fn, void* out, const void* q, const void* k_ca
   // (with starts a row's sequence is known on the device alone)
   if ((st = check_rows(cache, max_blocks, starts, num_rows, num_seqs, num_heads, fn)) != PA_OK)
     return st;
+  if (cache.num_kv_heads > 32768) return fail(PA_ERR_UNSUPPORTED, "num_kv_heads above 32768");
   pa::ScoreMod mod;
   if ((st = check_score(score, scale, max_blocks, cache.block_size, fn, &mod)) != PA_OK) return st;
   mod.prefix_lens = prefix_lens;
@@ -374,6 +375,7 @@ pa_status scored_rows(const char* fn, void* out, const void* q, const void* k_ca
   p.block_tables = block_tables;
   p.lens = lens;
   p.starts = starts;
+  p.err = static_cast<int*>(workspace);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.num_rows = num_rows;

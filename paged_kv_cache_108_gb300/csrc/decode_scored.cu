@@ -10,15 +10,16 @@
 // once.  end is i + 1, or the sequence's prefix for a row inside it.
 //
 // Bound: the visible tokens' bytes (at G = 4, 4 flop a byte in bf16, 8 in 8
-// bits).  Each warp streams 16-token chunks through a cp.async ring of its own
+// bits).  Each warp streams chunks of 16 or 32 tokens through a cp.async ring of its own
 // and keeps its own softmax state, as in the decode over listed blocks:
 //   S^T [16 tokens x 8 columns] = K q^T     (mma m16n8k16, K by ldmatrix)
 //   O^T [D x 8 columns] += V^T P^T          (V by ldmatrix.trans)
-// with the query heads in the 8 columns; for G <= 4 columns 4..7 repeat the
-// heads and carry what rounding takes from P, for G = 8 a second MMA does.
-// 8-bit elements are widened to f16 in registers (exact); q then enters in
-// f16 under a power of two per head, and P is raised by 2^14 (f16 ends at
-// 2^-24).  The unit of an 8-bit row multiplies its logit, and its weight in
+// with the query heads in the 8 columns.  Over bf16, columns 4..7 repeat the
+// heads for G <= 4 and carry what rounding takes from P, for G = 8 a second
+// MMA does.  8-bit elements are widened to f16 in registers (exact); q then
+// enters in f16 under a power of two per head, and P is raised by 2^14 (f16
+// ends at 2^-24) and rounded once: up to 2^-11 of a weight, an eighth of
+// the output's own rounding.  The unit of an 8-bit row multiplies its logit, and its weight in
 // P V, relative to the largest unit the warp has met (a running maximum like
 // the softmax's), so that f16 holds those products whatever the units' size.
 //
@@ -26,13 +27,19 @@
 // off by about 2^-22 of the cap.
 //
 // Work split: a unit is a (row, KV head); its visible tokens are cut into
-// steps of one chunk per warp, and the steps of all units in a row, K in all,
-// into equal ranges, one for each CTA that runs at once, whatever the lengths.
-// Loads run ahead across the ends of units.  A CTA's range splits at most two
+// steps of one chunk per warp, and the steps of all rows, K in all, into equal
+// ranges, whatever the lengths.  Each range is taken by H_kv neighbouring CTAs,
+// one a head, as many in all as run at once: they read the same tokens at the
+// same time, whose heads lie side by side (with ranges over the units' steps in
+// a row, heads far apart, 8 e4m3 rows of 64 K tokens took 152 us).  Loads run
+// ahead across the ends of units.  A CTA's range splits at most two
 // units (the one it starts in, the one it ends in): their partial sums go to
-// the workspace, and the last CTA to arrive at a unit adds them up in order of
-// their CTAs, so the result does not depend on who is last.  Where units are
-// many times the CTAs (kWholeUnits), each CTA takes one whole unit.
+// the workspace, and the CTA that holds the unit's end, once its own range is
+// done, waits for the others' flags and adds the parts up in their order.  (A
+// counter of arrivals, exchanged with the call's tag, made 38 CTAs of one unit
+// queue for it: one int8 row of 16 K tokens 41 us.)  Flags carry a tag of the
+// call, so the workspace needs no initialisation.  Where units are many times
+// the CTAs (kWholeUnits), each CTA takes one whole unit.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -47,17 +54,17 @@ namespace pa {
 
 namespace {
 
-constexpr int kChunk = 16;        // tokens a warp handles at a time
 constexpr int kCtasPerSm = 2;     // what registers and shared memory are kept to
 constexpr int kWholeUnits = 6;    // units per CTA from which none is split
-constexpr int kMinSteps = 2;      // steps of a CTA at least, where units are split
+constexpr int kMinSteps = 1;      // steps of a CTA at least, where units are split
 
-template <int D, KvFormat F>
+template <int D, int G, KvFormat F>
 struct Cfg {
   static constexpr int kRow = D * (F == kBf16 ? 2 : 1);  // bytes of a token's channels
   static constexpr int kPieces = kRow / 16;
+  static constexpr int kChunk = F == kBf16 ? 16 : 32;  // tokens a warp handles at a time
   static constexpr int kTile = kChunk * kRow;  // K (or V) bytes of a chunk
-  static constexpr int kWarps = F == kBf16 ? 4 : 8;
+  static constexpr int kWarps = F == kBf16 ? 4 : (D == 64 ? 8 : (G > 4 ? 5 : 6));
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = F == kBf16 ? 3 : 2;
   static constexpr int kUnits = F == kInt8 ? 2 * kChunk * 4 : 0;  // bytes of a chunk's units
@@ -95,6 +102,15 @@ __device__ __forceinline__ uint32_t widen_alternate(uint32_t w, bool odd) {
     return widen_int8(w, odd ? 0x4341 : 0x4240);
   else
     return widen((uint16_t)__byte_perm(w, 0, odd ? 0x4431 : 0x4420));
+}
+
+__device__ __forceinline__ void st_release(unsigned long long* p, unsigned long long v) {
+  asm volatile("st.release.gpu.u64 [%0], %1;\n" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ unsigned long long ld_acquire(const unsigned long long* p) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.u64 %0, [%1];\n" : "=l"(v) : "l"(p) : "memory");
+  return v;
 }
 
 // The factor of a part whose running max is m under the whole's max; 1 where
@@ -147,103 +163,123 @@ __device__ __forceinline__ Row row_of(const ScoredParams& p, int row) {
   r.first = min(r.first, r.end);
   return r;
 }
-// Tokens are visited from a multiple of the chunk on.
-__device__ __forceinline__ int first_chunk(const Row& r) { return r.first & ~(kChunk - 1); }
+// Tokens are visited from a multiple of 16 on.
+__device__ __forceinline__ int first_visited(int first) { return first & ~15; }
 template <int kStep>
 __device__ __forceinline__ int steps_of(const Row& r) {
-  const int n = r.end - first_chunk(r);
+  const int n = r.end - first_visited(r.first);
   return n <= 0 ? 1 : (n + kStep - 1) / kStep;  // a row without keys has its zeros written
 }
 
+// (whole 16-byte pieces)
+constexpr int part_words(int group, int head_dim) { return (group * (head_dim + 2) + 4) / 4 * 4; }
+
 // What a warp knows of a chunk that it has asked for.
 struct __align__(16) Chunk {
-  int row, kvh, tok, first;
-  int seen, pos, flags, steps;  // seen: a bit per token; steps: of the unit
+  int row, tok, first;
+  unsigned seen;  // a bit per token
+  int pos, flags, steps, none;  // steps: of the unit
 };
 enum { kOpens = 1, kCloses = 2, kNobody = 4 };
 
 template <int D, int G, KvFormat F>
-__global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
     decode_scored_kernel(const __grid_constant__ ScoredParams p, bool whole_units) {
-  using C = Cfg<D, F>;
+  using C = Cfg<D, G, F>;
   constexpr bool F16 = F != kBf16;
-  constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads, kChunk = C::kChunk;
+  constexpr int kGroups = kChunk / 16;    // 16-token MMA tiles of a chunk
   constexpr int kStep = kWarps * kChunk;  // tokens of a step
   constexpr int kSteps = D / 16;          // k16 steps of q . k; m16 tiles of O^T
   constexpr int kColHeads = G <= 4 ? 4 : 8;
-  constexpr int kPart = G * (D + 2) + 1;  // a partial: sums, then max and sum per head, unit
+  constexpr int kPart = part_words(G, D);  // a partial: sums, then max and sum per head, unit
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Chunk s_chunk[kWarps][C::kStages];
+  constexpr int kInfos = 4;  // steps asked for at a time, at most: kStages + 1
+  static_assert(C::kStages < kInfos, "");
+  __shared__ Chunk s_chunk[kWarps][kInfos];
   __shared__ float s_o[kWarps][kColHeads][D];
   __shared__ float s_ml[kWarps][kColHeads][2];
   __shared__ float s_unit[kWarps];
-  __shared__ long long s_sum[kWarps], s_before;
-  __shared__ int s_row, s_last;
+  __shared__ long long s_sum[kWarps], s_others[kWarps], s_before;
+  __shared__ Row s_cur;
+  __shared__ float s_factor[kWarps][G], s_max[G], s_l[G], s_post[G];
+  __shared__ int s_row;
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int g = lane / 4, c = lane % 4;  // MMA fragment coordinates
   const int hkv = p.num_kv_heads;
 
-  // ---- this CTA's range of steps: [lo, hi) of K, from step `at` of a unit ----
+  // ---- this CTA's head and range of steps: [lo, hi) of K, from step `at` of a row ----
+  const int part = blockIdx.x / hkv, kvh = blockIdx.x - part * hkv;
   long long K = 0, lo = 0, hi = 0;
-  int ctas = 1, row = 0, kvh = 0, at = 0;
+  int ctas = 1, row = 0, at = 0;  // ctas: those of a head
   Row cur;
   if (whole_units) {
-    row = blockIdx.x / hkv;
-    kvh = blockIdx.x - row * hkv;
+    row = part;
     cur = row_of(p, row);
     hi = K = steps_of<kStep>(cur);
   } else {
-    long long sum = 0;
-    for (int r = tid; r < p.num_rows; r += kThreads) sum += steps_of<kStep>(row_of(p, r));
-    for (int d = 16; d; d /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) K += s_sum[w];
-    K *= hkv;
-    ctas = (int)min((long long)gridDim.x, max(1ll, K / kMinSteps));
-    if ((int)blockIdx.x >= ctas) return;
-    lo = tc::range_lo(blockIdx.x, K, ctas);
-    hi = tc::range_lo(blockIdx.x + 1, K, ctas);
-    // the row that step lo lies in
+    // K, and (rows in tiles of one a thread) the row that step lo lies in
+    Row mine = {-1, 0, 0, 0};
+    int n = 0;  // steps of this thread's row
+    long long others = 0;
+    for (int r = tid + kThreads; r < p.num_rows; r += kThreads) others += steps_of<kStep>(row_of(p, r));
     long long before = 0;
     for (int base = 0; base < p.num_rows; base += kThreads) {
-      const int r = base + tid;
-      const long long n = r < p.num_rows ? (long long)steps_of<kStep>(row_of(p, r)) * hkv : 0;
-      long long incl = n;
-      for (int d = 1; d < 32; d *= 2) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
+      n = 0;
+      if (base + tid < p.num_rows) {
+        mine = row_of(p, base + tid);
+        n = steps_of<kStep>(mine);
       }
-      __syncthreads();  // s_sum is free
-      if (lane == 31) s_sum[warp] = incl;
+      long long wide = n;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const long long up = __shfl_up_sync(0xffffffffu, wide, d);
+        if (lane >= d) wide += up;
+      }
+      if (base == 0) {
+#pragma unroll
+        for (int d = 16; d; d /= 2) others += __shfl_xor_sync(0xffffffffu, others, d);
+      } else {
+        __syncthreads();  // s_sum is free
+      }
+      if (lane == 31) s_sum[warp] = wide;
+      if (base == 0 && lane == 0) s_others[warp] = others;
       if (tid == 0) s_row = -1;
       __syncthreads();
-      long long mine = before + incl - n, end = before;
+      long long start = before + wide - n, end = before;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) mine += s_sum[w];
+        if (w < warp) start += s_sum[w];
         end += s_sum[w];
       }
-      if (mine <= lo && lo < mine + n) {
-        s_row = r;
-        s_before = mine;
+      if (base == 0) {
+        K = end;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) K += s_others[w];
+        ctas = (int)min((long long)(gridDim.x / hkv), max(1ll, K / kMinSteps));
+        if (part >= ctas) return;
+        lo = tc::range_lo(part, K, ctas);
+        hi = tc::range_lo(part + 1, K, ctas);
+      }
+      if (start <= lo && lo < start + n) {
+        s_row = base + tid;
+        s_before = start;
+        s_cur = mine;
       }
       __syncthreads();
       if (s_row >= 0) break;
       before = end;
     }
     row = s_row;
-    cur = row_of(p, row);
-    const int n = steps_of<kStep>(cur);
-    const long long in = lo - s_before;
-    kvh = (int)(in / n);
-    at = (int)(in - (long long)kvh * n);
+    cur = s_cur;
+    at = (int)(lo - s_before);
   }
   const int total = (int)(hi - lo);
 
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage;
-  const int64_t stride = (int64_t)hkv * C::kRow;  // between tokens
+  const int stride = hkv * C::kRow;  // between tokens: bytes, below 2^24
   const int lb = p.log2_block_size;
   float ks = 1.f, post = 1.f;  // e4m3's scales
   if constexpr (F == kE4m3) {
@@ -251,67 +287,73 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
     post = *p.v_scale;
   }
 
-  // ---- loads: the chunk of step `asked`, and the slot of the one behind it ----
+  // ---- loads.  ask() looks up the slot of this lane's token of the cursor's
+  // chunk (-1: none) and goes on to the next; load_keys() and load_values() of
+  // the step then need no other address ----
   int asked = 0;
-  auto slot_of = [&]() -> int {  // of this lane's token of the cursor's chunk
-    const int tok = first_chunk(cur) + (at * kWarps + warp) * kChunk + (lane & 15);
-    if (asked >= total || tok < cur.first || tok >= cur.end) return -1;
-    const int phys = p.block_tables[(int64_t)cur.seq * p.max_blocks + (tok >> lb)];
-    return (unsigned)phys < (unsigned)p.num_blocks ? (phys << lb) + (tok & ((1 << lb) - 1)) : -1;
+  auto ask = [&]() -> int {
+    if (asked >= total) return -1;
+    const int n = steps_of<kStep>(cur);
+    const int tok0 = first_visited(cur.first) + (at * kWarps + warp) * kChunk;
+    if (lane == 0) {
+      Chunk& k = s_chunk[warp][asked % kInfos];
+      k.row = row;
+      k.tok = tok0;
+      k.first = cur.first;
+      k.pos = cur.pos;
+      k.steps = n;
+      k.flags = (asked == 0 || at == 0 ? kOpens : 0) |
+                (asked == total - 1 || at == n - 1 ? kCloses : 0) |
+                // a row of no sequence: nothing is written
+                (cur.seq < 0 ? kNobody : 0);
+    }
+    const int tok = tok0 + (lane & (kChunk - 1));
+    int slot = -1;
+    if (tok >= cur.first && tok < cur.end) {
+      const int phys = p.block_tables[(int64_t)cur.seq * p.max_blocks + (tok >> lb)];
+      if ((unsigned)phys < (unsigned)p.num_blocks) slot = (phys << lb) + (tok & ((1 << lb) - 1));
+    }
+    ++asked;
+    if (++at == n) {
+      at = 0;
+      ++row;
+      if (asked < total) cur = row_of(p, row);
+    }
+    return slot;
   };
-  int slot = slot_of();
-  auto load = [&]() {
-    if (asked < total) {
-      const int n = steps_of<kStep>(cur);
-      const int st = asked % C::kStages;
-      const uint32_t stage = ring + st * C::kStage;
-      const unsigned seen = __ballot_sync(0xffffffffu, slot >= 0) & 0xffff;
-      if (lane == 0) {
-        Chunk& k = s_chunk[warp][st];
-        k.row = row;
-        k.kvh = kvh;
-        k.tok = first_chunk(cur) + (at * kWarps + warp) * kChunk;
-        k.first = cur.first;
-        k.seen = (int)seen;
-        k.pos = cur.pos;
-        k.steps = n;
-        k.flags = (asked == 0 || at == 0 ? kOpens : 0) |
-                  (asked == total - 1 || at == n - 1 ? kCloses : 0) |
-                  // a row of no sequence: nothing is written
-                  (cur.seq < 0 ? kNobody : 0);
-      }
-      const uint8_t* kbase = static_cast<const uint8_t*>(p.k_cache) + (int64_t)kvh * C::kRow;
-      const uint8_t* vbase = static_cast<const uint8_t*>(p.v_cache) + (int64_t)kvh * C::kRow;
-      constexpr int kRowsPer = 32 / C::kPieces;  // tokens per instruction
-      const int piece = lane % C::kPieces;
+  constexpr int kRowsPer = 32 / C::kPieces;  // tokens per instruction
+  const int piece = lane % C::kPieces;
+  const int64_t lane_at = (int64_t)kvh * C::kRow + piece * 16;
+  const uint8_t* const kbase = static_cast<const uint8_t*>(p.k_cache) + lane_at;
+  const uint8_t* const vbase = static_cast<const uint8_t*>(p.v_cache) + lane_at;
+  auto load_rows = [&](uint32_t to, const uint8_t* base, int slot) {
 #pragma unroll
-      for (int r = 0; r < kChunk / kRowsPer; ++r) {
-        const int t = r * kRowsPer + lane / C::kPieces;
-        const int s = __shfl_sync(0xffffffffu, slot, t);
-        const int64_t from = (int64_t)max(s, 0) * stride + piece * 16;
-        const uint32_t dst = stage + t * C::kRow + C::swizzle(t, piece) * 16;
-        cp_async_16(dst, kbase + from, s >= 0 ? 16 : 0);  // zeros where there is no token
-        cp_async_16(dst + C::kTile, vbase + from, s >= 0 ? 16 : 0);
-      }
-      if constexpr (F == kInt8) {  // units: the keys' by lanes 0..15, the values' by 16..31
-        const float* u = lane < 16 ? p.k_scale : p.v_scale;
-        const uint32_t dst = stage + 2 * C::kTile + lane * 4;
-        if (slot >= 0)
-          cp_async_4(dst, u + (int64_t)slot * hkv + kvh);
-        else
-          asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(dst), "f"(0.f) : "memory");
-      }
-      // the next step's cursor
-      ++asked;
-      if (++at == n) {
-        at = 0;
-        if (++kvh == hkv) {
-          kvh = 0;
-          ++row;
-          if (asked < total) cur = row_of(p, row);
-        }
-      }
-      slot = slot_of();
+    for (int r = 0; r < kChunk / kRowsPer; ++r) {
+      const int t = r * kRowsPer + lane / C::kPieces;
+      const int s = __shfl_sync(0xffffffffu, slot, t);
+      cp_async_16(to + t * C::kRow + C::swizzle(t, piece) * 16, base + (int64_t)max(s, 0) * stride,
+                  s >= 0 ? 16 : 0);  // zeros where there is no token
+    }
+  };
+  auto load_units = [&](uint32_t to, const float* units, int slot) {
+    cp_async_4_or_zero(to + lane * 4, units + (int64_t)max(slot, 0) * hkv + kvh, slot >= 0 ? 4 : 0);
+  };
+  auto load_keys = [&](int step, int slot) {
+    if (step < total) {
+      unsigned seen = __ballot_sync(0xffffffffu, slot >= 0);
+      if constexpr (kChunk == 16) seen &= 0xffff;
+      if (lane == 0) s_chunk[warp][step % kInfos].seen = seen;
+      const uint32_t stage = ring + step % C::kStages * C::kStage;
+      load_rows(stage, kbase, slot);
+      if constexpr (F == kInt8) load_units(stage + 2 * C::kTile, p.k_scale, slot);
+    }
+    cp_async_commit();
+  };
+  auto load_values = [&](int step, int slot) {
+    if (step < total) {
+      const uint32_t stage = ring + step % C::kStages * C::kStage;
+      load_rows(stage + C::kTile, vbase, slot);
+      if constexpr (F == kInt8) load_units(stage + 2 * C::kTile + 4 * kChunk, p.v_scale, slot);
     }
     cp_async_commit();
   };
@@ -322,8 +364,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
   uint2 qw[kSteps];
   uint32_t qb[kSteps][2];
   float f0 = 0.f, f1 = 0.f, slope0 = 0.f, slope1 = 0.f;
-  auto fetch_q = [&](int unit_row, int unit_kvh) {
-    const int64_t unit = (int64_t)unit_row * hkv + unit_kvh;
+  auto fetch_q = [&](int unit_row) {
+    const int64_t unit = (int64_t)unit_row * hkv + kvh;
     const __nv_bfloat16* q = p.q + (unit * G + qh) * D;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
@@ -340,8 +382,8 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
     if (p.mod.slopes) {
       const int h0 = (2 * c) % kColHeads, h1 = (2 * c + 1) % kColHeads;
       constexpr float kLog2e = 1.4426950408889634f;
-      slope0 = h0 < G ? p.mod.slopes[unit_kvh * G + h0] * kLog2e : 0.f;
-      slope1 = h1 < G ? p.mod.slopes[unit_kvh * G + h1] * kLog2e : 0.f;
+      slope0 = h0 < G ? p.mod.slopes[kvh * G + h0] * kLog2e : 0.f;
+      slope1 = h1 < G ? p.mod.slopes[kvh * G + h1] * kLog2e : 0.f;
     }
   };
   auto place_q = [&]() {
@@ -386,24 +428,55 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
     unit_inverse = 1.f / kLeastUnit;
   };
 
-  fetch_q(row, kvh);
+  // Two outputs.  The division first: x and y are sums over all tokens, and
+  // the factor may bring them past the largest float where the result is in
+  // range.
+  auto store = [&](int64_t at, float x, float y, float l, float factor) {
+    if (l == 0.f) x = y = 0.f;
+    else x = x / l * factor, y = y / l * factor;
+    *reinterpret_cast<uint32_t*>(p.out + at) = pack_bf16x2_rn(x, y);
+  };
+
+  int64_t merge_unit = -1;  // the split unit whose end this CTA holds, and
+  long long merge_start = 0;  // the first of its steps
+  fetch_q(row);
+  int slot;  // of the step that is loaded next
+  {
+    int early[C::kStages];
 #pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) load();
+    for (int s = 0; s < C::kStages; ++s) early[s] = ask();
+    slot = ask();
+#pragma unroll
+    for (int s = 0; s < C::kStages; ++s) {
+      load_keys(s, early[s]);
+      load_values(s, early[s]);
+    }
+  }
+  // groups behind a step's keys, or behind its values with the keys that took
+  // their place in between
+  constexpr int kBehind = 2 * C::kStages - 1;
   for (int it = 0; it < total; ++it) {
-    load();
-    cp_async_wait<C::kStages - 1>();
+    cp_async_wait<kBehind>();
     __syncwarp();
-    const Chunk ch = s_chunk[warp][it % C::kStages];
+    const Chunk ch = s_chunk[warp][it % kInfos];
     if (ch.flags & kOpens) {
       place_q();
       open();
     }
     const uint32_t kt = ring + (it % C::kStages) * C::kStage;
     const uint32_t vt = kt + C::kTile;
+    // logits of tokens g, g + 8, g + 16 ... of the chunk, columns 2c and 2c + 1
+    float x[2 * kGroups][2];
+    const float* units = reinterpret_cast<const float*>(
+        smem + (warp * C::kStages + it % C::kStages) * C::kStage + 2 * C::kTile);
     if (ch.seen) {
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
-      {
-        const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
+      float ku[2 * kGroups];
+#pragma unroll
+      for (int i = 0; i < 2 * kGroups; ++i) ku[i] = F == kInt8 ? units[g + 8 * i] : 1.f;
+#pragma unroll
+      for (int gr = 0; gr < kGroups; ++gr) {
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        const int r = 16 * gr + (lane & 7) + ((lane >> 3) & 1) * 8;
         const uint32_t base = kt + r * C::kRow;
         if constexpr (F16) {
 #pragma unroll
@@ -412,9 +485,9 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
             ldmatrix_x4(w, base + C::swizzle(r, k + (lane >> 4)) * 16);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // the two 16-channel pieces
-              const uint32_t x = w[2 * h], y = w[2 * h + 1];
-              const uint32_t a[4] = {widen_half<F>(x, false), widen_half<F>(y, false),
-                                     widen_half<F>(x, true), widen_half<F>(y, true)};
+              const uint32_t y = w[2 * h], z = w[2 * h + 1];
+              const uint32_t a[4] = {widen_half<F>(y, false), widen_half<F>(z, false),
+                                     widen_half<F>(y, true), widen_half<F>(z, true)};
               mma16816<true>(s, a, qb[k + h][0], qb[k + h][1]);
             }
           }
@@ -426,38 +499,57 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
             mma16816<false>(s, a, qb[k][0], qb[k][1]);
           }
         }
+        x[2 * gr][0] = s[0];
+        x[2 * gr][1] = s[1];
+        x[2 * gr + 1][0] = s[2];
+        x[2 * gr + 1][1] = s[3];
       }
-      // tokens g and g + 8 of the chunk, columns 2c and 2c + 1
-      const int t0 = ch.tok + g, t1 = t0 + 8;
-      float x[4] = {s[0] * f0, s[1] * f1, s[2] * f0, s[3] * f1};
-      float vu0 = 1.f, vu1 = 1.f;
       if constexpr (F == kInt8) {
-        const float* u = reinterpret_cast<const float*>(
-            smem + (warp * C::kStages + it % C::kStages) * C::kStage + 2 * C::kTile);
-        x[0] *= u[g];
-        x[1] *= u[g];
-        x[2] *= u[g + 8];
-        x[3] *= u[g + 8];
-        vu0 = u[16 + g];
-        vu1 = u[16 + g + 8];
-      }
-      if (p.mod.cap_log2 > 0.f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[i] = p.mod.cap_log2 *
-                 (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(x[i] * p.mod.inv_cap_log2)));
+        for (int i = 0; i < 2 * kGroups; ++i) {
+          x[i][0] *= ku[i];
+          x[i][1] *= ku[i];
+        }
+      }
+    }
+    float n0 = -INFINITY, n1 = -INFINITY;  // each column's largest logit so far
+    __syncwarp();
+    load_keys(it + C::kStages, slot);  // in the place of the keys just used
+    if (ch.seen) {
+      if (p.mod.cap_log2 > 0.f) {
+        const float e0 = f0 * p.mod.inv_cap_log2, e1 = f1 * p.mod.inv_cap_log2;
+#pragma unroll
+        for (int i = 0; i < 2 * kGroups; ++i) {
+          x[i][0] = p.mod.cap_log2 * (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(x[i][0] * e0)));
+          x[i][1] = p.mod.cap_log2 * (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(x[i][1] * e1)));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * kGroups; ++i) {
+          x[i][0] *= f0;
+          x[i][1] *= f1;
+        }
       }
       if (p.mod.slopes) {
-        const float d0 = (float)abs(ch.pos - t0), d1 = (float)abs(ch.pos - t1);
-        x[0] -= slope0 * d0;
-        x[1] -= slope1 * d0;
-        x[2] -= slope0 * d1;
-        x[3] -= slope1 * d1;
+#pragma unroll
+        for (int i = 0; i < 2 * kGroups; ++i) {
+          const float d = (float)abs(ch.pos - (ch.tok + g + 8 * i));
+          x[i][0] -= slope0 * d;
+          x[i][1] -= slope1 * d;
+        }
       }
-      const bool in0 = ch.seen >> g & 1, in1 = ch.seen >> (g + 8) & 1;
-      const float x00 = in0 ? x[0] : -INFINITY, x01 = in0 ? x[1] : -INFINITY;
-      const float x10 = in1 ? x[2] : -INFINITY, x11 = in1 ? x[3] : -INFINITY;
-      float n0 = fmaxf(x00, x10), n1 = fmaxf(x01, x11);
+      if (ch.seen != (kChunk == 32 ? 0xffffffffu : 0xffffu)) {
+#pragma unroll
+        for (int i = 0; i < 2 * kGroups; ++i)
+          if (!(ch.seen >> (g + 8 * i) & 1)) x[i][0] = x[i][1] = -INFINITY;
+      }
+      n0 = x[0][0];
+      n1 = x[0][1];
+#pragma unroll
+      for (int i = 1; i < 2 * kGroups; ++i) {
+        n0 = fmaxf(n0, x[i][0]);
+        n1 = fmaxf(n1, x[i][1]);
+      }
 #pragma unroll
       for (int d = 4; d < 32; d *= 2) {
         n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, d));
@@ -465,10 +557,17 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
       }
       n0 = fmaxf(n0, m0);
       n1 = fmaxf(n1, m1);
+    }
+    cp_async_wait<kBehind>();
+    __syncwarp();
+    if (ch.seen) {
       float grown = unit_max;
+      float vu[2 * kGroups];
+#pragma unroll
+      for (int i = 0; i < 2 * kGroups; ++i) vu[i] = F == kInt8 ? units[kChunk + g + 8 * i] : 1.f;
       if constexpr (F == kInt8) {
-        const uint32_t most =
-            __reduce_max_sync(0xffffffffu, max(__float_as_uint(vu0), __float_as_uint(vu1)));
+        // (every lane's own token's)
+        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(units[kChunk + lane]));
         grown = larger_unit(unit_max, __uint_as_float(most));
       }
       if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1) || (F == kInt8 && grown != unit_max)) {
@@ -492,68 +591,79 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
         m0 = n0;
         m1 = n1;
       }
-      constexpr float kRaise = F16 ? 16384.f : 1.f;  // the factor that P and its sum carry
-      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-      float p00 = fast_exp2(x00 - z0) * kRaise, p01 = fast_exp2(x01 - z1) * kRaise;
-      float p10 = fast_exp2(x10 - z0) * kRaise, p11 = fast_exp2(x11 - z1) * kRaise;
-      l0 += p00 + p10;
-      l1 += p01 + p11;
+      constexpr float kRaise = F16 ? 14.f : 0.f;  // log2 of the factor that P and its sum carry
+      const float z0 = (m0 == -INFINITY ? 0.f : m0) - kRaise;
+      const float z1 = (m1 == -INFINITY ? 0.f : m1) - kRaise;
+#pragma unroll
+      for (int i = 0; i < 2 * kGroups; ++i) {
+        x[i][0] = fast_exp2(x[i][0] - z0);
+        x[i][1] = fast_exp2(x[i][1] - z1);
+        l0 += x[i][0];
+        l1 += x[i][1];
+      }
       if constexpr (F == kInt8) {
-        const float w0 = vu0 * unit_inverse, w1 = vu1 * unit_inverse;
-        p00 *= w0;
-        p01 *= w0;
-        p10 *= w1;
-        p11 *= w1;
-      }
-      uint32_t hi0 = pack2<F16>(p00, p01), hi1 = pack2<F16>(p10, p11);
-      const float2 r0 = unpack2<F16>(hi0), r1 = unpack2<F16>(hi1);
-      uint32_t lo0 = pack2<F16>(p00 - r0.x, p01 - r0.y), lo1 = pack2<F16>(p10 - r1.x, p11 - r1.y);
-      if constexpr (G <= 4) {  // columns 4..7 carry the remainders
-        if (c >= 2) {
-          hi0 = lo0;
-          hi1 = lo1;
+#pragma unroll
+        for (int i = 0; i < 2 * kGroups; ++i) {
+          const float u = vu[i] * unit_inverse;
+          x[i][0] *= u;
+          x[i][1] *= u;
         }
       }
-      const uint32_t b0 = movmatrix_trans(hi0), b1 = movmatrix_trans(hi1);
-      uint32_t d0 = 0, d1 = 0;
-      if constexpr (G > 4) {
-        d0 = movmatrix_trans(lo0);
-        d1 = movmatrix_trans(lo1);
-      }
-      if constexpr (F16) {
-        // a transposed 16-bit unit holds channels 2g and 2g + 1 of a token: the
-        // even ones become row g of the tile, the odd ones row g + 8
-        const int r = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-        for (int k = 0; k < kSteps; k += 2) {
-          uint32_t w[4];
-          ldmatrix_x4_trans(w, vt + r * C::kRow + C::swizzle(r, k + (lane >> 4)) * 16);
+      for (int gr = 0; gr < kGroups; ++gr) {
+        uint32_t hi0 = pack2<F16>(x[2 * gr][0], x[2 * gr][1]);
+        uint32_t hi1 = pack2<F16>(x[2 * gr + 1][0], x[2 * gr + 1][1]);
+        if constexpr (F16) {
+          const uint32_t b0 = movmatrix_trans(hi0), b1 = movmatrix_trans(hi1);
+          // a transposed 16-bit unit holds channels 2g and 2g + 1 of a token: the
+          // even ones become row g of the tile, the odd ones row g + 8
+          const int r = 16 * gr + (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = w[2 * h], y = w[2 * h + 1];
-            const uint32_t a[4] = {widen_alternate<F>(x, false), widen_alternate<F>(x, true),
-                                   widen_alternate<F>(y, false), widen_alternate<F>(y, true)};
-            mma16816<true>(o[k + h], a, b0, b1);
-            if constexpr (G > 4) mma16816<true>(o[k + h], a, d0, d1);
+          for (int k = 0; k < kSteps; k += 2) {
+            uint32_t w[4];
+            ldmatrix_x4_trans(w, vt + r * C::kRow + C::swizzle(r, k + (lane >> 4)) * 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t y = w[2 * h], z = w[2 * h + 1];
+              const uint32_t a[4] = {widen_alternate<F>(y, false), widen_alternate<F>(y, true),
+                                     widen_alternate<F>(z, false), widen_alternate<F>(z, true)};
+              mma16816<true>(o[k + h], a, b0, b1);
+            }
           }
-        }
-      } else {
-        const int r = (lane & 7) + (lane >> 4) * 8;
+        } else {
+          const float2 r0 = unpack2<false>(hi0), r1 = unpack2<false>(hi1);
+          uint32_t lo0 = pack2<false>(x[2 * gr][0] - r0.x, x[2 * gr][1] - r0.y);
+          uint32_t lo1 = pack2<false>(x[2 * gr + 1][0] - r1.x, x[2 * gr + 1][1] - r1.y);
+          if constexpr (G <= 4) {  // columns 4..7 carry the remainders
+            if (c >= 2) {
+              hi0 = lo0;
+              hi1 = lo1;
+            }
+          }
+          const uint32_t b0 = movmatrix_trans(hi0), b1 = movmatrix_trans(hi1);
+          uint32_t d0 = 0, d1 = 0;
+          if constexpr (G > 4) {
+            d0 = movmatrix_trans(lo0);
+            d1 = movmatrix_trans(lo1);
+          }
+          const int r = 16 * gr + (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t a[4];
-          ldmatrix_x4_trans(a, vt + r * C::kRow + C::swizzle(r, 2 * k + ((lane >> 3) & 1)) * 16);
-          mma16816<false>(o[k], a, b0, b1);
-          if constexpr (G > 4) mma16816<false>(o[k], a, d0, d1);
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t a[4];
+            ldmatrix_x4_trans(a, vt + r * C::kRow + C::swizzle(r, 2 * k + ((lane >> 3) & 1)) * 16);
+            mma16816<false>(o[k], a, b0, b1);
+            if constexpr (G > 4) mma16816<false>(o[k], a, d0, d1);
+          }
         }
       }
     }
     const bool closes = ch.flags & kCloses;
     if (closes && it + 1 < total) {  // the next unit's queries, while this one is added up
-      const Chunk& k = s_chunk[warp][(it + 1) % C::kStages];
-      fetch_q(k.row, k.kvh);
+      fetch_q(s_chunk[warp][(it + 1) % kInfos].row);
     }
-    __syncwarp();  // the stage may be filled again
+    __syncwarp();
+    load_values(it + C::kStages, slot);
+    slot = ask();
     if (!closes) continue;
 
     // ---- the piece is done: the warps' sums meet ----
@@ -562,7 +672,7 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
       l0 += __shfl_xor_sync(0xffffffffu, l0, d);
       l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
-    if constexpr (G <= 4) {
+    if constexpr (!F16 && G <= 4) {  // the remainders' columns
 #pragma unroll
       for (int i = 0; i < kSteps; ++i)
 #pragma unroll
@@ -587,99 +697,157 @@ __global__ void __launch_bounds__(Cfg<D, F>::kThreads, kCtasPerSm)
     }
     if (lane == 0) s_unit[warp] = unit_max;
     __syncthreads();
-    const int64_t unit = (int64_t)ch.row * hkv + ch.kvh;
+    const int64_t unit = (int64_t)ch.row * hkv + kvh;
     // the unit's steps in the order of all, [u0, u1)
-    const int in = ch.tok - warp * kChunk - (ch.first & ~(kChunk - 1));  // tokens before this step
+    const int in = ch.tok - warp * kChunk - first_visited(ch.first);  // tokens before this step
     const long long u0 = lo + it - in / kStep, u1 = u0 + ch.steps;
     const bool split = u0 < lo || u1 > hi;
-    // CTA k's part of the unit: it goes on with the unit, or starts it
-    auto part_of = [&](int k) -> float* {
-      return p.parts + (2 * (int64_t)k + (tc::range_lo(k, K, ctas) > u0 ? 0 : 1)) * kPart;
-    };
-    float* part = split ? part_of(blockIdx.x) : nullptr;
-    float whole_unit = kLeastUnit;
-    if constexpr (F == kInt8) {
+    const bool starts = u0 >= lo;
+    // the factors of the warps' sums, and each head's max and sum over them
+    if (tid < kWarps * G) {
+      const int w = tid / G, h = tid % G;
+      float mm = -INFINITY, uu = kLeastUnit, l = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) whole_unit = larger_unit(whole_unit, s_unit[w]);
+      for (int x = 0; x < kWarps; ++x) {
+        mm = fmaxf(mm, s_ml[x][h][0]);
+        if constexpr (F == kInt8) uu = larger_unit(uu, s_unit[x]);
+      }
+      const float a = weight(s_ml[w][h][0], mm);
+      s_factor[w][h] = F == kInt8 ? a * (s_unit[w] / uu) : a;
+      if (w == 0) {
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) l += weight(s_ml[x][h][0], mm) * s_ml[x][h][1];
+        s_max[h] = mm;
+        s_l[h] = l;
+        s_post[h] = F == kInt8 ? uu : post;
+      }
     }
-    for (int i = tid; i < G * D; i += kThreads) {
+    __syncthreads();
+    float* mine = p.parts + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * kPart;
+    for (int i = 2 * tid; i < G * D; i += 2 * kThreads) {
       const int h = i / D, d = i % D;
-      float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w][h][0]);
-      float acc = 0.f, l = 0.f;
+      float x = 0.f, y = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float a = weight(s_ml[w][h][0], mm);
-        const float u = F == kInt8 ? s_unit[w] / whole_unit : 1.f;
-        acc += a * u * s_o[w][h][d];
-        l += a * s_ml[w][h][1];
+        const float a = s_factor[w][h];
+        x += a * s_o[w][h][d];
+        y += a * s_o[w][h][d + 1];
       }
-      if (split) {
-        part[i] = acc;
-        if (d == 0) {
-          part[G * D + 2 * h] = mm;
-          part[G * D + 2 * h + 1] = l;
-          if (h == 0) part[G * (D + 2)] = whole_unit;
-        }
-      } else if (!(ch.flags & kNobody)) {
-        // the division first: acc is a sum over all tokens, and the factor may
-        // bring it past the largest float where the result is in range
-        p.out[unit * G * D + i] =
-            __float2bfloat16_rn(l == 0.f ? 0.f : acc / l * (F == kInt8 ? whole_unit : post));
-      }
+      if (split)
+        *reinterpret_cast<float2*>(mine + i) = make_float2(x, y);
+      else if (!(ch.flags & kNobody))
+        store(unit * G * D + i, x, y, s_l[h], s_post[h]);
     }
     if (!split) continue;
+    if (tid < G) {
+      mine[G * D + 2 * tid] = s_max[tid];
+      mine[G * D + 2 * tid + 1] = s_l[tid];
+      if (tid == 0) mine[G * (D + 2)] = s_post[0];
+    }
 
-    // ---- a split unit: the last of its CTAs to arrive adds the parts up ----
-    const int c0 = tc::cta_of(u0, K, ctas), c1 = tc::cta_of(u1 - 1, K, ctas);
     __syncthreads();  // the part is written
     if (tid == 0) {
       ptx::fence_acq_rel_gpu();
-      const int n = tc::arrive(&p.counters[unit], p.epoch);
-      s_last = n == c1 - c0 + 1;
-      if (s_last) p.counters[unit] = p.epoch << 16;  // none, for a replay of this launch
-      ptx::fence_acq_rel_gpu();
+      st_release(&p.flags[2 * blockIdx.x + (starts ? 1 : 0)], p.epoch);
     }
-    __syncthreads();
-    if (!s_last) continue;
-    for (int i = tid; i < G * D; i += kThreads) {
-      const int h = i / D;
-      float mm = -INFINITY, uu = kLeastUnit;
-      for (int k = c0; k <= c1; ++k) {
-        const float* q = part_of(k);
-        mm = fmaxf(mm, __ldcg(q + G * D + 2 * h));
-        if constexpr (F == kInt8) uu = larger_unit(uu, __ldcg(q + G * (D + 2)));
-      }
-      float acc = 0.f, l = 0.f;
-      for (int k = c0; k <= c1; ++k) {
-        const float* q = part_of(k);
-        const float a = weight(__ldcg(q + G * D + 2 * h), mm);
-        const float u = F == kInt8 ? __ldcg(q + G * (D + 2)) / uu : 1.f;
-        acc += a * u * __ldcg(q + i);
-        l += a * __ldcg(q + G * D + 2 * h + 1);
-      }
-      p.out[unit * G * D + i] =
-          __float2bfloat16_rn(l == 0.f ? 0.f : acc / l * (F == kInt8 ? uu : post));
+    if (!starts && u1 <= hi) {  // this CTA holds the unit's end (once: its first piece)
+      merge_unit = unit;
+      merge_start = u0;
     }
   }
   cp_async_wait<0>();
+  if (merge_unit < 0) return;
+
+  // ---- the CTA that holds a split unit's end adds the unit's parts up: those
+  // of CTAs before it, which have all been started, so that the wait ends ----
+  const int first = tc::cta_of(merge_start, K, ctas), count = part - first + 1;
+  // the first CTA's part starts the unit, the others' go on with it
+  auto index_of = [&](int k) { return 2 * ((first + k) * hkv + kvh) + (k == 0 ? 1 : 0); };
+  auto part_of = [&](int k) -> const float* { return p.parts + (int64_t)index_of(k) * kPart; };
+  bool all = true;
+  for (int k = tid; k < count; k += kThreads) {
+    unsigned long long* flag = &p.flags[index_of(k)];
+    const long long begun = clock64();
+    while (ld_acquire(flag) != p.epoch) {
+      if (clock64() - begun > tc::kWaitClocks) {
+        atomicExch(p.err, 41);
+        all = false;
+        break;
+      }
+    }
+    *flag = 0;  // for a replay of this launch
+  }
+  if (!__syncthreads_and(all)) return;
+  // eight parts at a time, so that a unit's usual few cost one trip to memory
+  for (int i = 4 * tid; i < G * D; i += 4 * kThreads) {
+    const int h = i / D;
+    float mm = -INFINITY, l = 0.f, uu = kLeastUnit;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < count; k0 += 8) {
+      float2 ml[8];
+      float un[8];
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        un[k] = kLeastUnit;
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + k < count) {
+          const float* q = part_of(k0 + k);
+          ml[k] = __ldcg(reinterpret_cast<const float2*>(q + G * D + 2 * h));
+          if constexpr (F == kInt8) un[k] = __ldcg(q + G * (D + 2));
+          v[k] = __ldcg(reinterpret_cast<const float4*>(q + i));
+        }
+      }
+      float most = mm, unit = uu;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        most = fmaxf(most, ml[k].x);
+        if constexpr (F == kInt8) unit = larger_unit(unit, un[k]);
+      }
+      const float inverse = F == kInt8 ? 1.f / unit : 1.f;
+      float a = weight(mm, most);
+      l *= a;
+      if constexpr (F == kInt8) a *= uu * inverse;
+      sum.x *= a, sum.y *= a, sum.z *= a, sum.w *= a;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        a = weight(ml[k].x, most);
+        l += a * ml[k].y;
+        if constexpr (F == kInt8) a *= un[k] * inverse;
+        sum.x += a * v[k].x, sum.y += a * v[k].y, sum.z += a * v[k].z, sum.w += a * v[k].w;
+      }
+      mm = most;
+      uu = unit;
+    }
+    const float factor = F == kInt8 ? uu : post;
+    store(merge_unit * G * D + i, sum.x, sum.y, l, factor);
+    store(merge_unit * G * D + i + 2, sum.z, sum.w, l, factor);
+  }
 }
 
-int64_t parts_bytes(int group, int head_dim, int num_sms) {
-  return (int64_t)kCtasPerSm * num_sms * 2 * (group * (head_dim + 2) + 1) * 4;
+// Ranges per head: such that the fewest rounds of the CTAs that run at once
+// do the most.
+int ranges_of(int64_t heads, int64_t at_once) {
+  int64_t best = 1;
+  auto rounds = [&](int64_t r) { return (r * heads + at_once - 1) / at_once; };
+  for (int64_t r = at_once / heads < 1 ? 1 : at_once / heads; r <= 16 || r * heads <= at_once; ++r)
+    if (rounds(r) * best < rounds(best) * r) best = r;
+  return (int)best;
 }
 
 template <int D, int G, KvFormat F>
 cudaError_t launch_one(const ScoredParams& p, int num_sms, cudaStream_t stream) {
-  using C = Cfg<D, F>;
+  using C = Cfg<D, G, F>;
   const int64_t units = (int64_t)p.num_rows * p.num_kv_heads;
   const int64_t at_once = (int64_t)kCtasPerSm * num_sms;
   const bool whole = units >= kWholeUnits * at_once;
   const cudaError_t e = allow_large<decode_scored_kernel<D, G, F>>();
   if (e != cudaSuccess) return e;
   return launch_dependent<decode_scored_kernel<D, G, F>>(
-      dim3((unsigned)(whole ? units : at_once)), dim3(C::kThreads), C::kRing, stream, 1, p, whole);
+      dim3((unsigned)(whole ? units
+                            : ranges_of(p.num_kv_heads, at_once) * (int64_t)p.num_kv_heads)),
+      dim3(C::kThreads), C::kRing, stream, 1, p, whole);
 }
 
 template <int D, KvFormat F>
@@ -706,22 +874,25 @@ cudaError_t launch_f(const ScoredParams& p, int group, KvFormat format, int num_
 
 }  // namespace
 
-// Parts of the CTAs that run at once, then a counter for each unit that may
-// be split.
+// Flags of two parts for each CTA, then the parts.
+static int64_t split_ctas(int64_t num_kv_heads, int num_sms) {
+  return ranges_of(num_kv_heads, (int64_t)kCtasPerSm * num_sms) * num_kv_heads;
+}
+static size_t flag_bytes(int64_t ctas) { return (size_t)(ctas * 16 + 255) / 256 * 256; }
+
 size_t scored_workspace_bytes(int64_t num_rows, int64_t num_heads, int64_t num_kv_heads,
                               int head_dim, int num_sms) {
-  const int64_t units = num_rows * num_kv_heads;
-  if (units >= (int64_t)kWholeUnits * kCtasPerSm * num_sms) return 0;
-  const int64_t parts = parts_bytes((int)(num_heads / num_kv_heads), head_dim, num_sms);
-  return (size_t)((parts + 255) / 256 * 256 + units * 8);
+  if (num_rows * num_kv_heads >= (int64_t)kWholeUnits * kCtasPerSm * num_sms) return 0;
+  const int64_t ctas = split_ctas(num_kv_heads, num_sms);
+  return flag_bytes(ctas) +
+         (size_t)ctas * 2 * part_words((int)(num_heads / num_kv_heads), head_dim) * 4;
 }
 
 cudaError_t launch_decode_scored(ScoredParams p, void* workspace, int head_dim, int group,
                                  KvFormat format, int num_sms, cudaStream_t stream) {
-  const int64_t parts = parts_bytes(group, head_dim, num_sms);
-  p.parts = static_cast<float*>(workspace);
-  p.counters = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) +
-                                                     (parts + 255) / 256 * 256);
+  p.flags = static_cast<unsigned long long*>(workspace);
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                     flag_bytes(split_ctas(p.num_kv_heads, num_sms)));
   p.epoch = tc::next_call_epoch();
   return head_dim == 128 ? launch_f<128>(p, group, format, num_sms, stream)
                          : launch_f<64>(p, group, format, num_sms, stream);

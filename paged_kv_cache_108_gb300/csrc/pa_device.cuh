@@ -24,6 +24,13 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src,
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
 }
+// The same, with zero bytes instead where src_bytes is 0.
+__device__ __forceinline__ void cp_async_4_or_zero(uint32_t dst, const void* src,
+                                                   uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src),
+               "r"(src_bytes)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;\n" ::: "memory");
 }

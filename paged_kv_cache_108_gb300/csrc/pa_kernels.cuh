@@ -216,8 +216,9 @@ struct ScoredParams {
   const int32_t* starts;        // [S + 1] first row of each sequence; null: one row each
   const float* k_scale;         // e4m3: scalars; int8: [num_slots, Hkv]
   const float* v_scale;
-  unsigned long long* counters;  // [units]: arrivals of a split unit's pieces
-  float* parts;                  // [CTAs][2][G][D + 2]: partial sums
+  unsigned long long* flags;  // [CTAs][2]: the call's tag once a part is written
+  float* parts;               // [CTAs][2]: partial sums of split units
+  int* err;                   // workspace word 0: a bounded wait that expired
   unsigned long long epoch;
   int32_t num_rows, num_seqs, num_kv_heads, num_blocks, max_blocks, log2_block_size;
   float scale_log2;  // scale * log2(e)

@@ -294,13 +294,14 @@ def weight_error(kv, d, most, cap, bias, tiles):
     three e4m3 parts (2^-12).  The cap adds 2^-20 of itself (one exponential,
     one sum, one reciprocal, each off by 2^-22 relative in a quotient of at
     most 2) and 4 u of the score; a bias three u of itself.  exp2 and its
-    argument: 2^-21.  Weights enter P V in two bf16 parts (2^-16), two f16 ones
-    (2^-21), or on the tiles in one bf16 part (2^-9) or two e4m3 parts (2^-8)."""
+    argument: 2^-21.  Weights enter P V in two bf16 parts (2^-16), one f16 part
+    over 8-bit elements (half a step: 2^-11), or on the tiles in one bf16 part
+    (2^-9) or two e4m3 parts (2^-8)."""
     e = (d + 6) * 2 ** -24 * most + 2 ** -21
     if tiles and kv == "fp8":
         e += 2 ** -12 * most + 2 ** -8
     else:
-        e += 2 ** -9 if tiles else 2 ** -16
+        e += 2 ** -9 if tiles else 2 ** -16 if kv == "bf16" else 2 ** -11
     if cap:
         e += 2 ** -20 * cap + 2 ** -22 * min(most, cap)
     return e + 3 * 2 ** -24 * bias
