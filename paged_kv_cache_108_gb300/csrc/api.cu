@@ -172,6 +172,14 @@ pa_status check_score(const pa_score_desc& s, float scale, int32_t max_blocks, i
   *mod = {};
   mod->cap_log2 = s.cap * 1.4426950408889634f;
   mod->inv_cap_log2 = s.cap > 0.f ? 2.f / s.cap : 0.f;
+  // an odd polynomial for tanh on [-1, 1], fitted to the smallest largest error
+  // (2.5e-7)
+  constexpr float kTanh[6] = {0.99999684f,  -0.33324003f, 0.13253525f,
+                              -0.050972853f, 0.016114172f, -0.0028394621f};
+  if (s.cap > 0.f) {
+    mod->inv_cap = 1.f / mod->cap_log2;
+    for (int k = 0; k < 6; ++k) mod->tanh_poly[k] = mod->cap_log2 * kTanh[k];
+  }
   mod->slopes = s.slopes;
   mod->window = s.window;
   return PA_OK;
@@ -363,9 +371,8 @@ pa_status scored_rows(const char* fn, void* out, const void* q, const void* k_ca
     a.fp8 = cache.dtype == PA_KV_FP8_E4M3;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
-    a.scored = true;
     a.mod = mod;
-    return cuda_status(pa::launch_prefill_tc(a, s), fn);
+    return cuda_status(pa::launch_prefill_scored(a, s), fn);
   }
   pa::ScoredParams p = {};
   p.out = static_cast<__nv_bfloat16*>(out);

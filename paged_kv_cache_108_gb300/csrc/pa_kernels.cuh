@@ -79,6 +79,8 @@ cudaError_t launch_decode_tc(const TcLaunch& a, cudaStream_t stream);
 struct ScoreMod {
   float cap_log2;      // > 0: s2 -> cap_log2 tanh(s2 / cap_log2)
   float inv_cap_log2;  // 2 log2(e) / cap_log2
+  float inv_cap;       // 1 / cap_log2
+  float tanh_poly[6];  // cap_log2 tanh(u) = u sum_k tanh_poly[k] u^2k, |u| <= 1
   const float* slopes;          // [H] or null
   const int32_t* prefix_lens;   // [S] or null
   int32_t window;               // > 0: keys of the last `window` positions only
@@ -104,11 +106,12 @@ struct PrefillLaunch {
   bool fp8;                // e4m3 cache: k_scale / v_scale are device scalars
   const float* k_scale;
   const float* v_scale;
-  bool scored;  // with changed scores
-  ScoreMod mod;
+  ScoreMod mod;            // changed scores
 };
 bool prefill_supported(int head_dim, int group, bool fp8, int num_seqs, int block_size);
 cudaError_t launch_prefill_tc(const PrefillLaunch& a, cudaStream_t stream);
+// The same with changed scores (prefill_scored.cu); the limits are those above.
+cudaError_t launch_prefill_scored(const PrefillLaunch& a, cudaStream_t stream);
 
 bool hp_supported(int head_dim, int group, bool fp8, int num_seqs, int num_kv_heads,
                   int block_size, int tokens_per_seq);

@@ -61,7 +61,6 @@
 
 #include <cstdint>
 
-#include "launch.cuh"
 #include "pa_device.cuh"
 #include "pa_kernels.cuh"
 #include "tc_ptx.cuh"
@@ -170,7 +169,6 @@ struct Params {
   float scale_log2;
   const float* k_scale;  // e4m3: per-tensor dequantisation scales (device scalars)
   const float* v_scale;
-  ScoreMod mod;  // changed scores (MOD kernels)
 };
 
 // One work item: request r, query tile qt (tokens qt*MQ ..), KV head g.
@@ -182,13 +180,9 @@ struct Item {
   int ntok;    // new tokens in this tile
   int kv_end;  // keys the tile's last token sees
   int nch;     // K/V chunks (0: the request's rows are zero, T > seq_len)
-  // changed scores only (0 otherwise):
-  int kv_lo;   // first key that any of the tile's tokens sees
-  int j0;      // its chunk
-  int prefix;  // tokens below this position all see the keys below it
 };
 
-template <int G, bool MOD>
+template <int G>
 __device__ __forceinline__ Item item_of(long long i, const uint16_t* tp, int R,
                                         const Params& p) {
   constexpr int MQ = 128 / G;
@@ -210,35 +204,11 @@ __device__ __forceinline__ Item item_of(long long i, const uint16_t* tp, int R,
   it.ntok = min(MQ, it.T - it.qt * MQ);
   it.kv_end = it.ctx + it.qt * MQ + it.ntok;
   const int cap = p.max_blocks << p.log2_bs;
-  it.kv_lo = it.j0 = it.prefix = 0;
-  if constexpr (MOD) {
-    const int pos = it.ctx + it.qt * MQ;  // of the tile's first token
-    if (p.mod.prefix_lens) it.prefix = min(__ldg(&p.mod.prefix_lens[lo]), sl);
-    if (pos < it.prefix) it.kv_end = max(it.kv_end, it.prefix);
-    if (p.mod.window > 0) it.kv_lo = max(0, pos - p.mod.window + 1);
-    it.j0 = it.kv_lo / CHK;
-  }
-  it.nch = (it.ctx < 0 || it.kv_end > cap) ? 0 : (it.kv_end + CHK - 1) / CHK - it.j0;
+  it.nch = (it.ctx < 0 || it.kv_end > cap) ? 0 : (it.kv_end + CHK - 1) / CHK;
   return it;
 }
 
-// The logits sv (times rs: in log2 units) as capped and biased ones in log2
-// units; the row's own position is `at` keys behind the first of them.
-__device__ __forceinline__ void change_scores(float (&sv)[2][32], float rs, const ScoreMod& mod,
-                                              float slope, int at) {
-  const bool cap = mod.cap_log2 > 0.f, bias = mod.slopes != nullptr;
-#pragma unroll
-  for (int q2 = 0; q2 < 2; ++q2)
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      float x = sv[q2][e] * rs;
-      if (cap) x = mod.cap_log2 * (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(x * mod.inv_cap_log2)));
-      if (bias) x -= slope * (float)abs(at - (q2 * 32 + e));
-      sv[q2][e] = x;
-    }
-}
-
-template <int G, bool FP8, bool MOD>
+template <int G, bool FP8>
 __global__ void __launch_bounds__(NTHREADS, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v,
@@ -363,7 +333,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         i = read_item(k, lane == 0);
       }
       if (i >= total) break;
-      const Item it = item_of<G, MOD>(i, tp, R, p);
+      const Item it = item_of<G>(i, tp, R, p);
       if (it.nch == 0) continue;
       if (isk) {
         if (qk > 0 && !wait_bar(sm, sm.bar(B_Q_EMPTY), (qk - 1) & 1, p.err, 21)) break;
@@ -381,17 +351,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int j = 0; j < it.nch; ++j, ++ck) {
         const int s = (int)(ck % nst);
         const uint32_t ph = (uint32_t)(ck / nst) & 1;
-        const int key0 = (it.j0 + j) * CHK;  // the chunk's first key
-        const int keys = min(CHK, it.kv_end - key0);
+        const int keys = min(CHK, it.kv_end - j * CHK);
         const int nbox = (keys + p.box_tok - 1) >> p.log2_box;
-        // the first box with a key that the tile sees: blocks that a window
-        // has left behind are not read
-        const int box0 = MOD ? max(0, it.kv_lo - key0) >> p.log2_box : 0;
         // the chunk's block ids, read while the stage drains
         int phys = 0;
-        if (lane >= box0 && lane < nbox)
+        if (lane < nbox)
           phys = __ldg(&p.block_tables[(int64_t)it.r * p.max_blocks +
-                                       ((key0 + lane * p.box_tok) >> p.log2_bs)]);
+                                       ((j * CHK + lane * p.box_tok) >> p.log2_bs)]);
         if (!wait_bar(sm, sm.bar(b_empty + s), ph ^ 1, p.err, 22)) {
           ok = false;
           break;
@@ -402,13 +368,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         if (lane == 0)
           ptx::mbar_arrive_expect_tx(sm.bar(b_full + s),
-                                     (uint32_t)(nbox - box0) * p.box_tok * (uint32_t)(D * C::ELT));
+                                     (uint32_t)nbox * p.box_tok * (uint32_t)(D * C::ELT));
         __syncwarp();
-        if (lane >= box0 && lane < nbox) {
+        if (lane < nbox) {
           // a row is one 128-byte box column (e4m3: all of d; bf16: two
           // 64-column halves HALF_B apart)
           const uint32_t dst = ring + s * TILE_B + (uint32_t)(lane * p.box_tok) * 128u;
-          const int off = (key0 + lane * p.box_tok) & (p.block_size - 1);
+          const int off = (j * CHK + lane * p.box_tok) & (p.block_size - 1);
           ptx::tma_load_4d(dst, tm, sm.bar(b_full + s), 0, it.g, off, phys);
           if (!FP8) ptx::tma_load_4d(dst + HALF_B, tm, sm.bar(b_full + s), 64, it.g, off, phys);
         }
@@ -442,12 +408,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // QK cursor: pulls items from the ring; the PV cursor follows through a
       // short local queue (it lags by at most the chunks in flight)
       constexpr int NQUEUE = 8;
-      int queue[NQUEUE];  // items' chunks
+      Item queue[NQUEUE];
       int kr = 0;          // ring slots read
       bool ring_done = false, have_q = false;
       Item qit{};
       int qj = 0, qk = 0;  // chunk in item, items with chunks so far
       bool q_ready = false;
+      Item pit{};
       int pj = 0, pk = 0;
       long long nq = 0, npv = 0;
       long long t_idle = clock64();
@@ -462,10 +429,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (i >= total) {
               ring_done = true;
             } else {
-              const Item it = item_of<G, MOD>(i, tp, R, p);
+              const Item it = item_of<G>(i, tp, R, p);
               if (it.nch > 0) {
                 qit = it;
-                queue[qk % NQUEUE] = it.nch;
+                queue[qk % NQUEUE] = it;
                 have_q = true;
                 qj = 0;
                 q_ready = false;
@@ -521,6 +488,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
         if (npv < nq) {
+          pit = queue[pk % NQUEUE];
           const int s = (int)(npv % NSTV);
           const int b = (int)(npv & 1);
           const uint32_t bph = (uint32_t)(npv >> 1) & 1;
@@ -559,7 +527,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             ptx::tc_commit(sm.bar(B_P_EMPTY));
             ptx::tc_commit(sm.bar(B_EMPTY_V + s));
             ++npv;
-            if (++pj == queue[pk % NQUEUE]) {
+            if (++pj == pit.nch) {
               pj = 0;
               ++pk;
             }
@@ -619,7 +587,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     for (int k = 0;; ++k) {
       const long long i = read_item(k, lane == 0);
       if (i >= total) break;
-      const Item it = item_of<G, MOD>(i, tp, R, p);
+      const Item it = item_of<G>(i, tp, R, p);
       const int rt = it.qt * MQ + tok;  // the row's token within the request
       const bool row_ok = tok < it.ntok;
       __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(p.out) +
@@ -631,14 +599,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         continue;
       }
-      int lim = row_ok ? it.ctx + rt + 1 : 0;  // keys < lim are visible to the row,
-      int low = 0;                             // from this one on
-      float slope = 0.f;
-      if constexpr (MOD) {
-        if (row_ok && it.ctx + rt < it.prefix) lim = max(lim, it.prefix);
-        if (p.mod.window > 0) low = max(0, it.ctx + rt - p.mod.window + 1);
-        if (p.mod.slopes) slope = __ldg(&p.mod.slopes[it.g * G + hd]) * 1.4426950408889634f;
-      }
+      const int lim = row_ok ? it.ctx + rt + 1 : 0;  // keys < lim are visible to the row
       float m_ref = -INFINITY, l = 0.f;
       bool good = true;
       float rs = p.scale_log2;  // logit scale of this row, log2 units
@@ -717,18 +678,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         ptx::mbar_arrive(sm.bar(B_S_EMPTY + b));
         // every row of a full tile sees every key of a chunk that ends before
         // the tile's first token: no mask (the common case on long contexts)
-        const int key0 = (it.j0 + j) * CHK;
-        bool whole = it.ntok == MQ && key0 + CHK <= it.ctx + it.qt * MQ + 1;
-        const int kl = lim - key0 - half * 64;  // visible keys among this thread's 64,
-        int kf = 0;                             // from this one on
-        if constexpr (MOD) {
-          if (p.mod.window > 0) {
-            // the tile's last token sees the fewest
-            whole = whole && key0 >= it.ctx + it.qt * MQ + MQ - p.mod.window;
-            kf = low - key0 - half * 64;
-          }
-          change_scores(sv, rs, p.mod, slope, it.ctx + rt - key0 - half * 64);
-        }
+        const bool whole = it.ntok == MQ && (j + 1) * CHK <= it.ctx + it.qt * MQ + 1;
+        const int kl = lim - j * CHK - half * 64;  // visible keys among this thread's 64
         // max of the raw logits (scale > 0), four independent chains
         float hm4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if (whole) {
@@ -741,15 +692,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int q2 = 0; q2 < 2; ++q2)
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const bool in = good && q2 * 32 + e < kl && (!MOD || q2 * 32 + e >= kf);
-              const float x = in ? sv[q2][e] : -INFINITY;
+              const float x = (good && q2 * 32 + e < kl) ? sv[q2][e] : -INFINITY;
               sv[q2][e] = x;
               hm4[e & 3] = fmaxf(hm4[e & 3], x);
             }
         }
         const float hm = fmaxf(fmaxf(hm4[0], hm4[1]), fmaxf(hm4[2], hm4[3]));
         // the row's chunk max in log2 units, the same in both threads
-        const float cm = fmaxf(hm, partner(hm)) * (MOD ? 1.f : rs);
+        const float cm = fmaxf(hm, partner(hm)) * rs;
         if constexpr (FP8) {
           // O^T: row r of O is column r of the tensor-memory tile, spread over
           // all 128 lanes (d).  Each row publishes its factor (1 when it keeps
@@ -815,12 +765,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const float msafe = m_ref == -INFINITY ? 0.f : m_ref;
         // ---- P (and the V rows past the item's last key) ----
         wait_bar(sm, sm.bar(B_P_EMPTY), (uint32_t)(ck & 1) ^ 1, p.err, 25);
-        if (j == it.nch - 1 || (MOD && j == 0)) {
-          const int kc = it.kv_end - key0;
-          const int k0 = it.kv_lo - key0;  // rows before it: unseen, some of them not loaded
-          if (kc < CHK || (MOD && k0 > 0)) {
+        if (j == it.nch - 1) {
+          const int kc = it.kv_end - j * CHK;
+          if (kc < CHK) {
             wait_bar(sm, sm.bar(B_FULL_V + s), ph, p.err, 26);
-            if (row >= kc || (MOD && row < k0)) {
+            if (row >= kc) {
               // this thread's 64 columns of V row `row` (e4m3: bytes half * 64
               // .. of the 128-byte row; bf16: the row's 64-column half)
               if constexpr (FP8) {
@@ -848,7 +797,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           unsigned char* prow = sm.base + OFF_P + row * 128;
           // 2^(8 - R) p = 2^(s * scale - m + 8 - R): the factor folds into the
           // FMA's bias; logits and sums go two to an instruction
-          const float2 rs2 = MOD ? make_float2(1.f, 1.f) : make_float2(rs, rs);
+          const float2 rs2 = make_float2(rs, rs);
           const float bias = C::kPScaleLog2 - msafe;
           const float2 nb2 = make_float2(bias, bias);
           float2 l2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
@@ -885,8 +834,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           unsigned char* prow = sm.base + OFF_P + half * HALF_B + row * 128;
           float2 l2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                           make_float2(0.f, 0.f)};
-          const float2 rs2 = MOD ? make_float2(1.f, 1.f) : make_float2(rs, rs);
-          const float2 nm2 = make_float2(-msafe, -msafe);
+          const float2 rs2 = make_float2(rs, rs), nm2 = make_float2(-msafe, -msafe);
 #pragma unroll
           for (int c8 = 0; c8 < 8; ++c8) {
             uint32_t w[4];
@@ -984,11 +932,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
 // ---------------- host side ----------------
 
-template <int G, bool FP8, bool MOD>
+template <int G, bool FP8>
 cudaError_t launch_g(const Params& prm, const CUtensorMap& mk, const CUtensorMap& mv,
                      const CUtensorMap& mq, int num_ctas, cudaStream_t stream) {
-  const cudaError_t large = allow_large<prefill_tc_kernel<G, FP8, MOD>>();
-  if (large != cudaSuccess) return large;
+  static bool configured = false;
+  if (!configured) {
+    cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<G, FP8>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         PCfg<FP8>::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    configured = true;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_ctas);
   cfg.blockDim = dim3(NTHREADS);
@@ -999,21 +953,9 @@ cudaError_t launch_g(const Params& prm, const CUtensorMap& mk, const CUtensorMap
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_tc_kernel<G, FP8, MOD>, mk, mv, mq, prm);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_tc_kernel<G, FP8>, mk, mv, mq, prm);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
-}
-
-template <bool FP8, bool MOD>
-cudaError_t launch_mod(const Params& prm, const CUtensorMap& mk, const CUtensorMap& mv,
-                       const CUtensorMap& mq, int group, int num_ctas, cudaStream_t stream) {
-  switch (group) {
-    case 1: return launch_g<1, FP8, MOD>(prm, mk, mv, mq, num_ctas, stream);
-    case 2: return launch_g<2, FP8, MOD>(prm, mk, mv, mq, num_ctas, stream);
-    case 4: return launch_g<4, FP8, MOD>(prm, mk, mv, mq, num_ctas, stream);
-    case 8: return launch_g<8, FP8, MOD>(prm, mk, mv, mq, num_ctas, stream);
-    default: return cudaErrorInvalidValue;
-  }
 }
 
 }  // namespace pf
@@ -1098,12 +1040,22 @@ cudaError_t launch_prefill_tc(const PrefillLaunch& a, cudaStream_t stream) {
   prm.scale_log2 = a.scale * 1.4426950408889634f;
   prm.k_scale = a.k_scale;
   prm.v_scale = a.v_scale;
-  prm.mod = a.mod;
-  if (a.fp8)
-    return a.scored ? launch_mod<true, true>(prm, mk, mv, mq, group, a.num_ctas, stream)
-                    : launch_mod<true, false>(prm, mk, mv, mq, group, a.num_ctas, stream);
-  return a.scored ? launch_mod<false, true>(prm, mk, mv, mq, group, a.num_ctas, stream)
-                  : launch_mod<false, false>(prm, mk, mv, mq, group, a.num_ctas, stream);
+  if (a.fp8) {
+    switch (group) {
+      case 1: return launch_g<1, true>(prm, mk, mv, mq, a.num_ctas, stream);
+      case 2: return launch_g<2, true>(prm, mk, mv, mq, a.num_ctas, stream);
+      case 4: return launch_g<4, true>(prm, mk, mv, mq, a.num_ctas, stream);
+      case 8: return launch_g<8, true>(prm, mk, mv, mq, a.num_ctas, stream);
+      default: return cudaErrorInvalidValue;
+    }
+  }
+  switch (group) {
+    case 1: return launch_g<1, false>(prm, mk, mv, mq, a.num_ctas, stream);
+    case 2: return launch_g<2, false>(prm, mk, mv, mq, a.num_ctas, stream);
+    case 4: return launch_g<4, false>(prm, mk, mv, mq, a.num_ctas, stream);
+    case 8: return launch_g<8, false>(prm, mk, mv, mq, a.num_ctas, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace pa
