@@ -173,12 +173,11 @@ pa_status check_score(const pa_score_desc& s, float scale, int32_t max_blocks, i
   mod->cap_log2 = s.cap * 1.4426950408889634f;
   mod->inv_cap_log2 = s.cap > 0.f ? 2.f / s.cap : 0.f;
   // an odd polynomial for tanh on [-1, 1], fitted to the smallest largest error
-  // (2.5e-7)
-  constexpr float kTanh[6] = {0.99999684f,  -0.33324003f, 0.13253525f,
-                              -0.050972853f, 0.016114172f, -0.0028394621f};
+  // (2.8e-6)
+  constexpr float kTanh[5] = {0.99996847f, -0.33265823f, 0.12922066f, -0.04329985f, 0.0083658816f};
   if (s.cap > 0.f) {
     mod->inv_cap = 1.f / mod->cap_log2;
-    for (int k = 0; k < 6; ++k) mod->tanh_poly[k] = mod->cap_log2 * kTanh[k];
+    for (int k = 0; k < 5; ++k) mod->tanh_poly[k] = mod->cap_log2 * kTanh[k];
   }
   mod->slopes = s.slopes;
   mod->window = s.window;
@@ -340,16 +339,21 @@ pa_status scored_rows(const char* fn, void* out, const void* q, const void* k_ca
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(block_tables, 4) || !aligned(lens, 4) || !aligned(workspace, 256))
     return fail(PA_ERR_INVALID, "misaligned pointer");
-  const size_t need =
-      pa_scored_workspace_size(num_rows, num_heads, cache.num_kv_heads, cache.head_dim);
-  if (workspace_bytes < need)
-    return fail(PA_ERR_INVALID, ("workspace of " + std::to_string(need) + " bytes needed").c_str());
   const int group = num_heads / cache.num_kv_heads;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (starts && cache.dtype != PA_KV_INT8 && num_rows > kRowsPerRequest * (int64_t)num_seqs &&
+  const bool tiles =
+      starts && cache.dtype != PA_KV_INT8 && num_rows > kRowsPerRequest * (int64_t)num_seqs &&
       num_rows <= 65535 &&
       pa::prefill_supported(cache.head_dim, group, cache.dtype == PA_KV_FP8_E4M3, num_seqs,
-                            cache.block_size)) {
+                            cache.block_size);
+  const size_t need =
+      kScoredHead +
+      (tiles ? pa::prefill_scored_workspace_bytes(cache.num_kv_heads, num_sms())
+             : pa::scored_workspace_bytes(num_rows, num_heads, cache.num_kv_heads, cache.head_dim,
+                                          num_sms()));
+  if (workspace_bytes < need)
+    return fail(PA_ERR_INVALID, ("workspace of " + std::to_string(need) + " bytes needed").c_str());
+  if (tiles) {
     pa::PrefillLaunch a{};
     a.out = out;
     a.q = q;
@@ -1241,8 +1245,13 @@ size_t pa_scored_workspace_size(int32_t num_rows, int32_t num_heads, int32_t num
   if (num_rows < 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads ||
       head_dim <= 0)
     return 0;
-  return kScoredHead +
-         pa::scored_workspace_bytes(num_rows, num_heads, num_kv_heads, head_dim, num_sms());
+  const size_t rows =
+      pa::scored_workspace_bytes(num_rows, num_heads, num_kv_heads, head_dim, num_sms());
+  // (tiles: more than kRowsPerRequest tokens of a request)
+  const size_t tiles = head_dim == 128 && num_rows > kRowsPerRequest
+                           ? pa::prefill_scored_workspace_bytes(num_kv_heads, num_sms())
+                           : 0;
+  return kScoredHead + (rows > tiles ? rows : tiles);
 }
 
 pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const void* v_cache,

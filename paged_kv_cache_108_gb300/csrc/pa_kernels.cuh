@@ -80,7 +80,7 @@ struct ScoreMod {
   float cap_log2;      // > 0: s2 -> cap_log2 tanh(s2 / cap_log2)
   float inv_cap_log2;  // 2 log2(e) / cap_log2
   float inv_cap;       // 1 / cap_log2
-  float tanh_poly[6];  // cap_log2 tanh(u) = u sum_k tanh_poly[k] u^2k, |u| <= 1
+  float tanh_poly[5];  // cap_log2 tanh(u) = u sum_k tanh_poly[k] u^2k, |u| <= 1
   const float* slopes;          // [H] or null
   const int32_t* prefix_lens;   // [S] or null
   int32_t window;               // > 0: keys of the last `window` positions only
@@ -111,6 +111,8 @@ struct PrefillLaunch {
 bool prefill_supported(int head_dim, int group, bool fp8, int num_seqs, int block_size);
 cudaError_t launch_prefill_tc(const PrefillLaunch& a, cudaStream_t stream);
 // The same with changed scores (prefill_scored.cu); the limits are those above.
+// Its workspace: the error word's 256 bytes, then so many.
+size_t prefill_scored_workspace_bytes(int num_kv_heads, int num_sms);
 cudaError_t launch_prefill_scored(const PrefillLaunch& a, cudaStream_t stream);
 
 bool hp_supported(int head_dim, int group, bool fp8, int num_seqs, int num_kv_heads,

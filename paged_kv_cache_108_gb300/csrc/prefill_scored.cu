@@ -12,20 +12,23 @@
 //
 // A work item is a pair of neighbouring query tiles of one request and KV head:
 // 2 x 128 rows, row = token * G + query head in the group.  Both tiles use
-// each K and V chunk of 128 keys while it is in shared memory, and alternate
-// on the tensor cores: while one tile's softmax runs, the other's products do.
-//   S_t = Q_t K^T   M = 128 rows, N = 128 keys, K = 128, into tensor memory
-//   P_t             one thread a row: 128 logits from tensor memory, changed,
-//                   masked, exponentiated; 16-bit weights written back over S_t
-//   O_t += P_t V    A = P_t from tensor memory, B = the V chunk, MN-major
-// Tensor memory is full: S_0, S_1 (P over them), O_0, O_1 of 128 columns.
+// each K and V chunk of 128 keys while it is in shared memory.  A chunk's keys
+// are taken in two halves, each with logits of its own in tensor memory, so
+// that a tile's softmax of one half runs while the products of the other do:
+//   S_th = Q_t K_h^T   M = 128 rows, N = 64 keys, K = 128, into tensor memory
+//   P_th               one thread a row: 64 logits from tensor memory, changed,
+//                      masked, exponentiated; 16-bit weights back over S_th
+//   O_t += P_th V_h    A = P_th from tensor memory, B = V's rows, MN-major
+// Tensor memory is full: S_00 S_01 S_10 S_11 of 64 columns (P over them), O_0
+// and O_1 of 128.  (With whole chunks in one buffer a tile's softmax waited
+// 1600 of its 5200 clocks a chunk for the products.)
 // O is rescaled only when a row's running max grows by more than 2^8; all lanes
 // of the row's warp take part (by 1), as tensor memory accesses are a warp's.
 //
-// The cap.  tanh(u) for |u| <= 1 is an odd polynomial of degree 11 (fitted to
-// the smallest largest error over [0, 1]: 2.5e-7), which runs on the FMA pipe
-// two logits an instruction; a chunk with a larger |u| in one of the warp's
-// rows takes 1 - 2 / (1 + e^2u), one exponential and one reciprocal.
+// The cap.  tanh(u) for |u| <= 1 is an odd polynomial of degree 9 (fitted to
+// the smallest largest error over [0, 1]: 2.8e-6, which a cap of 50 makes 1.4e-4
+// of a weight, a fourteenth of its 16-bit rounding), six FMAs a logit; a half chunk with a larger |u| in one of the
+// warp's rows takes 1 - 2 / (1 + e^2u), one exponential and one reciprocal.
 //
 // An e4m3 cache: two warps widen each chunk to f16 (exact) in shared memory;
 // q, scaled by a power of two a row that puts its largest |q| in [1, 2), is
@@ -38,9 +41,17 @@
 //
 // Roles (384 threads): warps 0-3 and 4-7 softmax and epilogue of tile 0 and 1;
 // warp 8 loads (q, K, V) and hands out items; warp 9 issues the MMAs; warps
-// 10-11 widen or zero.  Items come from a counter in the workspace (word 1,
-// zeroed by the host before the launch), each request's longest first.  Every
-// mbarrier wait is bounded: error word 0, the CTA gives up.
+// 10-11 widen or zero.  Every wait is bounded: error word 0, the CTA gives up.
+//
+// Work split: the chunks of all items of a head in a row, K in all, are cut
+// into equal ranges, each taken by H_kv neighbouring CTAs, one a head (ragged
+// chunks of 168 items on 152 SMs, an item a CTA: 134 us, half the SMs idle in
+// the second round).  An item's chunks are visited from its last keys to its
+// first: a bias by distance has its largest weights there, and the running max
+// hardly grows.  A CTA's range splits at most two items: their sums go to the
+// workspace in fp32, and the CTA that holds an item's end (its first keys) adds
+// them up once its own range is done and the others' flags, tagged with the
+// call, are up; those are CTAs before it, which have all been started.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -60,7 +71,6 @@ namespace ps {
 
 using tc::Smem;
 using tc::drain_bar;
-using tc::wait_bar;
 
 constexpr int D = 128, CHK = 128;       // keys per chunk
 constexpr int kMaxReqs = 256;
@@ -70,9 +80,16 @@ constexpr int RAW_B = CHK * D;          // a K or V chunk in e4m3
 constexpr int NTHREADS = 384;
 constexpr int PROD_WARP = 8, MMA_WARP = 9, FIX_WARP = 10;
 constexpr int NITEM = 4;                // items published ahead
+constexpr int kItemCost = 1;            // of an item, in chunks
+constexpr int kMinUnits = 2;            // units of a CTA at least, where there are few
 constexpr int NFIX = 4;                 // zeroed V chunks ahead of their MMA, at most
-constexpr int S_COL = 0, O_COL = 256;   // tile t: + 128 t
+constexpr int S_COL = 0, O_COL = 256;   // tile t: + 128 t; logits of the h-th half: + 64 h
 constexpr float kRescaleLog2 = 8.f;
+
+constexpr int kItemBytes = 80;
+// Sums of an item's 2 x 128 rows: [tile][column / 4][row] float4, then
+// [tile][row] (max, sum)
+constexpr int kPartWords = 2 * 128 * (D + 2);
 
 template <bool FP8>
 struct Cfg {
@@ -86,14 +103,15 @@ struct Cfg {
   static constexpr int B_Q_FULL = 0, B_Q_EMPTY = 1, B_Q_READY = 2 /* [2] */, B_FULL = 4,
                        B_EMPTY = B_FULL + NLOAD, B_WIDE = B_EMPTY + NLOAD,
                        B_WIDE_EMPTY = B_WIDE + NST, B_FIX = B_WIDE_EMPTY + NST,
-                       B_S_FULL = B_FIX + NFIX, B_P_FULL = B_S_FULL + 2, B_O_FULL = B_P_FULL + 2,
-                       B_O_EMPTY = B_O_FULL + 2, B_ITEM_FULL = B_O_EMPTY + 2,
-                       B_ITEM_EMPTY = B_ITEM_FULL + NITEM, NBARS = B_ITEM_EMPTY + NITEM;
+                       B_S_FULL = B_FIX + NFIX /* [tile][half] */, B_P_FULL = B_S_FULL + 4,
+                       B_O_FULL = B_P_FULL + 4, B_O_EMPTY = B_O_FULL + 4, B_ITEM_FULL = B_O_EMPTY + 2,
+                       B_ITEM_EMPTY = B_ITEM_FULL + NITEM, B_PART = B_ITEM_EMPTY + NITEM,
+                       B_MERGE = B_PART + 1, NBARS = B_MERGE + 1;
   static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
-  static constexpr int OFF_RING = OFF_ABORT + 4;
+  static constexpr int OFF_RING = (OFF_ABORT + 4 + 15) / 16 * 16;
   // pairs of tiles before each request, [R + 1]; at most 65535 new tokens
-  static constexpr int OFF_TP = OFF_RING + NITEM * 4;
+  static constexpr int OFF_TP = OFF_RING + NITEM * kItemBytes;
   static constexpr int SMEM_BYTES = OFF_TP + (kMaxReqs + 1) * 2 + 1024;  // + alignment slack
   static constexpr float kRaise = FP8 ? 7.f : 0.f;  // log2 of the factor of P and its sum
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
@@ -106,13 +124,43 @@ struct Params {
   const int32_t* seq_lens;      // [R]
   const int32_t* qsl;           // [R + 1]
   int* err;                     // workspace word 0
-  unsigned* next_item;          // workspace word 1
+  unsigned long long* flags;    // [CTAs][2]: the call's tag once a part is written
+  float* parts;                 // [CTAs][2][kPartWords]
+  unsigned long long epoch;
+  int ranges;                   // CTAs of a head
   int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks, block_size, log2_bs;
   int box_tok, log2_box;
   float scale_log2;
   const float* k_scale;  // e4m3: device scalars
   const float* v_scale;
   ScoreMod mod;
+};
+
+__device__ __forceinline__ void st_release(unsigned long long* p, unsigned long long v) {
+  asm volatile("st.release.gpu.u64 [%0], %1;\n" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ unsigned long long ld_acquire(const unsigned long long* p) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.u64 %0, [%1];\n" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// A wait that the other side usually has ended: the test comes first.
+__device__ __forceinline__ bool wait_at(const Smem& sm, uint32_t bar, uint32_t parity, int* err,
+                                        int code) {
+  return ptx::mbar_try_wait(bar, parity) || tc::wait_bar(sm, bar, parity, err, code);
+}
+// A stage of a ring and the parity of its use.
+template <int N>
+struct Stage {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
 };
 
 // Two lanes of fp32 arithmetic an instruction.
@@ -158,24 +206,37 @@ __device__ __forceinline__ void mma_from_tmem(uint32_t d_tmem, uint32_t a_tmem, 
       : "memory");
 }
 
-// One work item.
-struct Item {
-  int r, g;
+__device__ __forceinline__ void store_32(void* to, const uint32_t (&w)[8], bool aligned) {
+  if (!aligned) {
+    static_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(to), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// An item, or the part of its chunks that falls to a CTA.
+struct __align__(16) Item {
+  int r, g;      // request (-1: there are no more items), KV head
   int q0;        // first q row of the pair
   int pos;       // position of its first token
   int ntok[2];   // new tokens of each tile
   int kv_lo, kv_end;  // keys that the pair's tokens see lie in [kv_lo, kv_end)
   int prefix;
-  int j0, n;     // chunks of the pair: first, count (0: zero rows)
-  int a[2], b[2];  // those of each tile, relative to j0: [a, b)
+  int jl, n;     // the last chunk's keys, count (0: zero rows); chunk c has keys jl - c
+  int a[2], b[2];  // chunks of each tile: [a, b)
+  int part;      // slot of its sums, -1: the item is whole
+  int merge;     // the first of the CTAs that share the item, where this one adds up; or -1
 };
+static_assert(sizeof(Item) == kItemBytes, "");
 
 template <int G>
-__device__ __forceinline__ Item item_of(int i, const uint16_t* tp, const Params& p) {
+__device__ __forceinline__ Item item_of(int pair, int g, const uint16_t* tp, const Params& p) {
   constexpr int MQ = 128 / G;
   Item it;
-  const int pair = i / p.num_kv_heads;
-  it.g = i - pair * p.num_kv_heads;
+  it.g = g;
   int lo = 0, hi = p.num_seqs;  // the request of this pair: tp[r] <= pair < tp[r + 1]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -185,7 +246,7 @@ __device__ __forceinline__ Item item_of(int i, const uint16_t* tp, const Params&
   it.r = lo;
   const int first = __ldg(&p.qsl[lo]), T = __ldg(&p.qsl[lo + 1]) - first;
   const int sl = __ldg(&p.seq_lens[lo]), ctx = sl - T;
-  const int tok = (tp[lo + 1] - 1 - pair) * 2 * MQ;  // the last tokens, which see most, first
+  const int tok = (pair - tp[lo]) * 2 * MQ;
   it.q0 = first + tok;
   it.pos = ctx + tok;
   it.prefix = p.mod.prefix_lens ? min(__ldg(&p.mod.prefix_lens[lo]), sl) : 0;
@@ -200,67 +261,43 @@ __device__ __forceinline__ Item item_of(int i, const uint16_t* tp, const Params&
   }
   it.kv_lo = low[0];
   it.kv_end = it.ntok[1] ? max(end[0], end[1]) : end[0];
-  it.j0 = it.kv_lo / CHK;
   const bool none = ctx < 0 || it.kv_end > (p.max_blocks << p.log2_bs);
-  it.n = none ? 0 : (it.kv_end + CHK - 1) / CHK - it.j0;
+  it.jl = (it.kv_end + CHK - 1) / CHK - 1;
+  it.n = none ? 0 : it.jl + 1 - it.kv_lo / CHK;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const bool some = it.ntok[t] > 0 && !none;
-    it.a[t] = some ? low[t] / CHK - it.j0 : 0;
-    it.b[t] = some ? (end[t] + CHK - 1) / CHK - it.j0 : 0;
+    it.a[t] = some ? it.jl - (end[t] - 1) / CHK : 0;
+    it.b[t] = some ? it.jl + 1 - low[t] / CHK : 0;
   }
+  it.part = it.merge = -1;
   return it;
+}
+// Its chunks [from, to) alone.
+__device__ __forceinline__ void restrict_to(Item& it, int from, int to) {
+  it.jl -= from;
+  it.n = to - from;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    it.a[t] = min(max(it.a[t] - from, 0), it.n);
+    it.b[t] = min(max(it.b[t] - from, 0), it.n);
+  }
 }
 // Whether a chunk holds keys that no token of the item sees.
 __device__ __forceinline__ bool ragged(const Item& it, int c) {
-  const int key0 = (it.j0 + c) * CHK;
+  const int key0 = (it.jl - c) * CHK;
   return key0 < it.kv_lo || key0 + CHK > it.kv_end;
 }
 
-// The logits s (times rs: in log2 units) as changed ones in log2 units; the
-// row's own position is `at` keys behind the first of them.
-__device__ __forceinline__ void change_scores(float2 (&s)[64], float rs, const ScoreMod& mod,
-                                              float slope, float at) {
-  if (mod.cap_log2 > 0.f) {
-    const float ru = rs * mod.inv_cap;  // to u = score / cap
-    float most = 0.f;
-#pragma unroll
-    for (int e = 0; e < 64; ++e) most = fmaxf(most, fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
-    const float2 ru2 = both(ru);
-    if (__all_sync(0xffffffffu, most * fabsf(ru) <= 1.f)) {
-      float2 c[6];
-#pragma unroll
-      for (int k = 0; k < 6; ++k) c[k] = both(mod.tanh_poly[k]);
-#pragma unroll
-      for (int e = 0; e < 64; ++e) {
-        const float2 u = mul2(s[e], ru2), z = mul2(u, u);
-        float2 h = fma2(c[5], z, c[4]);
-        h = fma2(h, z, c[3]);
-        h = fma2(h, z, c[2]);
-        h = fma2(h, z, c[1]);
-        h = fma2(h, z, c[0]);
-        s[e] = mul2(h, u);
-      }
-    } else {
-      const float re = ru * 2.f * 1.4426950408889634f, cap = mod.cap_log2;
-#pragma unroll
-      for (int e = 0; e < 64; ++e) {
-        s[e].x = cap - 2.f * cap * fast_reciprocal(1.f + fast_exp2(s[e].x * re));
-        s[e].y = cap - 2.f * cap * fast_reciprocal(1.f + fast_exp2(s[e].y * re));
-      }
-    }
-  } else {
-    const float2 rs2 = both(rs);
-#pragma unroll
-    for (int e = 0; e < 64; ++e) s[e] = mul2(s[e], rs2);
-  }
-  if (mod.slopes) {
-#pragma unroll
-    for (int e = 0; e < 64; ++e) {
-      s[e].x -= slope * fabsf(at - (float)(2 * e));
-      s[e].y -= slope * fabsf(at - (float)(2 * e + 1));
-    }
-  }
+// cap tanh(s rs / cap) + bias in log2 units for |s rs| <= cap, the cap's and
+// the scale's factors being in the coefficients: one square, five products.
+__device__ __forceinline__ float2 capped_poly(float2 s, const float2 (&k)[5], float2 bias) {
+  const float2 z = mul2(s, s);
+  float2 f = fma2(k[4], z, k[3]);
+  f = fma2(f, z, k[2]);
+  f = fma2(f, z, k[1]);
+  f = fma2(f, z, k[0]);
+  return fma2(f, s, bias);
 }
 
 template <int G, bool FP8>
@@ -293,7 +330,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < C::NBARS; ++i) {
       uint32_t cnt = 1;
-      if ((i >= C::B_Q_READY && i < C::B_Q_READY + 2) || (i >= C::B_P_FULL && i < C::B_P_FULL + 2) ||
+      if ((i >= C::B_Q_READY && i < C::B_Q_READY + 2) || (i >= C::B_P_FULL && i < C::B_P_FULL + 4) ||
           (i >= C::B_O_EMPTY && i < C::B_O_EMPTY + 2))
         cnt = 128;
       // the MMAs, and the two zeroing warps
@@ -302,6 +339,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if ((FP8 && i >= C::B_EMPTY && i < C::B_EMPTY + NLOAD) ||
           (i >= C::B_WIDE && i < C::B_WIDE + NST) || (i >= C::B_FIX && i < C::B_FIX + NFIX))
         cnt = 64;
+      // the softmax warps
+      if (i == C::B_PART || i == C::B_MERGE) cnt = 8;
       // an item is read by the MMA thread, 8 softmax warps and those two
       if (i >= C::B_ITEM_EMPTY && i < C::B_ITEM_EMPTY + NITEM) cnt = 11;
       ptx::mbar_init(sm.bar(i), cnt);
@@ -338,45 +377,116 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm.base + C::OFF_TMEM);
-  const int total = (int)min((long long)tp[R] * p.num_kv_heads, (long long)0x7fffffff);
-  volatile int* ring_s = reinterpret_cast<volatile int*>(sm.base + C::OFF_RING);
-  // the k-th item of this CTA (total: no more); by a whole warp
-  auto read_item = [&](int k) -> int {
+  // This CTA's head and range of chunks: [lo, hi) of K, from chunk off0 of a pair.
+  __shared__ long long s_sum[NTHREADS / 32], s_others[NTHREADS / 32], s_before;
+  __shared__ int s_pair;
+  const int j = blockIdx.x / p.num_kv_heads, g = blockIdx.x - j * p.num_kv_heads;
+  const int pairs = tp[R];
+  // A pair's chunks, and kItemCost more for what an item takes besides (the
+  // first units of a pair; one without keys has its zeros written).
+  auto units_of = [&](int pair) -> int { return item_of<G>(pair, g, tp, p).n + kItemCost; };
+  long long K = 0, lo = 0, hi = 0;
+  int ranges = 1;
+  {
+    long long others = 0, before = 0;
+    for (int x = tid + NTHREADS; x < pairs; x += NTHREADS) others += units_of(x);
+    for (int base = 0; base < pairs; base += NTHREADS) {
+      const int n = base + tid < pairs ? units_of(base + tid) : 0;
+      long long incl = n;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += up;
+      }
+      if (base == 0) {
+#pragma unroll
+        for (int d = 16; d; d /= 2) others += __shfl_xor_sync(0xffffffffu, others, d);
+      } else {
+        __syncthreads();  // s_sum is free
+      }
+      if (lane == 31) s_sum[warp] = incl;
+      if (base == 0 && lane == 0) s_others[warp] = others;
+      if (tid == 0) s_pair = -1;
+      __syncthreads();
+      long long start = before + incl - n, end = before;
+      for (int w = 0; w < NTHREADS / 32; ++w) {
+        if (w < warp) start += s_sum[w];
+        end += s_sum[w];
+      }
+      if (base == 0) {
+        K = end;
+        for (int w = 0; w < NTHREADS / 32; ++w) K += s_others[w];
+        ranges = (int)min((long long)p.ranges, max(1ll, K / kMinUnits));
+        if (j < ranges) {
+          lo = tc::range_lo(j, K, ranges);
+          hi = tc::range_lo(j + 1, K, ranges);
+        }
+      }
+      if (j < ranges && start <= lo && lo < start + n) {
+        s_pair = base + tid;
+        s_before = start;
+      }
+      __syncthreads();
+      if (j >= ranges || s_pair >= 0) break;
+      before = end;
+    }
+  }
+  Item* items = reinterpret_cast<Item*>(sm.base + C::OFF_RING);
+  // the k-th item of this CTA; by a whole warp
+  auto read_item = [&](int k) -> Item {
     const int slot = k % NITEM;
-    if (!wait_bar(sm, sm.bar(C::B_ITEM_FULL + slot), (uint32_t)(k / NITEM) & 1, p.err, 60))
-      return total;
-    const int i = ring_s[slot];
+    Item it;
+    it.r = -1;
+    if (wait_at(sm, sm.bar(C::B_ITEM_FULL + slot), (uint32_t)(k / NITEM) & 1, p.err, 60))
+      it = items[slot];
     __syncwarp();
     if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_ITEM_EMPTY + slot));
-    return i;
+    return it;
   };
 
-  // Registers: 384 threads were launched with 168, 64512 in all; 256 go on with
-  // 208 and 128 with 88, which is as many.
   if (warp >= PROD_WARP) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
     if (warp == PROD_WARP) {
       // ================= loads =================
-      long long ns = 0;  // stages filled: K and V chunks in turn
+      Stage<NLOAD> st;  // K and V chunks in turn
+      long long ns = 0;  // those filled
       int nq = 0;        // q pairs
+      int pair = hi > lo ? s_pair : 0, off = hi > lo ? (int)(lo - s_before) : 0;
+      long long left = hi - lo;
       for (int k = 0;; ++k) {
         const int slot = k % NITEM;
-        if (!wait_bar(sm, sm.bar(C::B_ITEM_EMPTY + slot), ((uint32_t)(k / NITEM) & 1) ^ 1, p.err, 61))
+        if (!wait_at(sm, sm.bar(C::B_ITEM_EMPTY + slot), ((uint32_t)(k / NITEM) & 1) ^ 1, p.err, 61))
           break;
-        int i = 0;
+        Item it;
+        it.r = -1;
+        while (left > 0) {
+          it = item_of<G>(pair, g, tp, p);
+          const int all = it.n + kItemCost, upto = (int)min((long long)all, off + left);
+          const long long u0 = hi - left - off;  // the pair's first unit
+          const int from = max(off - kItemCost, 0), to = upto - kItemCost;
+          left -= upto - off;
+          off = 0;
+          ++pair;
+          if (it.n == 0 && upto == all) break;  // zeros
+          if (to > from) {
+            if (from > 0 || to < it.n) {
+              it.part = from > 0 ? 0 : 1;
+              if (to == it.n) it.merge = tc::cta_of(u0 + kItemCost, K, ranges);
+              restrict_to(it, from, to);
+            }
+            break;
+          }
+          it.r = -1;  // (none of the pair's chunks)
+        }
         if (lane == 0) {
-          const unsigned got = atomicAdd(p.next_item, 1u);
-          i = got < (unsigned)total ? (int)got : total;
-          ring_s[slot] = i;
+          items[slot] = it;
           ptx::mbar_arrive(sm.bar(C::B_ITEM_FULL + slot));
         }
-        i = __shfl_sync(0xffffffffu, i, 0);
-        if (i >= total) break;
-        const Item it = item_of<G>(i, tp, p);
+        if (it.r < 0) break;
         bool ok = true;
+        const int q_at = nq > 0 ? 1 : 0;
         for (int x = 0; x < 2 * it.n; ++x) {
-          if (x == 1) {  // the q tiles, behind the first keys
-            if (nq > 0 && !wait_bar(sm, sm.bar(C::B_Q_EMPTY), (nq - 1) & 1, p.err, 62)) {
+          if (x == q_at) {  // the q tiles: behind the first keys, once the last ones are free
+            if (nq > 0 && !wait_at(sm, sm.bar(C::B_Q_EMPTY), (nq - 1) & 1, p.err, 62)) {
               ok = false;
               break;
             }
@@ -391,9 +501,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             ++nq;
           }
-          const int s = (int)(ns % NLOAD);
-          const uint32_t ph = (uint32_t)(ns / NLOAD) & 1;
-          const int key0 = (it.j0 + x / 2) * CHK;
+          const int s = st.s;
+          const int key0 = (it.jl - x / 2) * CHK;
           const int keys = min(CHK, it.kv_end - key0);
           const int nbox = (keys + p.box_tok - 1) >> p.log2_box;
           // blocks that lie before every window are not read
@@ -403,7 +512,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (mine)
             phys = __ldg(&p.block_tables[(int64_t)it.r * p.max_blocks +
                                          ((key0 + lane * p.box_tok) >> p.log2_bs)]);
-          if (!wait_bar(sm, sm.bar(C::B_EMPTY + s), ph ^ 1, p.err, 63)) {
+          if (!wait_at(sm, sm.bar(C::B_EMPTY + s), st.ph ^ 1, p.err, 63)) {
             ok = false;
             break;
           }
@@ -423,6 +532,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             ptx::tma_load_4d(dst, tm, sm.bar(C::B_FULL + s), 0, it.g, off, phys);
             if (!FP8) ptx::tma_load_4d(dst + HALF_B, tm, sm.bar(C::B_FULL + s), 64, it.g, off, phys);
           }
+          st.next();
           ++ns;
         }
         if (!ok) break;
@@ -437,92 +547,100 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     } else if (warp == MMA_WARP) {
       // ================= MMAs =================
       if (lane == 0) {
-        constexpr uint32_t kIdescBf16 = ptx::idesc_bf16_f32_ab(128, 128, false, false);
+        constexpr uint32_t kIdescBf16 = ptx::idesc_bf16_f32_ab(128, 64, false, false);
         constexpr uint32_t kIdescBf16T = ptx::idesc_bf16_f32_ab(128, 128, false, true);
         // f16 operands: format 0 in both fields
         constexpr uint32_t kFormat = (1u << 7) | (1u << 10);
         constexpr uint32_t IDESC_QK = FP8 ? kIdescBf16 & ~kFormat : kIdescBf16;
         constexpr uint32_t IDESC_PV = FP8 ? kIdescBf16T & ~kFormat : kIdescBf16T;
-        long long ns = 0;            // stages before this item
+        Stage<NST> st;               // of the next chunk: K_0 V_0 K_1 V_1 ... of every item
+        long long ns = 0;            // chunks used
         int nq = 0, nfix = 0;
-        int np[2] = {0, 0}, ni[2] = {0, 0};  // PV products, items with some, of each tile
+        int np[2] = {0, 0}, ni[2] = {0, 0};  // chunks done, items with some, of each tile
         bool ok = true;
-        auto staged = [&](long long s) {  // chunk s is in shared memory, in 16 bits
-          return FP8 ? wait_bar(sm, sm.bar(C::B_WIDE + (int)(s % NST)), (uint32_t)(s / NST) & 1, p.err, 64)
-                     : wait_bar(sm, sm.bar(C::B_FULL + (int)(s % NST)), (uint32_t)(s / NST) & 1, p.err, 65);
-        };
-        auto release = [&](long long s) {
-          ptx::tc_commit(sm.bar((FP8 ? C::B_WIDE_EMPTY : C::B_EMPTY) + (int)(s % NST)));
-        };
+        const int b_staged = FP8 ? C::B_WIDE : C::B_FULL, b_free = FP8 ? C::B_WIDE_EMPTY : C::B_EMPTY;
+        // descriptors of the first tile or stage: others lie so many 16-byte units on
+        const uint64_t q_desc = ptx::smem_desc_sw128(sm.base_u32 + C::OFF_Q, 16, 1024);
+        const uint64_t k_desc = ptx::smem_desc_sw128(sm.base_u32 + C::OFF_ST, 16, 1024);
+        const uint64_t v_desc = ptx::smem_desc_sw128(sm.base_u32 + C::OFF_ST, HALF_B, 1024);
         for (int k = 0; ok; ++k) {
           const int slot = k % NITEM;
-          if (!wait_bar(sm, sm.bar(C::B_ITEM_FULL + slot), (uint32_t)(k / NITEM) & 1, p.err, 66)) break;
-          const int i = ring_s[slot];
+          if (!wait_at(sm, sm.bar(C::B_ITEM_FULL + slot), (uint32_t)(k / NITEM) & 1, p.err, 66)) break;
+          const Item it = items[slot];
           ptx::mbar_arrive(sm.bar(C::B_ITEM_EMPTY + slot));
-          if (i >= total) break;
-          const Item it = item_of<G>(i, tp, p);
+          if (it.r < 0) break;
           if (it.n == 0) continue;
-          ok = wait_bar(sm, sm.bar(C::B_Q_FULL), nq & 1, p.err, 67);
+          ok = wait_at(sm, sm.bar(C::B_Q_FULL), nq & 1, p.err, 67);
           if (FP8)
             for (int t = 0; t < 2; ++t)
-              ok = ok && wait_bar(sm, sm.bar(C::B_Q_READY + t), nq & 1, p.err, 68);
+              ok = ok && wait_at(sm, sm.bar(C::B_Q_READY + t), nq & 1, p.err, 68);
+          Stage<NST> v_st;  // the chunk before's values
           for (int c = 0; c <= it.n && ok; ++c) {
-  #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int pc = c - 1;
-              if (pc >= it.a[t] && pc < it.b[t]) {  // P V of the chunk before
-                const long long s = ns + 2 * pc + 1;
-                ok = ok && staged(s);
-                const bool first = t == 0 || !(pc >= it.a[0] && pc < it.b[0]);
-                if (!FP8 && first && ragged(it, pc)) {
-                  ok = ok && wait_bar(sm, sm.bar(C::B_FIX + nfix % NFIX), (uint32_t)(nfix / NFIX) & 1,
-                                      p.err, 69);
-                  ++nfix;
-                }
-                if (pc == it.a[t] && ni[t] > 0)
-                  ok = ok && wait_bar(sm, sm.bar(C::B_O_EMPTY + t), (ni[t] - 1) & 1, p.err, 70);
-                ok = ok && wait_bar(sm, sm.bar(C::B_P_FULL + t), np[t] & 1, p.err, 71);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint32_t v = sm.base_u32 + C::OFF_ST + (int)(s % NST) * TILE_B;
-  #pragma unroll
-                for (int kk = 0; kk < CHK / 16; ++kk)
-                  mma_from_tmem(tmem + O_COL + 128 * t, tmem + S_COL + 128 * t + 8 * kk,
-                                ptx::smem_desc_sw128(v + kk * 2048, HALF_B, 1024), IDESC_PV,
-                                pc > it.a[t] || kk > 0);
-                ptx::tc_commit(sm.bar(C::B_O_FULL + t));
-                ++np[t];
-                if (t == 1 || !(pc >= it.a[1] && pc < it.b[1])) release(s);
-              }
-              if (c >= it.a[t] && c < it.b[t]) {  // Q K^T, over the weights just used
-                const long long s = ns + 2 * c;
-                ok = ok && staged(s);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint32_t q = sm.base_u32 + C::OFF_Q + t * TILE_B;
-                const uint32_t kb = sm.base_u32 + C::OFF_ST + (int)(s % NST) * TILE_B;
-  #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint32_t at = (kk >> 2) * HALF_B + (kk & 3) * 32;
-                  ptx::tc_mma_f16(tmem + S_COL + 128 * t, ptx::smem_desc_sw128(q + at, 16, 1024),
-                                  ptx::smem_desc_sw128(kb + at, 16, 1024), IDESC_QK, kk > 0);
-                }
-                ptx::tc_commit(sm.bar(C::B_S_FULL + t));
-                if (t == 1 || !(c >= it.a[1] && c < it.b[1])) release(s);
+            const int pc = c - 1;
+            const bool keys = c < it.n, values = c > 0;
+            if (values) {
+              v_st = st;
+              st.next();
+              ok = wait_at(sm, sm.bar(b_staged + v_st.s), v_st.ph, p.err, 64);
+              if (!FP8 && ragged(it, pc)) {
+                ok = ok && wait_at(sm, sm.bar(C::B_FIX + nfix % NFIX), (uint32_t)(nfix / NFIX) & 1,
+                                   p.err, 69);
+                ++nfix;
               }
             }
-            if (c == it.n - 1 && ok) ptx::tc_commit(sm.bar(C::B_Q_EMPTY));
+#pragma unroll
+            for (int ht = 0; ht < 4; ++ht) {
+              const int h = ht >> 1, t = ht & 1;
+              if (!ok) break;
+              if (pc >= it.a[t] && pc < it.b[t]) {  // P V of the chunk before
+                if (h == 0 && pc == it.a[t] && ni[t] > 0)
+                  ok = wait_at(sm, sm.bar(C::B_O_EMPTY + t), (ni[t] - 1) & 1, p.err, 70);
+                ok = ok && wait_at(sm, sm.bar(C::B_P_FULL + 2 * t + h), np[t] & 1, p.err, 71);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint64_t v =
+                    v_desc + (uint32_t)v_st.s * (TILE_B >> 4) + (1 - h) * (4 * 2048 >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_from_tmem(tmem + O_COL + 128 * t, tmem + S_COL + 128 * t + 64 * h + 8 * kk,
+                                v + kk * (2048 >> 4), IDESC_PV, h > 0 || kk > 0 || pc > it.a[t]);
+                ptx::tc_commit(sm.bar(C::B_O_FULL + 2 * t + h));
+                if (h == 1) ++np[t];
+              }
+              if (c >= it.a[t] && c < it.b[t]) {  // Q K^T, over the weights just used
+                ok = wait_at(sm, sm.bar(b_staged + st.s), st.ph, p.err, 65);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint64_t q = q_desc + t * (TILE_B >> 4);
+                const uint64_t kb =
+                    k_desc + (uint32_t)st.s * (TILE_B >> 4) + (1 - h) * (64 * 128 >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const int at = (kk >> 2) * (HALF_B >> 4) + (kk & 3) * 2;
+                  ptx::tc_mma_f16(tmem + S_COL + 128 * t + 64 * h, q + at, kb + at, IDESC_QK, kk > 0);
+                }
+                ptx::tc_commit(sm.bar(C::B_S_FULL + 2 * t + h));
+              }
+            }
+            if (!ok) break;
+            if (values) ptx::tc_commit(sm.bar(b_free + v_st.s));
+            if (keys) {
+              ptx::tc_commit(sm.bar(b_free + st.s));
+              if (c == it.n - 1) ptx::tc_commit(sm.bar(C::B_Q_EMPTY));
+              st.next();
+            }
           }
           if (!ok) break;
           ns += 2 * it.n;
           ++nq;
-  #pragma unroll
+#pragma unroll
           for (int t = 0; t < 2; ++t) ni[t] += it.b[t] > it.a[t];
         }
         // drain: every product and commit issued must have landed before the end
   #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (np[t] > 0) drain_bar(sm.bar(C::B_O_FULL + t), (np[t] - 1) & 1);
+          for (int h = 0; h < 2; ++h)
+            if (np[t] > 0) drain_bar(sm.bar(C::B_O_FULL + 2 * t + h), (np[t] - 1) & 1);
         if (nq > 0) drain_bar(sm.bar(C::B_Q_EMPTY), (nq - 1) & 1);
         for (long long l = ns > NST ? ns - NST : 0; l < ns; ++l)
           drain_bar(sm.bar((FP8 ? C::B_WIDE_EMPTY : C::B_EMPTY) + (int)(l % NST)), (uint32_t)(l / NST) & 1);
@@ -530,19 +648,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     } else {
       // ================= widening (e4m3) and zeroing =================
       const int x = tid - FIX_WARP * 32;
-      long long ns = 0;
+      Stage<NST> st;
+      Stage<FP8 ? C::NRAW : 1> raw_st;
       int nfix = 0;
       for (int k = 0;; ++k) {
-        const int i = read_item(k);
-        if (i >= total) break;
-        const Item it = item_of<G>(i, tp, p);
+        const Item it = read_item(k);
+        if (it.r < 0) break;
         bool ok = true;
         if constexpr (FP8) {
-          for (int st = 0; st < 2 * it.n && ok; ++st, ++ns) {
-            const int s = (int)(ns % NLOAD), w = (int)(ns % NST);
-            const int key0 = (it.j0 + st / 2) * CHK;
-            ok = wait_bar(sm, sm.bar(C::B_FULL + s), (uint32_t)(ns / NLOAD) & 1, p.err, 72) &&
-                 wait_bar(sm, sm.bar(C::B_WIDE_EMPTY + w), ((uint32_t)(ns / NST) & 1) ^ 1, p.err, 73);
+          for (int c = 0; c < 2 * it.n && ok; ++c, raw_st.next(), st.next()) {
+            const int s = raw_st.s, w = st.s;
+            const int key0 = (it.jl - c / 2) * CHK;
+            ok = wait_at(sm, sm.bar(C::B_FULL + s), raw_st.ph, p.err, 72) &&
+                 wait_at(sm, sm.bar(C::B_WIDE_EMPTY + w), st.ph ^ 1, p.err, 73);
             __syncwarp();
             if (!ok) break;
             const unsigned char* raw = sm.base + C::OFF_RAW + s * RAW_B;
@@ -570,17 +688,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         } else {
           // Every chunk is waited for and let go, whether zeroed or not, so that
           // these warps are never a stage's whole round ahead or behind.
-          for (int st = 0; st < 2 * it.n && ok; ++st, ++ns) {
-            const int s = (int)(ns % NST), c = st / 2;
-            ok = wait_bar(sm, sm.bar(C::B_FULL + s), (uint32_t)(ns / NST) & 1, p.err, 74);
+          for (int x2 = 0; x2 < 2 * it.n && ok; ++x2, st.next()) {
+            const int s = st.s, c = x2 / 2;
+            ok = wait_at(sm, sm.bar(C::B_FULL + s), st.ph, p.err, 74);
             __syncwarp();
             if (!ok) break;
-            if (!(st & 1) || !ragged(it, c)) {
+            if (!(x2 & 1) || !ragged(it, c)) {
               if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_EMPTY + s));
               continue;
             }
             unsigned char* v = sm.base + C::OFF_ST + s * TILE_B;
-            const int key0 = (it.j0 + c) * CHK;
+            const int key0 = (it.jl - c) * CHK;
             for (int u = x; u < CHK * 16; u += 64) {
               const int row = u >> 4;
               if (key0 + row < it.kv_lo || key0 + row >= it.kv_end)
@@ -598,7 +716,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
     // ================= softmax and epilogue =================
     const int t = warp >> 2;
     const int row = tid & 127, tok = row / G, hd = row % G;
@@ -607,12 +724,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t o_col = tmem + lane_base + O_COL + 128 * t;
     const float ksc = FP8 ? __ldg(p.k_scale) : 1.f;
     const float vsc = FP8 ? __ldg(p.v_scale) : 1.f;
+    const bool out_aligned = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
     int nc = 0, nq = 0;  // chunks of this tile, items with chunks
+    int merge = -1, np = 0;  // parts written
+    __nv_bfloat16* merge_row = nullptr;
+    auto part_at = [&](int cta, int slot) -> float* {
+      return p.parts + (2 * (int64_t)cta + slot) * kPartWords;
+    };
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      const int i = read_item(k);
-      if (i >= total) break;
-      const Item it = item_of<G>(i, tp, p);
+      const Item it = read_item(k);
+      if (it.r < 0) break;
       const int ntok = t ? it.ntok[1] : it.ntok[0];
       const int first = t ? it.a[1] : it.a[0], last = t ? it.b[1] : it.b[0];
       const bool row_ok = tok < ntok;
@@ -628,14 +750,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       float rs = p.scale_log2;
       if constexpr (FP8) {
         // the row of q as f16, in place, under a power of two of its own
-        ok = wait_bar(sm, sm.bar(C::B_Q_FULL), nq & 1, p.err, 75);
+        ok = wait_at(sm, sm.bar(C::B_Q_FULL), nq & 1, p.err, 75);
         __syncwarp();
         if (!ok) break;
         unsigned char* qrow = sm.base + C::OFF_Q + t * TILE_B + row * 128;
         float amax = 0.f;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const uint4 v = *reinterpret_cast<const uint4*>(qrow + (c >> 3) * HALF_B + ((c & 7) << 4));
+          const uint4 v =
+              *reinterpret_cast<const uint4*>(qrow + (c >> 3) * HALF_B + (((c ^ row) & 7) << 4));
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -647,7 +770,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         rs *= ksc * __int_as_float((127 + e2) << 23);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          uint4* at = reinterpret_cast<uint4*>(qrow + (c >> 3) * HALF_B + ((c & 7) << 4));
+          uint4* at = reinterpret_cast<uint4*>(qrow + (c >> 3) * HALF_B + (((c ^ row) & 7) << 4));
           const uint4 v = *at;
           *at = make_uint4(pack2<true>(bf16_lo(v.x) * inv, bf16_hi(v.x) * inv),
                            pack2<true>(bf16_lo(v.y) * inv, bf16_hi(v.y) * inv),
@@ -665,119 +788,309 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const float slope =
           p.mod.slopes ? __ldg(&p.mod.slopes[it.g * G + hd]) * 1.4426950408889634f : 0.f;
       const int pos0 = it.pos + t * MQ;  // of the tile's first token
+      const bool cap = p.mod.cap_log2 > 0.f;
+      const float ru = rs * p.mod.inv_cap;  // to u = score / cap
+      // The polynomial's coefficients, with the powers of ru in them; where the
+      // highest leaves the normal floats, the cap is taken the other way.  (Rows
+      // under e4m3's scales are multiplied by ru first.)
+      const float ru2 = ru * ru;
+      const bool ru_fits = FP8 || (fabsf(ru) >= 0x1p-13f && fabsf(ru) <= 0x1p13f);
+      float2 k5[5];
+      {
+        float r = ru;
+#pragma unroll
+        for (int x = 0; x < 5; ++x, r *= ru2) k5[x] = both(p.mod.tanh_poly[x] * (FP8 ? 1.f : r));
+      }
       float m_ref = -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
-      for (int c = first; c < last; ++c, ++nc) {
-        float2 s[64];
-        ok = wait_bar(sm, sm.bar(C::B_S_FULL + t), nc & 1, p.err, 76);
+      for (int c2 = 2 * first; c2 < 2 * last; ++c2) {
+        const int h = c2 & 1;
+        const uint32_t sh_col = s_col + 64 * h;
+        ok = wait_at(sm, sm.bar(C::B_S_FULL + 2 * t + h), nc & 1, p.err, 76);
         __syncwarp();
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
+        float2 s[32];
         {
-          float v[4][32];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) ptx::tmem_ld_x32(s_col + 32 * h, v[h]);
+          float v[2][32];
+          ptx::tmem_ld_x32(sh_col, v[0]);
+          ptx::tmem_ld_x32(sh_col + 32, v[1]);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 64; ++e) s[e] = make_float2(v[e >> 4][2 * (e & 15)], v[e >> 4][2 * (e & 15) + 1]);
+          for (int e = 0; e < 32; ++e)
+            s[e] = make_float2(v[e >> 4][2 * (e & 15)], v[e >> 4][2 * (e & 15) + 1]);
         }
-        const int key0 = (it.j0 + c) * CHK;
-        change_scores(s, rs, p.mod, slope, (float)(pos - key0));
-        // every row of a full tile sees every key of a chunk between the last
-        // token's window and the first token
-        const bool whole = ntok == MQ && key0 + CHK <= pos0 + 1 &&
+        const int key0 = it.jl * CHK + 64 - c2 * 64;  // a chunk's later half first
+        // every row of a full tile sees every key between the last token's
+        // window and the first token
+        const bool whole = ntok == MQ && key0 + 64 <= pos0 + 1 &&
                            (p.mod.window <= 0 || key0 >= pos0 + MQ - p.mod.window);
-        if (!whole) {
-          const int kf = low - key0;
-          const unsigned kn = (unsigned)max(0, lim - max(low, 0));
+        float top[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            if ((unsigned)(2 * e - kf) >= kn) s[e].x = -INFINITY;
-            if ((unsigned)(2 * e + 1 - kf) >= kn) s[e].y = -INFINITY;
-          }
+        for (int e = 0; e < 32; ++e) {
+          top[e & 1] = fmaxf(top[e & 1], fmaxf(s[e].x, s[e].y));
+          size[e & 1] = fmaxf(size[e & 1], fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
         }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // The row's largest logit: of whole halves without a bias that of the
+        // raw ones, changed (the cap is monotonic); others are changed first.
+        const bool poly =
+            cap && __all_sync(0xffffffffu, ru_fits && fmaxf(size[0], size[1]) * fabsf(ru) <= 1.f);
+        const bool late = whole && !p.mod.slopes && rs >= 0.f && (poly || !cap);
+        float cm;
+        if (late) {
+          cm = fmaxf(top[0], top[1]) * rs;
+          if (cap)
+            cm = p.mod.cap_log2 * (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(cm * p.mod.inv_cap_log2)));
+        } else {
+          if (poly) {
 #pragma unroll
-        for (int e = 0; e < 64; ++e) m4[e & 3] = fmaxf(m4[e & 3], fmaxf(s[e].x, s[e].y));
-        const float cm = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            for (int e = 0; e < 32; ++e) s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], k5, both(0.f));
+          } else if (cap) {
+            const float re = rs * p.mod.inv_cap_log2, two = -2.f * p.mod.cap_log2;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              s[e].x = fmaf(two, fast_reciprocal(1.f + fast_exp2(s[e].x * re)), p.mod.cap_log2);
+              s[e].y = fmaf(two, fast_reciprocal(1.f + fast_exp2(s[e].y * re)), p.mod.cap_log2);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = mul2(s[e], both(rs));
+          }
+          if (p.mod.slopes) {
+            const float at = (float)(pos - key0);
+            if (__all_sync(0xffffffffu, pos - key0 >= 63)) {  // no key behind a row's own
+              const float base = -slope * at;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                s[e] = add2(s[e], make_float2(fmaf(slope, (float)(2 * e), base),
+                                              fmaf(slope, (float)(2 * e + 1), base)));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                s[e].x = fmaf(-slope, fabsf(at - (float)(2 * e)), s[e].x);
+                s[e].y = fmaf(-slope, fabsf(at - (float)(2 * e + 1)), s[e].y);
+              }
+            }
+          }
+          if (!whole) {
+            const unsigned seen = (unsigned)max(0, lim - low);
+            const int kf = low - key0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if ((unsigned)(2 * e - kf) >= seen) s[e].x = -INFINITY;
+              if ((unsigned)(2 * e + 1 - kf) >= seen) s[e].y = -INFINITY;
+            }
+          }
+          top[0] = top[1] = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) top[e & 1] = fmaxf(top[e & 1], fmaxf(s[e].x, s[e].y));
+          cm = fmaxf(top[0], top[1]);
+        }
         float alpha = 1.f;
         if (cm > m_ref + kRescaleLog2) {
           if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - cm);
           m_ref = cm;
         }
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {  // (never at an item's first chunk)
-          ok = wait_bar(sm, sm.bar(C::B_O_FULL + t), (nc - 1) & 1, p.err, 77);
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {  // (never at an item's first keys)
+          // the products of the half before; those before it are done
+          ok = wait_at(sm, sm.bar(C::B_O_FULL + 2 * t + (h ^ 1)), (h ? nc : nc - 1) & 1, p.err, 77);
           __syncwarp();
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
             float o[32];
-            ptx::tmem_ld_x32(o_col + 32 * h, o);
+            ptx::tmem_ld_x32(o_col + 32 * x, o);
             ptx::tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] *= alpha;
-            ptx::tmem_st_x32(o_col + 32 * h, o);
+            ptx::tmem_st_x32(o_col + 32 * x, o);
           }
           ptx::tmem_st_wait();
           l2.x *= alpha;
           l2.y *= alpha;
         }
         const float2 bias = both(C::kRaise - (m_ref == -INFINITY ? 0.f : m_ref));
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        if (late && cap) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float w[32];
+          for (int e = 0; e < 32; ++e) s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], k5, bias);
+        } else {
+          const float2 factor = both(late ? rs : 1.f);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 y = add2(s[32 * h + e], bias);
-            const float2 q = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            sum[e & 1] = add2(sum[e & 1], q);  // before the 16-bit rounding the MMA sees
-            w[e] = __uint_as_float(pack2<FP8>(q.x, q.y));
-          }
-          ptx::tmem_st_x32(s_col + 32 * h, w);
+          for (int e = 0; e < 32; ++e) s[e] = fma2(s[e], factor, bias);
         }
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float2 q = make_float2(fast_exp2(s[e].x), fast_exp2(s[e].y));
+          sum[e & 1] = add2(sum[e & 1], q);  // before the 16-bit rounding the MMA sees
+          w[e] = __uint_as_float(pack2<FP8>(q.x, q.y));
+        }
+        ptx::tmem_st_x32(sh_col, w);
         l2 = add2(l2, add2(sum[0], sum[1]));
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(sm.bar(C::B_P_FULL + t));
+        ptx::mbar_arrive(sm.bar(C::B_P_FULL + 2 * t + h));
+        nc += h;
       }
       if (!ok) break;
-      if (first == last) continue;  // a tile without tokens
-      ok = wait_bar(sm, sm.bar(C::B_O_FULL + t), (nc - 1) & 1, p.err, 78);
-      __syncwarp();
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      ptx::tc_fence_after();
       const float l = l2.x + l2.y;
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+      float* part = nullptr;
+      if (it.part >= 0) {
+        part = part_at(blockIdx.x, it.part);
+        __stcg(reinterpret_cast<float2*>(part + 256 * D) + tid, make_float2(m_ref, l));
+      }
+      if (first < last) {  // (a tile may have no tokens, or no chunks in this part)
+        ok = wait_at(sm, sm.bar(C::B_O_FULL + 2 * t + 1), (nc - 1) & 1, p.err, 78);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          float o[32];
+          ptx::tmem_ld_x32(o_col + 32 * x, o);
+          ptx::tmem_ld_wait();
+          if (it.part >= 0) {
+            float4* to = reinterpret_cast<float4*>(part) + (t * 32 + 8 * x) * 128 + row;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        float o[32];
-        ptx::tmem_ld_x32(o_col + 32 * h, o);
-        ptx::tmem_ld_wait();
-        if (row_ok) {
+            for (int e = 0; e < 8; ++e)
+              __stcg(to + 128 * e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+          } else if (row_ok) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[4];
+            for (int c = 0; c < 2; ++c) {
+              uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2_rn(o[8 * c + 2 * e] * inv * vsc, o[8 * c + 2 * e + 1] * inv * vsc);
-            reinterpret_cast<uint4*>(orow)[4 * h + c] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int e = 0; e < 8; ++e)
+                w[e] = pack_bf16x2_rn(o[16 * c + 2 * e] * inv * vsc, o[16 * c + 2 * e + 1] * inv * vsc);
+              store_32(orow + 32 * x + 16 * c, w, out_aligned);  // (rows lie apart: whole sectors)
+            }
+          }
+          __syncwarp();
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(sm.bar(C::B_O_EMPTY + t));
+      }
+      if (it.part >= 0) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_PART));
+        if (warp == 0) {  // once both tiles' sums are written
+          ok = wait_at(sm, sm.bar(C::B_PART), np & 1, p.err, 80);
+          if (ok && lane == 0) {
+            ptx::fence_acq_rel_gpu();
+            st_release(&p.flags[2 * blockIdx.x + it.part], p.epoch);
           }
         }
-        __syncwarp();
+        ++np;
+        if (it.merge >= 0) {  // (once: the CTA's first item)
+          merge = it.merge;
+          merge_row = row_ok ? orow : nullptr;
+        }
       }
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(sm.bar(C::B_O_EMPTY + t));
+    }
+    // ---- the item whose end this CTA holds: its parts, in the CTAs' order ----
+    if (ok && merge >= 0) {
+      const int count = j - merge + 1;
+      // the first CTA's part starts the item, the others' go on with it
+      auto cta = [&](int k) { return (merge + k) * p.num_kv_heads + g; };
+      for (int k = lane; k < count; k += 32) {  // (each warp for itself)
+        const long long begun = clock64();
+        while (ld_acquire(&p.flags[2 * cta(k) + (k == 0 ? 1 : 0)]) != p.epoch) {
+          if (clock64() - begun > tc::kWaitClocks) {
+            atomicExch(p.err, 79);
+            ok = false;
+            break;
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_MERGE));
+      if (warp == 0 && wait_at(sm, sm.bar(C::B_MERGE), 0, p.err, 81)) {
+        // all warps have seen the flags: down, for a replay of this launch
+        for (int k = lane; k < count; k += 32) p.flags[2 * cta(k) + (k == 0 ? 1 : 0)] = 0;
+      }
+      __syncwarp();
+      if (ok && merge_row) {
+        // Sums come through shared memory, free by now, in pieces of 64 columns of
+        // a part: 16 copies a thread, of its own row, three pieces ahead.  (By
+        // plain loads, two or three parts took 15 us.)
+        constexpr int kAhead = 3;
+        static_assert(kAhead * 256 * 256 <= C::OFF_BAR, "the pieces' room");
+        const uint32_t own = sm.base_u32 + tid * 16;
+        auto ml_of = [&](int k) {
+          return __ldcg(reinterpret_cast<const float2*>(part_at(cta(k), k == 0 ? 1 : 0) + 256 * D) +
+                        tid);
+        };
+        const int pieces = 2 * count;
+        auto fetch = [&](int i) {  // piece i: columns 64 (i / count) on, of part i % count
+          if (i < pieces) {
+            const int x = i >= count, k = i - x * count;
+            const float4* from =
+                reinterpret_cast<const float4*>(part_at(cta(k), k == 0 ? 1 : 0)) + (t * 32 + 16 * x) * 128 + row;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              cp_async_16(own + ((i % kAhead) * 16 + e) * 4096, from + 128 * e, 16);
+          }
+          cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i);
+        float most = -INFINITY, l = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) most = fmaxf(most, ml_of(k).x);
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) {
+          const float2 ml = ml_of(k);
+          if (ml.x != -INFINITY || ml.y != 0.f) l += fast_exp2(ml.x - most) * ml.y;
+        }
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        float4 sum[16];
+        float2 ml = ml_of(0);
+        for (int i = 0; i < pieces; ++i) {
+          const int x = i >= count, k = i - x * count;
+          const float2 now = ml;
+          ml = ml_of(k + 1 < count ? k + 1 : 0);
+          if (k == 0) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          cp_async_wait<kAhead - 1>();
+          if (now.x != -INFINITY || now.y != 0.f) {  // (else: no keys, or no sums written)
+            const float f = fast_exp2(now.x - most);
+            const float4* v = reinterpret_cast<const float4*>(sm.base) + (i % kAhead) * 16 * 256 + tid;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float4 w = v[256 * e];
+              sum[e].x += f * w.x, sum[e].y += f * w.y, sum[e].z += f * w.z, sum[e].w += f * w.w;
+            }
+          }
+          fetch(i + kAhead);
+          if (k == count - 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[8];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float4 s = sum[4 * e + y];
+                w[2 * y] = pack_bf16x2_rn(s.x * inv * vsc, s.y * inv * vsc);
+                w[2 * y + 1] = pack_bf16x2_rn(s.z * inv * vsc, s.w * inv * vsc);
+              }
+              store_32(merge_row + 64 * x + 16 * e, w, out_aligned);
+            }
+          }
+        }
+        cp_async_wait<0>();
+      }
     }
   }
 
@@ -791,29 +1104,44 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
+// Ranges per head: those whose CTAs fill the SMs best in one round or two.
+int ranges_of(int heads, int num_sms) {
+  int best = 1;
+  auto rounds = [&](int64_t r) { return (r * heads + num_sms - 1) / num_sms; };
+  for (int r = 2; (int64_t)r * heads <= 2 * num_sms; ++r)
+    if (rounds(r) * best < rounds(best) * r) best = r;
+  return best;
+}
+size_t flag_bytes(int64_t ctas) { return (size_t)(ctas * 16 + 255) / 256 * 256; }
+
 template <int G, bool FP8>
 cudaError_t launch_g(const Params& prm, const CUtensorMap& mk, const CUtensorMap& mv,
-                     const CUtensorMap& mq, int num_ctas, cudaStream_t stream) {
+                     const CUtensorMap& mq, cudaStream_t stream) {
   const cudaError_t e = allow_large<prefill_scored_kernel<G, FP8>>();
   if (e != cudaSuccess) return e;
-  return launch_dependent<prefill_scored_kernel<G, FP8>>(dim3(num_ctas), dim3(NTHREADS),
+  return launch_dependent<prefill_scored_kernel<G, FP8>>(dim3(prm.ranges * prm.num_kv_heads), dim3(NTHREADS),
                                                          Cfg<FP8>::SMEM_BYTES, stream, 1, mk, mv,
                                                          mq, prm);
 }
 
 template <bool FP8>
 cudaError_t launch_f(const Params& prm, const CUtensorMap& mk, const CUtensorMap& mv,
-                     const CUtensorMap& mq, int group, int num_ctas, cudaStream_t stream) {
+                     const CUtensorMap& mq, int group, cudaStream_t stream) {
   switch (group) {
-    case 1: return launch_g<1, FP8>(prm, mk, mv, mq, num_ctas, stream);
-    case 2: return launch_g<2, FP8>(prm, mk, mv, mq, num_ctas, stream);
-    case 4: return launch_g<4, FP8>(prm, mk, mv, mq, num_ctas, stream);
-    case 8: return launch_g<8, FP8>(prm, mk, mv, mq, num_ctas, stream);
+    case 1: return launch_g<1, FP8>(prm, mk, mv, mq, stream);
+    case 2: return launch_g<2, FP8>(prm, mk, mv, mq, stream);
+    case 4: return launch_g<4, FP8>(prm, mk, mv, mq, stream);
+    case 8: return launch_g<8, FP8>(prm, mk, mv, mq, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace ps
+
+size_t prefill_scored_workspace_bytes(int num_kv_heads, int num_sms) {
+  const int64_t ctas = (int64_t)ps::ranges_of(num_kv_heads, num_sms) * num_kv_heads;
+  return ps::flag_bytes(ctas) + (size_t)ctas * 2 * ps::kPartWords * 4;
+}
 
 cudaError_t launch_prefill_scored(const PrefillLaunch& a, cudaStream_t stream) {
   using namespace ps;
@@ -858,9 +1186,11 @@ cudaError_t launch_prefill_scored(const PrefillLaunch& a, cudaStream_t stream) {
   prm.seq_lens = a.seq_lens;
   prm.qsl = a.query_start_loc;
   prm.err = static_cast<int*>(a.workspace);
-  prm.next_item = reinterpret_cast<unsigned*>(static_cast<char*>(a.workspace) + 4);
-  const cudaError_t ez = cudaMemsetAsync(prm.next_item, 0, sizeof(unsigned), stream);
-  if (ez != cudaSuccess) return ez;
+  prm.ranges = ranges_of(a.num_kv_heads, a.num_ctas);
+  char* ws = static_cast<char*>(a.workspace) + 256;
+  prm.flags = reinterpret_cast<unsigned long long*>(ws);
+  prm.parts = reinterpret_cast<float*>(ws + flag_bytes(prm.ranges * a.num_kv_heads));
+  prm.epoch = tc::next_call_epoch();
   prm.num_seqs = a.num_seqs;
   prm.num_heads = a.num_heads;
   prm.num_kv_heads = a.num_kv_heads;
@@ -874,8 +1204,8 @@ cudaError_t launch_prefill_scored(const PrefillLaunch& a, cudaStream_t stream) {
   prm.k_scale = a.k_scale;
   prm.v_scale = a.v_scale;
   prm.mod = a.mod;
-  return a.fp8 ? launch_f<true>(prm, mk, mv, mq, group, a.num_ctas, stream)
-               : launch_f<false>(prm, mk, mv, mq, group, a.num_ctas, stream);
+  return a.fp8 ? launch_f<true>(prm, mk, mv, mq, group, stream)
+               : launch_f<false>(prm, mk, mv, mq, group, stream);
 }
 
 }  // namespace pa

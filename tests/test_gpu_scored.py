@@ -293,7 +293,8 @@ def weight_error(kv, d, most, cap, bias, tiles):
     roundings of u: q's and the row's units, the scale), e4m3 tiles hold q in
     three e4m3 parts (2^-12).  The cap adds 2^-20 of itself (one exponential,
     one sum, one reciprocal, each off by 2^-22 relative in a quotient of at
-    most 2) and 4 u of the score; a bias three u of itself.  exp2 and its
+    most 2; on the tiles a polynomial within 2.8e-6 < 2^-18.4 and six roundings of
+    u) and 4 u of the score; a bias three u of itself.  exp2 and its
     argument: 2^-21.  Weights enter P V in two bf16 parts (2^-16), one f16 part
     over 8-bit elements (half a step: 2^-11), or on the tiles in one bf16 part
     (2^-9) or two e4m3 parts (2^-8)."""
@@ -303,7 +304,7 @@ def weight_error(kv, d, most, cap, bias, tiles):
     else:
         e += 2 ** -9 if tiles else 2 ** -16 if kv == "bf16" else 2 ** -11
     if cap:
-        e += 2 ** -20 * cap + 2 ** -22 * min(most, cap)
+        e += (2 ** -18 if tiles else 2 ** -20) * cap + 2 ** -22 * min(most, cap)
     return e + 3 * 2 ** -24 * bias
 
 
