@@ -172,12 +172,12 @@ pa_status check_score(const pa_score_desc& s, float scale, int32_t max_blocks, i
   *mod = {};
   mod->cap_log2 = s.cap * 1.4426950408889634f;
   mod->inv_cap_log2 = s.cap > 0.f ? 2.f / s.cap : 0.f;
-  // an odd polynomial for tanh on [-1, 1], fitted to the smallest largest error
-  // (2.8e-6)
-  constexpr float kTanh[5] = {0.99996847f, -0.33265823f, 0.12922066f, -0.04329985f, 0.0083658816f};
+  // an odd polynomial for tanh on [-3/4, 3/4], fitted to the smallest largest
+  // error (3.6e-6)
+  constexpr float kTanh[4] = {0.9999556f, -0.33222765f, 0.12577091f, -0.033778276f};
   if (s.cap > 0.f) {
     mod->inv_cap = 1.f / mod->cap_log2;
-    for (int k = 0; k < 5; ++k) mod->tanh_poly[k] = mod->cap_log2 * kTanh[k];
+    for (int k = 0; k < 4; ++k) mod->tanh_poly[k] = mod->cap_log2 * kTanh[k];
   }
   mod->slopes = s.slopes;
   mod->window = s.window;

@@ -80,7 +80,7 @@ struct ScoreMod {
   float cap_log2;      // > 0: s2 -> cap_log2 tanh(s2 / cap_log2)
   float inv_cap_log2;  // 2 log2(e) / cap_log2
   float inv_cap;       // 1 / cap_log2
-  float tanh_poly[5];  // cap_log2 tanh(u) = u sum_k tanh_poly[k] u^2k, |u| <= 1
+  float tanh_poly[4];  // cap_log2 tanh(u) = u sum_k tanh_poly[k] u^2k, |u| <= 3/4
   const float* slopes;          // [H] or null
   const int32_t* prefix_lens;   // [S] or null
   int32_t window;               // > 0: keys of the last `window` positions only

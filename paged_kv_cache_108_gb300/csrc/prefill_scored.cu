@@ -22,12 +22,14 @@
 // Tensor memory is full: S_00 S_01 S_10 S_11 of 64 columns (P over them), O_0
 // and O_1 of 128.  (With whole chunks in one buffer a tile's softmax waited
 // 1600 of its 5200 clocks a chunk for the products.)
+// Capped logits without a bias need no running max over a bf16 cache: they lie
+// within the cap, and bf16 and fp32 hold 2^-100 to 2^100.  Elsewhere
 // O is rescaled only when a row's running max grows by more than 2^8; all lanes
 // of the row's warp take part (by 1), as tensor memory accesses are a warp's.
 //
-// The cap.  tanh(u) for |u| <= 1 is an odd polynomial of degree 9 (fitted to
-// the smallest largest error over [0, 1]: 2.8e-6, which a cap of 50 makes 1.4e-4
-// of a weight, a fourteenth of its 16-bit rounding), six FMAs a logit; a half chunk with a larger |u| in one of the
+// The cap.  tanh(u) for |u| <= 3/4 is an odd polynomial of degree 7 (fitted to
+// the smallest largest error over that range: 3.6e-6, which a cap of 50 makes
+// 1.8e-4 of a weight, a tenth of its 16-bit rounding), five FMAs a logit; a half chunk with a larger |u| in one of the
 // warp's rows takes 1 - 2 / (1 + e^2u), one exponential and one reciprocal.
 //
 // An e4m3 cache: two warps widen each chunk to f16 (exact) in shared memory;
@@ -289,12 +291,11 @@ __device__ __forceinline__ bool ragged(const Item& it, int c) {
   return key0 < it.kv_lo || key0 + CHK > it.kv_end;
 }
 
-// cap tanh(s rs / cap) + bias in log2 units for |s rs| <= cap, the cap's and
-// the scale's factors being in the coefficients: one square, five products.
-__device__ __forceinline__ float2 capped_poly(float2 s, const float2 (&k)[5], float2 bias) {
+// cap tanh(s rs / cap) + bias in log2 units for |s rs| <= 3/4 cap, the cap's
+// and the scale's factors being in the coefficients.
+__device__ __forceinline__ float2 capped_poly(float2 s, const float2 (&k)[4], float2 bias) {
   const float2 z = mul2(s, s);
-  float2 f = fma2(k[4], z, k[3]);
-  f = fma2(f, z, k[2]);
+  float2 f = fma2(k[3], z, k[2]);
   f = fma2(f, z, k[1]);
   f = fma2(f, z, k[0]);
   return fma2(f, s, bias);
@@ -795,13 +796,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // under e4m3's scales are multiplied by ru first.)
       const float ru2 = ru * ru;
       const bool ru_fits = FP8 || (fabsf(ru) >= 0x1p-13f && fabsf(ru) <= 0x1p13f);
-      float2 k5[5];
+      float2 poly_k[4];
       {
         float r = ru;
 #pragma unroll
-        for (int x = 0; x < 5; ++x, r *= ru2) k5[x] = both(p.mod.tanh_poly[x] * (FP8 ? 1.f : r));
+        for (int x = 0; x < 4; ++x, r *= ru2) poly_k[x] = both(p.mod.tanh_poly[x] * (FP8 ? 1.f : r));
       }
-      float m_ref = -INFINITY;
+      // capped, without a bias, over bf16: weights are 2^s as it is
+      const bool bounded = !FP8 && cap && !p.mod.slopes && p.mod.cap_log2 <= 100.f;
+      float m_ref = bounded && first < last ? 0.f : -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       for (int c2 = 2 * first; c2 < 2 * last; ++c2) {
         const int h = c2 & 1;
@@ -829,25 +832,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const bool whole = ntok == MQ && key0 + 64 <= pos0 + 1 &&
                            (p.mod.window <= 0 || key0 >= pos0 + MQ - p.mod.window);
         float top[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
+        if (!bounded) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          top[e & 1] = fmaxf(top[e & 1], fmaxf(s[e].x, s[e].y));
-          size[e & 1] = fmaxf(size[e & 1], fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
+          for (int e = 0; e < 32; ++e) top[e & 1] = fmaxf(top[e & 1], fmaxf(s[e].x, s[e].y));
+        }
+        if (cap) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            size[e & 1] = fmaxf(size[e & 1], fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
         }
         // The row's largest logit: of whole halves without a bias that of the
         // raw ones, changed (the cap is monotonic); others are changed first.
         const bool poly =
-            cap && __all_sync(0xffffffffu, ru_fits && fmaxf(size[0], size[1]) * fabsf(ru) <= 1.f);
-        const bool late = whole && !p.mod.slopes && rs >= 0.f && (poly || !cap);
-        float cm;
-        if (late) {
+            cap && __all_sync(0xffffffffu, ru_fits && fmaxf(size[0], size[1]) * fabsf(ru) <= 0.75f);
+        const bool late = whole && !p.mod.slopes && (bounded || rs >= 0.f) && (poly || !cap);
+        float cm = 0.f;
+        if (late && !bounded) {
           cm = fmaxf(top[0], top[1]) * rs;
           if (cap)
             cm = p.mod.cap_log2 * (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(cm * p.mod.inv_cap_log2)));
-        } else {
+        } else if (!late) {
           if (poly) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], k5, both(0.f));
+            for (int e = 0; e < 32; ++e) s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], poly_k, both(0.f));
           } else if (cap) {
             const float re = rs * p.mod.inv_cap_log2, two = -2.f * p.mod.cap_log2;
 #pragma unroll
@@ -884,10 +891,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               if ((unsigned)(2 * e + 1 - kf) >= seen) s[e].y = -INFINITY;
             }
           }
-          top[0] = top[1] = -INFINITY;
+          if (!bounded) {
+            top[0] = top[1] = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) top[e & 1] = fmaxf(top[e & 1], fmaxf(s[e].x, s[e].y));
-          cm = fmaxf(top[0], top[1]);
+            for (int e = 0; e < 32; ++e) top[e & 1] = fmaxf(top[e & 1], fmaxf(s[e].x, s[e].y));
+            cm = fmaxf(top[0], top[1]);
+          }
         }
         float alpha = 1.f;
         if (cm > m_ref + kRescaleLog2) {
@@ -919,7 +928,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const float2 bias = both(C::kRaise - (m_ref == -INFINITY ? 0.f : m_ref));
         if (late && cap) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], k5, bias);
+          for (int e = 0; e < 32; ++e) s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], poly_k, bias);
         } else {
           const float2 factor = both(late ? rs : 1.f);
 #pragma unroll

@@ -293,7 +293,7 @@ def weight_error(kv, d, most, cap, bias, tiles):
     roundings of u: q's and the row's units, the scale), e4m3 tiles hold q in
     three e4m3 parts (2^-12).  The cap adds 2^-20 of itself (one exponential,
     one sum, one reciprocal, each off by 2^-22 relative in a quotient of at
-    most 2; on the tiles a polynomial within 2.8e-6 < 2^-18.4 and six roundings of
+    most 2; on the tiles a polynomial within 3.7e-6 < 2^-18 and six roundings of
     u) and 4 u of the score; a bias three u of itself.  exp2 and its
     argument: 2^-21.  Weights enter P V in two bf16 parts (2^-16), one f16 part
     over 8-bit elements (half a step: 2^-11), or on the tiles in one bf16 part
