@@ -12,16 +12,16 @@
 //
 // A work item is a pair of neighbouring query tiles of one request and KV head:
 // 2 x 128 rows, row = token * G + query head in the group.  Both tiles use
-// each K and V chunk of 128 keys while it is in shared memory.  A chunk's keys
-// are taken in two halves, each with logits of its own in tensor memory, so
-// that a tile's softmax of one half runs while the products of the other do:
-//   S_th = Q_t K_h^T   M = 128 rows, N = 64 keys, K = 128, into tensor memory
-//   P_th               one thread a row: 64 logits from tensor memory, changed,
-//                      masked, exponentiated; 16-bit weights back over S_th
-//   O_t += P_th V_h    A = P_th from tensor memory, B = V's rows, MN-major
-// Tensor memory is full: S_00 S_01 S_10 S_11 of 64 columns (P over them), O_0
-// and O_1 of 128.  (With whole chunks in one buffer a tile's softmax waited
-// 1600 of its 5200 clocks a chunk for the products.)
+// each K and V chunk of 128 keys while it is in shared memory, and alternate on
+// the tensor cores: while one tile's softmax runs, the other's products do.
+//   S_t = Q_t K^T      M = 128 rows, N = 128 keys, K = 128, into tensor memory
+//   P_th               one thread a row, a half h of 64 logits at a time: changed,
+//                      masked, exponentiated; 16-bit weights back over them
+//   O_t += P_th V_h    A = P_th from tensor memory, B = V's rows, MN-major: of
+//                      the first half while the second's softmax runs
+// Tensor memory is full: S_0, S_1 (P over them), O_0, O_1 of 128 columns.
+// (Halves with logits and products of their own, N = 64, took 136 us for four
+// capped prompts of 2048.)
 // Capped logits without a bias need no running max over a bf16 cache: they lie
 // within the cap, and bf16 and fp32 hold 2^-100 to 2^100.  Elsewhere
 // O is rescaled only when a row's running max grows by more than 2^8; all lanes
@@ -105,7 +105,7 @@ struct Cfg {
   static constexpr int B_Q_FULL = 0, B_Q_EMPTY = 1, B_Q_READY = 2 /* [2] */, B_FULL = 4,
                        B_EMPTY = B_FULL + NLOAD, B_WIDE = B_EMPTY + NLOAD,
                        B_WIDE_EMPTY = B_WIDE + NST, B_FIX = B_WIDE_EMPTY + NST,
-                       B_S_FULL = B_FIX + NFIX /* [tile][half] */, B_P_FULL = B_S_FULL + 4,
+                       B_S_FULL = B_FIX + NFIX, B_P_FULL = B_S_FULL + 2 /* [tile][half] */,
                        B_O_FULL = B_P_FULL + 4, B_O_EMPTY = B_O_FULL + 4, B_ITEM_FULL = B_O_EMPTY + 2,
                        B_ITEM_EMPTY = B_ITEM_FULL + NITEM, B_PART = B_ITEM_EMPTY + NITEM,
                        B_MERGE = B_PART + 1, NBARS = B_MERGE + 1;
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     } else if (warp == MMA_WARP) {
       // ================= MMAs =================
       if (lane == 0) {
-        constexpr uint32_t kIdescBf16 = ptx::idesc_bf16_f32_ab(128, 64, false, false);
+        constexpr uint32_t kIdescBf16 = ptx::idesc_bf16_f32_ab(128, 128, false, false);
         constexpr uint32_t kIdescBf16T = ptx::idesc_bf16_f32_ab(128, 128, false, true);
         // f16 operands: format 0 in both fields
         constexpr uint32_t kFormat = (1u << 7) | (1u << 10);
@@ -603,24 +603,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                     v_desc + (uint32_t)v_st.s * (TILE_B >> 4) + (1 - h) * (4 * 2048 >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  mma_from_tmem(tmem + O_COL + 128 * t, tmem + S_COL + 128 * t + 64 * h + 8 * kk,
+                  mma_from_tmem(tmem + O_COL + 128 * t, tmem + S_COL + 128 * t + 64 * (1 - h) + 8 * kk,
                                 v + kk * (2048 >> 4), IDESC_PV, h > 0 || kk > 0 || pc > it.a[t]);
                 ptx::tc_commit(sm.bar(C::B_O_FULL + 2 * t + h));
                 if (h == 1) ++np[t];
               }
-              if (c >= it.a[t] && c < it.b[t]) {  // Q K^T, over the weights just used
+              if (h == 1 && c >= it.a[t] && c < it.b[t]) {  // Q K^T, over the weights just used
                 ok = wait_at(sm, sm.bar(b_staged + st.s), st.ph, p.err, 65);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const uint64_t q = q_desc + t * (TILE_B >> 4);
-                const uint64_t kb =
-                    k_desc + (uint32_t)st.s * (TILE_B >> 4) + (1 - h) * (64 * 128 >> 4);
+                const uint64_t kb = k_desc + (uint32_t)st.s * (TILE_B >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                   const int at = (kk >> 2) * (HALF_B >> 4) + (kk & 3) * 2;
-                  ptx::tc_mma_f16(tmem + S_COL + 128 * t + 64 * h, q + at, kb + at, IDESC_QK, kk > 0);
+                  ptx::tc_mma_f16(tmem + S_COL + 128 * t, q + at, kb + at, IDESC_QK, kk > 0);
                 }
-                ptx::tc_commit(sm.bar(C::B_S_FULL + 2 * t + h));
+                ptx::tc_commit(sm.bar(C::B_S_FULL + t));
               }
             }
             if (!ok) break;
@@ -808,14 +807,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       float2 l2 = make_float2(0.f, 0.f);
       for (int c2 = 2 * first; c2 < 2 * last; ++c2) {
         const int h = c2 & 1;
-        const uint32_t sh_col = s_col + 64 * h;
-        ok = wait_at(sm, sm.bar(C::B_S_FULL + 2 * t + h), nc & 1, p.err, 76);
-        __syncwarp();
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
+        const uint32_t sh_col = s_col + 64 * (1 - h);  // a chunk's later half first
+        if (h == 0) {
+          ok = wait_at(sm, sm.bar(C::B_S_FULL + t), nc & 1, p.err, 76);
+          __syncwarp();
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
         }
-        ptx::tc_fence_after();
         float2 s[32];
         {
           float v[2][32];
@@ -826,7 +827,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int e = 0; e < 32; ++e)
             s[e] = make_float2(v[e >> 4][2 * (e & 15)], v[e >> 4][2 * (e & 15) + 1]);
         }
-        const int key0 = it.jl * CHK + 64 - c2 * 64;  // a chunk's later half first
+        const int key0 = it.jl * CHK + 64 - c2 * 64;
         // every row of a full tile sees every key between the last token's
         // window and the first token
         const bool whole = ntok == MQ && key0 + 64 <= pos0 + 1 &&
