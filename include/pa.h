@@ -727,11 +727,15 @@ typedef struct {
   const float* slopes;
 } pa_score_desc;
 
-/* Workspace bytes of pa_decode_scored (num_rows: sequences) and
- * pa_varlen_scored (num_rows: new tokens), on the current device; 0 for bad
- * sizes.  A workspace that is large enough serves calls of any sizes that
- * need no more, on one stream; calls that share one must not overlap on the
- * GPU.  It needs no initialisation. */
+/* Workspace bytes that serve both pa_decode_scored (num_rows: sequences) and
+ * pa_varlen_scored (num_rows: new tokens) on the current device; 0 for bad
+ * sizes.  (Partial sums of the work that the SMs share: up to 5 MB, or with
+ * head_dim 128 and more than 8 rows 40 to 81 MB, whatever the lengths.)  A
+ * workspace serves calls of any sizes that need no more, on one stream; calls
+ * that share one must not overlap on the GPU.  It needs no initialisation.
+ * The calls set its word 0 (int32) to a nonzero code if a bounded wait inside
+ * a kernel expired, or (tiles) a block id was out of range; they never clear
+ * it.  After such a code it must be zeroed before the call's graph is replayed. */
 size_t pa_scored_workspace_size(int32_t num_rows, int32_t num_heads, int32_t num_kv_heads,
                                 int32_t head_dim);
 
@@ -760,14 +764,13 @@ pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const 
  *                is cut.
  *  workspace     >= pa_scored_workspace_size(num_tokens, ...) bytes, 256-byte
  *                aligned.
- *  Steps with more than 2 new tokens per request on average run on the
- *  tensor-core prefill tiles, for a bf16 or e4m3 cache with head_dim 128,
+ *  Steps of many new tokens run on tensor-core tiles (more than 2 per request
+ *  on average and 8 in all over bf16, 4 and 16 over e4m3), with head_dim 128,
  *  block_size >= 8, at most 256 requests and 65535 new tokens; a request that
  *  sees more than max_blocks_per_seq * block_size keys then gets zero rows,
- *  and workspace word 0 (int32) is set to a nonzero code if a bounded wait
- *  expired or a block id was out of range; the library never clears it.  All
- *  other steps are computed row by row, each new token reading its keys (long
- *  prompts over 8-bit rows are better gathered first).
+ *  and a block outside the pool is replaced by block 0.  All other steps are
+ *  computed row by row, each new token reading its keys (long prompts over
+ *  8-bit rows are better gathered first).
  *  A request whose new tokens exceed its seq_len gets zero rows.  Rows of out
  *  before query_start_loc[0] or behind query_start_loc[num_seqs] are left as
  *  they were.

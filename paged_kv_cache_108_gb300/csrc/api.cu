@@ -22,9 +22,16 @@ constexpr int kMaxPartition = 65536;
 // take the tensor-core prefill tiles
 constexpr int kTileMinTokens = 16;
 
-// pa_varlen_scored: up to this many new tokens per request on average each
-// is a row of its own, with more the tensor-core tiles serve them
-constexpr int kRowsPerRequest = 2;
+// pa_varlen_scored: up to this many new tokens per request on average, or in
+// all, each is a row of its own; with more the tensor-core tiles serve them.
+// Rows read their keys once each, the tiles once for all but after some 15 us of
+// set-up and joining (bf16, us by rows and by tiles: 16 requests of 2000 tokens,
+// 3 new each: 51, 48; 8 each: 98, 49; one of 4000, 4 new: 17, 31; 16 new: 40, 31.
+// e4m3: 3 new each 35, 55; 8 each 62, 55; one request's 16 new 27, 33).
+struct RowsRule {
+  int per_request, in_all;
+};
+constexpr RowsRule kRowsBf16 = {2, 8}, kRowsE4m3 = {4, 16};
 
 bool is_pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
@@ -341,9 +348,10 @@ pa_status scored_rows(const char* fn, void* out, const void* q, const void* k_ca
     return fail(PA_ERR_INVALID, "misaligned pointer");
   const int group = num_heads / cache.num_kv_heads;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const RowsRule rows = cache.dtype == PA_KV_BF16 ? kRowsBf16 : kRowsE4m3;
   const bool tiles =
-      starts && cache.dtype != PA_KV_INT8 && num_rows > kRowsPerRequest * (int64_t)num_seqs &&
-      num_rows <= 65535 &&
+      starts && cache.dtype != PA_KV_INT8 && num_rows > rows.in_all &&
+      num_rows > rows.per_request * (int64_t)num_seqs && num_rows <= 65535 &&
       pa::prefill_supported(cache.head_dim, group, cache.dtype == PA_KV_FP8_E4M3, num_seqs,
                             cache.block_size);
   const size_t need =
@@ -1247,8 +1255,7 @@ size_t pa_scored_workspace_size(int32_t num_rows, int32_t num_heads, int32_t num
     return 0;
   const size_t rows =
       pa::scored_workspace_bytes(num_rows, num_heads, num_kv_heads, head_dim, num_sms());
-  // (tiles: more than kRowsPerRequest tokens of a request)
-  const size_t tiles = head_dim == 128 && num_rows > kRowsPerRequest
+  const size_t tiles = head_dim == 128 && num_rows > kRowsBf16.in_all
                            ? pa::prefill_scored_workspace_bytes(num_kv_heads, num_sms())
                            : 0;
   return kScoredHead + (rows > tiles ? rows : tiles);

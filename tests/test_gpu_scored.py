@@ -481,7 +481,9 @@ def test_prompts_match_oracle(kv, case):
     ops.varlen_scored(out, q, c["kc"], c["vc"], _dev(c["tables"]), _dev(lens), _dev(starts),
                       c["scale"], prefix_lens=None if prefix is None else _dev(prefix),
                       workspace=ws, **_mod(c, cap, window, bias))
-    tiles = (kv != "int8" and d == 128 and B >= 8 and q.shape[0] > 2 * len(lens))
+    n = q.shape[0]
+    tiles = (kv != "int8" and d == 128 and B >= 8
+             and (n > 8 and n > 2 * len(lens) if kv == "bf16" else n > 16 and n > 4 * len(lens)))
     if tiles:
         assert int(ws[:4].view(torch.int32).item()) == 0
     assert (out[int(starts[-1]):] == 7.0).all()  # rows behind the last request
