@@ -56,7 +56,6 @@ namespace {
 
 constexpr int kCtasPerSm = 2;     // what registers and shared memory are kept to
 constexpr int kWholeUnits = 6;    // units per CTA from which none is split
-constexpr int kMinSteps = 1;      // steps of a CTA at least, where units are split
 
 template <int D, int G, KvFormat F>
 struct Cfg {
@@ -102,15 +101,6 @@ __device__ __forceinline__ uint32_t widen_alternate(uint32_t w, bool odd) {
     return widen_int8(w, odd ? 0x4341 : 0x4240);
   else
     return widen((uint16_t)__byte_perm(w, 0, odd ? 0x4431 : 0x4420));
-}
-
-__device__ __forceinline__ void st_release(unsigned long long* p, unsigned long long v) {
-  asm volatile("st.release.gpu.u64 [%0], %1;\n" ::"l"(p), "l"(v) : "memory");
-}
-__device__ __forceinline__ unsigned long long ld_acquire(const unsigned long long* p) {
-  unsigned long long v;
-  asm volatile("ld.acquire.gpu.u64 %0, [%1];\n" : "=l"(v) : "l"(p) : "memory");
-  return v;
 }
 
 // The factor of a part whose running max is m under the whole's max; 1 where
@@ -258,7 +248,7 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
         K = end;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) K += s_others[w];
-        ctas = (int)min((long long)(gridDim.x / hkv), max(1ll, K / kMinSteps));
+        ctas = (int)min((long long)(gridDim.x / hkv), K);  // (K is not 0)
         if (part >= ctas) return;
         lo = tc::range_lo(part, K, ctas);
         hi = tc::range_lo(part + 1, K, ctas);

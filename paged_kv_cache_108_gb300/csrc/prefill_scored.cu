@@ -23,14 +23,16 @@
 // (Halves with logits and products of their own, N = 64, took 136 us for four
 // capped prompts of 2048.)
 // Capped logits without a bias need no running max over a bf16 cache: they lie
-// within the cap, and bf16 and fp32 hold 2^-100 to 2^100.  Elsewhere
-// O is rescaled only when a row's running max grows by more than 2^8; all lanes
+// within the cap, and for a cap up to 55 weights from 2^-80 to 2^80 leave bf16
+// and the fp32 sums room for values and counts (2^127 = 2^80 2^17 keys 2^30 of a
+// value).  Elsewhere O is rescaled only when a row's running max grows by more than 2^8; all lanes
 // of the row's warp take part (by 1), as tensor memory accesses are a warp's.
 //
 // The cap.  tanh(u) for |u| <= 3/4 is an odd polynomial of degree 7 (fitted to
 // the smallest largest error over that range: 3.6e-6, which a cap of 50 makes
-// 1.8e-4 of a weight, a tenth of its 16-bit rounding), five FMAs a logit; a half chunk with a larger |u| in one of the
-// warp's rows takes 1 - 2 / (1 + e^2u), one exponential and one reciprocal.
+// 1.8e-4 of a weight, a tenth of its 16-bit rounding), five FMAs a logit; a half
+// chunk with a larger |u| in one of the warp's rows takes 1 - 2 / (1 + e^2u), one
+// exponential and one reciprocal.
 //
 // An e4m3 cache: two warps widen each chunk to f16 (exact) in shared memory;
 // q, scaled by a power of two a row that puts its largest |q| in [1, 2), is
@@ -87,6 +89,7 @@ constexpr int kMinUnits = 2;            // units of a CTA at least, where there 
 constexpr int NFIX = 4;                 // zeroed V chunks ahead of their MMA, at most
 constexpr int S_COL = 0, O_COL = 256;   // tile t: + 128 t; logits of the h-th half: + 64 h
 constexpr float kRescaleLog2 = 8.f;
+constexpr float kBoundedLog2 = 80.f;    // caps up to this need no running max
 
 constexpr int kItemBytes = 80;
 // Sums of an item's 2 x 128 rows: [tile][column / 4][row] float4, then
@@ -130,22 +133,13 @@ struct Params {
   float* parts;                 // [CTAs][2][kPartWords]
   unsigned long long epoch;
   int ranges;                   // CTAs of a head
-  int num_seqs, num_heads, num_kv_heads, max_blocks, num_blocks, block_size, log2_bs;
+  int num_seqs, num_tokens, num_heads, num_kv_heads, max_blocks, num_blocks, block_size, log2_bs;
   int box_tok, log2_box;
   float scale_log2;
   const float* k_scale;  // e4m3: device scalars
   const float* v_scale;
   ScoreMod mod;
 };
-
-__device__ __forceinline__ void st_release(unsigned long long* p, unsigned long long v) {
-  asm volatile("st.release.gpu.u64 [%0], %1;\n" ::"l"(p), "l"(v) : "memory");
-}
-__device__ __forceinline__ unsigned long long ld_acquire(const unsigned long long* p) {
-  unsigned long long v;
-  asm volatile("ld.acquire.gpu.u64 %0, [%1];\n" : "=l"(v) : "l"(p) : "memory");
-  return v;
-}
 
 // A wait that the other side usually has ended: the test comes first.
 __device__ __forceinline__ bool wait_at(const Smem& sm, uint32_t bar, uint32_t parity, int* err,
@@ -531,7 +525,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                                  (uint32_t)(lane * p.box_tok) * 128u;
             const int off = (key0 + lane * p.box_tok) & (p.block_size - 1);
             ptx::tma_load_4d(dst, tm, sm.bar(C::B_FULL + s), 0, it.g, off, phys);
-            if (!FP8) ptx::tma_load_4d(dst + HALF_B, tm, sm.bar(C::B_FULL + s), 64, it.g, off, phys);
+            if (!FP8)
+              ptx::tma_load_4d(dst + HALF_B, tm, sm.bar(C::B_FULL + s), 64, it.g, off, phys);
           }
           st.next();
           ++ns;
@@ -637,13 +632,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int t = 0; t < 2; ++t) ni[t] += it.b[t] > it.a[t];
         }
         // drain: every product and commit issued must have landed before the end
-  #pragma unroll
+#pragma unroll
         for (int t = 0; t < 2; ++t)
           for (int h = 0; h < 2; ++h)
             if (np[t] > 0) drain_bar(sm.bar(C::B_O_FULL + 2 * t + h), (np[t] - 1) & 1);
         if (nq > 0) drain_bar(sm.bar(C::B_Q_EMPTY), (nq - 1) & 1);
         for (long long l = ns > NST ? ns - NST : 0; l < ns; ++l)
-          drain_bar(sm.bar((FP8 ? C::B_WIDE_EMPTY : C::B_EMPTY) + (int)(l % NST)), (uint32_t)(l / NST) & 1);
+          drain_bar(sm.bar(b_free + (int)(l % NST)), (uint32_t)(l / NST) & 1);
       }
     } else {
       // ================= widening (e4m3) and zeroing =================
@@ -667,11 +662,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             unsigned char* wide = sm.base + C::OFF_ST + w * TILE_B;
             // 16 elements at a time; 8 lanes take 4 pieces of two neighbouring
             // rows, whose stores then fall in different banks
-  #pragma unroll 4
+#pragma unroll 4
             for (int u = x; u < CHK * 8; u += 64) {
               const int pc = u & 3, row = ((u >> 3) & ~1) | ((u >> 2) & 1), half = (u >> 3) & 1;
               const int piece = 4 * half + pc;
-              uint4 v = *reinterpret_cast<const uint4*>(raw + row * 128 + ((piece ^ (row & 7)) << 4));
+              uint4 v =
+                  *reinterpret_cast<const uint4*>(raw + row * 128 + ((piece ^ (row & 7)) << 4));
               if (key0 + row < it.kv_lo || key0 + row >= it.kv_end) v = make_uint4(0, 0, 0, 0);
               unsigned char* to = wide + half * HALF_B + row * 128;
               *reinterpret_cast<uint4*>(to + (((2 * pc) ^ (row & 7)) << 4)) =
@@ -737,9 +733,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (it.r < 0) break;
       const int ntok = t ? it.ntok[1] : it.ntok[0];
       const int first = t ? it.a[1] : it.a[0], last = t ? it.b[1] : it.b[0];
-      const bool row_ok = tok < ntok;
+      // (nothing is written outside the batch, whatever the starts say)
+      const bool row_ok =
+          tok < ntok && (unsigned)(it.q0 + t * MQ + tok) < (unsigned)p.num_tokens;
       const int pos = it.pos + t * MQ + tok;
-      __nv_bfloat16* orow = p.out + ((int64_t)(it.q0 + t * MQ + tok) * p.num_heads + it.g * G + hd) * D;
+      __nv_bfloat16* orow =
+          p.out + ((int64_t)(it.q0 + t * MQ + tok) * p.num_heads + it.g * G + hd) * D;
       if (it.n == 0) {
         if (row_ok) {
 #pragma unroll
@@ -802,7 +801,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int x = 0; x < 4; ++x, r *= ru2) poly_k[x] = both(p.mod.tanh_poly[x] * (FP8 ? 1.f : r));
       }
       // capped, without a bias, over bf16: weights are 2^s as it is
-      const bool bounded = !FP8 && cap && !p.mod.slopes && p.mod.cap_log2 <= 100.f;
+      const bool bounded = !FP8 && cap && !p.mod.slopes && p.mod.cap_log2 <= kBoundedLog2;
       float m_ref = bounded && first < last ? 0.f : -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       for (int c2 = 2 * first; c2 < 2 * last; ++c2) {
@@ -851,11 +850,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (late && !bounded) {
           cm = fmaxf(top[0], top[1]) * rs;
           if (cap)
-            cm = p.mod.cap_log2 * (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(cm * p.mod.inv_cap_log2)));
+            cm = p.mod.cap_log2 *
+                 (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(cm * p.mod.inv_cap_log2)));
         } else if (!late) {
           if (poly) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], poly_k, both(0.f));
+            for (int e = 0; e < 32; ++e)
+              s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], poly_k, both(0.f));
           } else if (cap) {
             const float re = rs * p.mod.inv_cap_log2, two = -2.f * p.mod.cap_log2;
 #pragma unroll
@@ -929,7 +930,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const float2 bias = both(C::kRaise - (m_ref == -INFINITY ? 0.f : m_ref));
         if (late && cap) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], poly_k, bias);
+          for (int e = 0; e < 32; ++e)
+            s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], poly_k, bias);
         } else {
           const float2 factor = both(late ? rs : 1.f);
 #pragma unroll
@@ -940,8 +942,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const float2 q = make_float2(fast_exp2(s[e].x), fast_exp2(s[e].y));
-          sum[e & 1] = add2(sum[e & 1], q);  // before the 16-bit rounding the MMA sees
-          w[e] = __uint_as_float(pack2<FP8>(q.x, q.y));
+          const uint32_t w2 = pack2<FP8>(q.x, q.y);
+          w[e] = __uint_as_float(w2);
+          // bf16: the sum is of the weights as rounded, so that a large one's
+          // rounding (2^-9) leaves the quotient; f16's 2^-12 may stay in
+          sum[e & 1] = add2(sum[e & 1], FP8 ? q : make_float2(bf16_lo(w2), bf16_hi(w2)));
         }
         ptx::tmem_st_x32(sh_col, w);
         l2 = add2(l2, add2(sum[0], sum[1]));
@@ -1025,14 +1030,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
       if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_MERGE));
-      if (warp == 0 && wait_at(sm, sm.bar(C::B_MERGE), 0, p.err, 81)) {
-        // all warps have seen the flags: down, for a replay of this launch
+      // Both tiles' warps are done with their items: shared memory is free (a last
+      // item may have products for one tile alone), and all have seen the flags.
+      const bool all = wait_at(sm, sm.bar(C::B_MERGE), 0, p.err, 81);
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok && all);
+      if (ok && warp == 0) {  // down, for a replay of this launch
         for (int k = lane; k < count; k += 32) p.flags[2 * cta(k) + (k == 0 ? 1 : 0)] = 0;
       }
-      __syncwarp();
       if (ok && merge_row) {
-        // Sums come through shared memory, free by now, in pieces of 64 columns of
-        // a part: 16 copies a thread, of its own row, three pieces ahead.  (By
+        // Sums come through shared memory, in pieces of 64 columns of a part: 16 copies a thread, of its own row, three pieces ahead.  (By
         // plain loads, two or three parts took 15 us.)
         constexpr int kAhead = 3;
         static_assert(kAhead * 256 * 256 <= C::OFF_BAR, "the pieces' room");
@@ -1046,7 +1053,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (i < pieces) {
             const int x = i >= count, k = i - x * count;
             const float4* from =
-                reinterpret_cast<const float4*>(part_at(cta(k), k == 0 ? 1 : 0)) + (t * 32 + 16 * x) * 128 + row;
+                reinterpret_cast<const float4*>(part_at(cta(k), k == 0 ? 1 : 0)) +
+                (t * 32 + 16 * x) * 128 + row;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               cp_async_16(own + ((i % kAhead) * 16 + e) * 4096, from + 128 * e, 16);
@@ -1077,7 +1085,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           cp_async_wait<kAhead - 1>();
           if (now.x != -INFINITY || now.y != 0.f) {  // (else: no keys, or no sums written)
             const float f = fast_exp2(now.x - most);
-            const float4* v = reinterpret_cast<const float4*>(sm.base) + (i % kAhead) * 16 * 256 + tid;
+            const float4* v =
+                reinterpret_cast<const float4*>(sm.base) + (i % kAhead) * 16 * 256 + tid;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const float4 w = v[256 * e];
@@ -1129,9 +1138,9 @@ cudaError_t launch_g(const Params& prm, const CUtensorMap& mk, const CUtensorMap
                      const CUtensorMap& mq, cudaStream_t stream) {
   const cudaError_t e = allow_large<prefill_scored_kernel<G, FP8>>();
   if (e != cudaSuccess) return e;
-  return launch_dependent<prefill_scored_kernel<G, FP8>>(dim3(prm.ranges * prm.num_kv_heads), dim3(NTHREADS),
-                                                         Cfg<FP8>::SMEM_BYTES, stream, 1, mk, mv,
-                                                         mq, prm);
+  return launch_dependent<prefill_scored_kernel<G, FP8>>(
+      dim3(prm.ranges * prm.num_kv_heads), dim3(NTHREADS), Cfg<FP8>::SMEM_BYTES, stream, 1, mk, mv, mq,
+      prm);
 }
 
 template <bool FP8>
@@ -1149,7 +1158,8 @@ cudaError_t launch_f(const Params& prm, const CUtensorMap& mk, const CUtensorMap
 }  // namespace ps
 
 size_t prefill_scored_workspace_bytes(int num_kv_heads, int num_sms) {
-  const int64_t ctas = (int64_t)ps::ranges_of(num_kv_heads, num_sms) * num_kv_heads;
+  const int64_t ranges = ps::ranges_of(num_kv_heads, num_sms), ctas = ranges * num_kv_heads;
+  if (ranges == 1) return 0;  // nothing is split
   return ps::flag_bytes(ctas) + (size_t)ctas * 2 * ps::kPartWords * 4;
 }
 
@@ -1202,6 +1212,7 @@ cudaError_t launch_prefill_scored(const PrefillLaunch& a, cudaStream_t stream) {
   prm.parts = reinterpret_cast<float*>(ws + flag_bytes(prm.ranges * a.num_kv_heads));
   prm.epoch = tc::next_call_epoch();
   prm.num_seqs = a.num_seqs;
+  prm.num_tokens = a.num_tokens;
   prm.num_heads = a.num_heads;
   prm.num_kv_heads = a.num_kv_heads;
   prm.max_blocks = a.max_blocks;
