@@ -70,11 +70,6 @@ bool tc_supported(int head_dim, int group, bool fp8, int num_seqs, int block_siz
 size_t tc_workspace_bytes(int64_t num_seqs, int64_t num_heads, int64_t max_ctx, int num_ctas,
                           int tokens_per_seq = 1);
 cudaError_t launch_decode_tc(const TcLaunch& a, cudaStream_t stream);
-// The head-packed tensor-core kernel (decode_hp.cu): a bf16 cache, one token
-// per sequence, GQA group 1, 2 or 4, H_kv a multiple of its heads per tile
-// (16 for group 1, else 8); any block size (head-major tiles for blocks of
-// at least 128 / that many tokens, token-major below).
-// Takes the same TcLaunch (fp8, tokens_per_seq and non_causal unused).
 // What changes a score before the softmax (log2 units where named so).
 struct ScoreMod {
   float cap_log2;      // > 0: s2 -> cap_log2 tanh(s2 / cap_log2)
@@ -115,6 +110,11 @@ cudaError_t launch_prefill_tc(const PrefillLaunch& a, cudaStream_t stream);
 size_t prefill_scored_workspace_bytes(int num_kv_heads, int num_sms);
 cudaError_t launch_prefill_scored(const PrefillLaunch& a, cudaStream_t stream);
 
+// The head-packed tensor-core kernel (decode_hp.cu): a bf16 cache, one token
+// per sequence, GQA group 1, 2 or 4, H_kv a multiple of its heads per tile
+// (16 for group 1, else 8); any block size (head-major tiles for blocks of
+// at least 128 / that many tokens, token-major below).
+// Takes the same TcLaunch (fp8, tokens_per_seq and non_causal unused).
 bool hp_supported(int head_dim, int group, bool fp8, int num_seqs, int num_kv_heads,
                   int block_size, int tokens_per_seq);
 size_t hp_workspace_bytes(int64_t num_seqs, int64_t num_heads, int num_ctas);

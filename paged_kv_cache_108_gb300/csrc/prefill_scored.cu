@@ -62,6 +62,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "launch.cuh"
 #include "mma_ptx.cuh"
@@ -81,8 +82,8 @@ constexpr int kMaxReqs = 256;
 constexpr int HALF_B = 128 * 128;       // 128 rows of 64 16-bit columns
 constexpr int TILE_B = 2 * HALF_B;      // a q tile, a K or V chunk in 16 bits
 constexpr int RAW_B = CHK * D;          // a K or V chunk in e4m3
-constexpr int NTHREADS = 384;
-constexpr int PROD_WARP = 8, MMA_WARP = 9, FIX_WARP = 10;
+constexpr int NTHREADS = 640;
+constexpr int PROD_WARP = 16, MMA_WARP = 17, FIX_WARP = 18;
 constexpr int NITEM = 4;                // items published ahead
 constexpr int kItemCost = 1;            // of an item, in chunks
 constexpr int kMinUnits = 2;            // units of a CTA at least, where there are few
@@ -98,18 +99,19 @@ constexpr int kPartWords = 2 * 128 * (D + 2);
 
 template <bool FP8>
 struct Cfg {
-  static constexpr int NST = FP8 ? 3 : 5;   // 16-bit chunks in shared memory
+  static constexpr int NST = FP8 ? 3 : 4;   // 16-bit chunks in shared memory
   static constexpr int NRAW = FP8 ? 3 : 0;  // e4m3 chunks
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_ST = OFF_Q + 2 * TILE_B;
   static constexpr int OFF_RAW = OFF_ST + NST * TILE_B;
-  static constexpr int OFF_BAR = OFF_RAW + NRAW * RAW_B;
+  static constexpr int OFF_X = OFF_RAW + NRAW * RAW_B;  // [2 uses][tile][half][row] words exchanged
+  static constexpr int OFF_BAR = OFF_X + 2 * 2 * 2 * 128 * 4;
   static constexpr int NLOAD = FP8 ? NRAW : NST;  // stages that TMA fills
   static constexpr int B_Q_FULL = 0, B_Q_EMPTY = 1, B_Q_READY = 2 /* [2] */, B_FULL = 4,
                        B_EMPTY = B_FULL + NLOAD, B_WIDE = B_EMPTY + NLOAD,
                        B_WIDE_EMPTY = B_WIDE + NST, B_FIX = B_WIDE_EMPTY + NST,
-                       B_S_FULL = B_FIX + NFIX, B_P_FULL = B_S_FULL + 2 /* [tile][half] */,
-                       B_O_FULL = B_P_FULL + 4, B_O_EMPTY = B_O_FULL + 4, B_ITEM_FULL = B_O_EMPTY + 2,
+                       B_S_FULL = B_FIX + NFIX, B_P_FULL = B_S_FULL + 2, B_O_FULL = B_P_FULL + 2,
+                       B_O_EMPTY = B_O_FULL + 2, B_X = B_O_EMPTY + 2, B_ITEM_FULL = B_X + 2,
                        B_ITEM_EMPTY = B_ITEM_FULL + NITEM, B_PART = B_ITEM_EMPTY + NITEM,
                        B_MERGE = B_PART + 1, NBARS = B_MERGE + 1;
   static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
@@ -287,11 +289,11 @@ __device__ __forceinline__ bool ragged(const Item& it, int c) {
 
 // cap tanh(s rs / cap) + bias in log2 units for |s rs| <= 3/4 cap, the cap's
 // and the scale's factors being in the coefficients.
-__device__ __forceinline__ float2 capped_poly(float2 s, const float2 (&k)[4], float2 bias) {
+__device__ __forceinline__ float2 capped_poly(float2 s, const float (&k)[4], float2 bias) {
   const float2 z = mul2(s, s);
-  float2 f = fma2(k[3], z, k[2]);
-  f = fma2(f, z, k[1]);
-  f = fma2(f, z, k[0]);
+  float2 f = fma2(both(k[3]), z, both(k[2]));
+  f = fma2(f, z, both(k[1]));
+  f = fma2(f, z, both(k[0]));
   return fma2(f, s, bias);
 }
 
@@ -325,9 +327,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < C::NBARS; ++i) {
       uint32_t cnt = 1;
-      if ((i >= C::B_Q_READY && i < C::B_Q_READY + 2) || (i >= C::B_P_FULL && i < C::B_P_FULL + 4) ||
-          (i >= C::B_O_EMPTY && i < C::B_O_EMPTY + 2))
-        cnt = 128;
+      if (i >= C::B_Q_READY && i < C::B_Q_READY + 2) cnt = 256;
+      // a tile's softmax warps
+      if ((i >= C::B_P_FULL && i < C::B_P_FULL + 2) || (i >= C::B_O_EMPTY && i < C::B_O_EMPTY + 2) ||
+          (i >= C::B_X && i < C::B_X + 2))
+        cnt = 8;
       // the MMAs, and the two zeroing warps
       if (!FP8 && i >= C::B_EMPTY && i < C::B_EMPTY + NLOAD) cnt = 3;
       // the two widening or zeroing warps' threads
@@ -335,9 +339,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           (i >= C::B_WIDE && i < C::B_WIDE + NST) || (i >= C::B_FIX && i < C::B_FIX + NFIX))
         cnt = 64;
       // the softmax warps
-      if (i == C::B_PART || i == C::B_MERGE) cnt = 8;
-      // an item is read by the MMA thread, 8 softmax warps and those two
-      if (i >= C::B_ITEM_EMPTY && i < C::B_ITEM_EMPTY + NITEM) cnt = 11;
+      if (i == C::B_PART || i == C::B_MERGE) cnt = 16;
+      // an item is read by the MMA thread, 16 softmax warps and those two
+      if (i >= C::B_ITEM_EMPTY && i < C::B_ITEM_EMPTY + NITEM) cnt = 19;
       ptx::mbar_init(sm.bar(i), cnt);
     }
     *sm.abort_flag() = 0;
@@ -542,110 +546,133 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     } else if (warp == MMA_WARP) {
       // ================= MMAs =================
-      if (lane == 0) {
-        constexpr uint32_t kIdescBf16 = ptx::idesc_bf16_f32_ab(128, 128, false, false);
-        constexpr uint32_t kIdescBf16T = ptx::idesc_bf16_f32_ab(128, 128, false, true);
-        // f16 operands: format 0 in both fields
-        constexpr uint32_t kFormat = (1u << 7) | (1u << 10);
-        constexpr uint32_t IDESC_QK = FP8 ? kIdescBf16 & ~kFormat : kIdescBf16;
-        constexpr uint32_t IDESC_PV = FP8 ? kIdescBf16T & ~kFormat : kIdescBf16T;
-        Stage<NST> st;               // of the next chunk: K_0 V_0 K_1 V_1 ... of every item
-        long long ns = 0;            // chunks used
-        int nq = 0, nfix = 0;
-        int np[2] = {0, 0}, ni[2] = {0, 0};  // chunks done, items with some, of each tile
-        bool ok = true;
-        const int b_staged = FP8 ? C::B_WIDE : C::B_FULL, b_free = FP8 ? C::B_WIDE_EMPTY : C::B_EMPTY;
-        // descriptors of the first tile or stage: others lie so many 16-byte units on
-        const uint64_t q_desc = ptx::smem_desc_sw128(sm.base_u32 + C::OFF_Q, 16, 1024);
-        const uint64_t k_desc = ptx::smem_desc_sw128(sm.base_u32 + C::OFF_ST, 16, 1024);
-        const uint64_t v_desc = ptx::smem_desc_sw128(sm.base_u32 + C::OFF_ST, HALF_B, 1024);
-        for (int k = 0; ok; ++k) {
-          const int slot = k % NITEM;
-          if (!wait_at(sm, sm.bar(C::B_ITEM_FULL + slot), (uint32_t)(k / NITEM) & 1, p.err, 66)) break;
-          const Item it = items[slot];
-          ptx::mbar_arrive(sm.bar(C::B_ITEM_EMPTY + slot));
-          if (it.r < 0) break;
-          if (it.n == 0) continue;
-          ok = wait_at(sm, sm.bar(C::B_Q_FULL), nq & 1, p.err, 67);
-          if (FP8)
-            for (int t = 0; t < 2; ++t)
-              ok = ok && wait_at(sm, sm.bar(C::B_Q_READY + t), nq & 1, p.err, 68);
-          Stage<NST> v_st;  // the chunk before's values
-          for (int c = 0; c <= it.n && ok; ++c) {
-            const int pc = c - 1;
-            const bool keys = c < it.n, values = c > 0;
-            if (values) {
-              v_st = st;
-              st.next();
-              ok = wait_at(sm, sm.bar(b_staged + v_st.s), v_st.ph, p.err, 64);
-              if (!FP8 && ragged(it, pc)) {
-                ok = ok && wait_at(sm, sm.bar(C::B_FIX + nfix % NFIX), (uint32_t)(nfix / NFIX) & 1,
-                                   p.err, 69);
-                ++nfix;
-              }
+      // The whole warp walks the chunks with values it knows to be the same in all
+      // lanes, one lane issues.
+      constexpr uint32_t kIdescBf16 = ptx::idesc_bf16_f32_ab(128, 128, false, false);
+      constexpr uint32_t kIdescBf16T = ptx::idesc_bf16_f32_ab(128, 128, false, true);
+      // f16 operands: format 0 in both fields
+      constexpr uint32_t kFormat = (1u << 7) | (1u << 10);
+      constexpr uint32_t IDESC_QK = FP8 ? kIdescBf16 & ~kFormat : kIdescBf16;
+      constexpr uint32_t IDESC_PV = FP8 ? kIdescBf16T & ~kFormat : kIdescBf16T;
+      constexpr int b_staged = FP8 ? C::B_WIDE : C::B_FULL;
+      constexpr int b_free = FP8 ? C::B_WIDE_EMPTY : C::B_EMPTY;
+      Stage<NST> st;     // of the next chunk: K_0 V_0 K_1 V_1 ... of every item
+      long long ns = 0;  // chunks used
+      int nq = 0, nfix = 0;
+      int np[2] = {0, 0}, ni[2] = {0, 0};  // chunks done, items with some, of each tile
+      // descriptors of the first tile or stage: others lie so many 16-byte units on
+      const uint32_t base = __reduce_or_sync(0xffffffffu, sm.base_u32);
+      const uint32_t tm = __reduce_or_sync(0xffffffffu, tmem);
+      const uint64_t q_desc = ptx::smem_desc_sw128(base + C::OFF_Q, 16, 1024);
+      const uint64_t k_desc = ptx::smem_desc_sw128(base + C::OFF_ST, 16, 1024);
+      const uint64_t v_desc = ptx::smem_desc_sw128(base + C::OFF_ST, HALF_B, 1024);
+      const bool leader = ptx::elect_one();
+      auto wait = [&](int bar, uint32_t parity, int code) -> bool {
+        return __all_sync(0xffffffffu, wait_at(sm, sm.bar(bar), parity, p.err, code)) != 0;
+      };
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const int slot = k % NITEM;
+        if (!wait(C::B_ITEM_FULL + slot, (uint32_t)(k / NITEM) & 1, 66)) break;
+        auto field = [&](const int& x) { return (int)__reduce_or_sync(0xffffffffu, (unsigned)x); };
+        const Item& in = items[slot];
+        Item it;
+        it.r = field(in.r), it.n = field(in.n), it.jl = field(in.jl);
+        it.kv_lo = field(in.kv_lo), it.kv_end = field(in.kv_end);
+        const int from[2] = {field(in.a[0]), field(in.a[1])}, to[2] = {field(in.b[0]), field(in.b[1])};
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_ITEM_EMPTY + slot));
+        if (it.r < 0) break;
+        if (it.n == 0) continue;
+        ok = wait(C::B_Q_FULL, nq & 1, 67);
+        if (FP8)
+          for (int t = 0; t < 2; ++t) ok = ok && wait(C::B_Q_READY + t, nq & 1, 68);
+        int v_st = 0;  // the chunk before's values
+        for (int c = 0; c <= it.n && ok; ++c) {
+          const int pc = c - 1;
+          const bool keys = c < it.n, values = c > 0;
+          if (values) {
+            v_st = st.s;
+            ok = wait(b_staged + v_st, st.ph, 64);
+            if (!FP8 && ragged(it, pc)) {
+              ok = ok && wait(C::B_FIX + nfix % NFIX, (uint32_t)(nfix / NFIX) & 1, 69);
+              ++nfix;
             }
+            st.next();
+          }
+          if (keys) ok = ok && wait(b_staged + st.s, st.ph, 65);
+          if (!ok) break;
 #pragma unroll
-            for (int ht = 0; ht < 4; ++ht) {
-              const int h = ht >> 1, t = ht & 1;
+          for (int t = 0; t < 2; ++t) {
+            const uint32_t s_tm = tm + S_COL + 128 * t, o_tm = tm + O_COL + 128 * t;
+            if (pc >= from[t] && pc < to[t]) {  // P V of the chunk before
+              if (pc == from[t] && ni[t] > 0) ok = ok && wait(C::B_O_EMPTY + t, (ni[t] - 1) & 1, 70);
+              ok = ok && wait(C::B_P_FULL + t, np[t] & 1, 71);
               if (!ok) break;
-              if (pc >= it.a[t] && pc < it.b[t]) {  // P V of the chunk before
-                if (h == 0 && pc == it.a[t] && ni[t] > 0)
-                  ok = wait_at(sm, sm.bar(C::B_O_EMPTY + t), (ni[t] - 1) & 1, p.err, 70);
-                ok = ok && wait_at(sm, sm.bar(C::B_P_FULL + 2 * t + h), np[t] & 1, p.err, 71);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint64_t v =
-                    v_desc + (uint32_t)v_st.s * (TILE_B >> 4) + (1 - h) * (4 * 2048 >> 4);
+              ptx::tc_fence_after();
+              const uint64_t v = v_desc + (uint32_t)v_st * (TILE_B >> 4);
+              const uint32_t add = pc > from[t];
+              if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_from_tmem(tmem + O_COL + 128 * t, tmem + S_COL + 128 * t + 64 * (1 - h) + 8 * kk,
-                                v + kk * (2048 >> 4), IDESC_PV, h > 0 || kk > 0 || pc > it.a[t]);
-                ptx::tc_commit(sm.bar(C::B_O_FULL + 2 * t + h));
-                if (h == 1) ++np[t];
+                for (int kk = 0; kk < 8; ++kk)  // weights lie over the first half of their logits
+                  mma_from_tmem(o_tm, s_tm + 64 * (kk >> 2) + 8 * (kk & 3), v + kk * (2048 >> 4),
+                                IDESC_PV, kk > 0 ? 1u : add);
+                ptx::tc_commit(sm.bar(C::B_O_FULL + t));
               }
-              if (h == 1 && c >= it.a[t] && c < it.b[t]) {  // Q K^T, over the weights just used
-                ok = wait_at(sm, sm.bar(b_staged + st.s), st.ph, p.err, 65);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const uint64_t q = q_desc + t * (TILE_B >> 4);
-                const uint64_t kb = k_desc + (uint32_t)st.s * (TILE_B >> 4);
+              __syncwarp();
+              ++np[t];
+            }
+            if (c >= from[t] && c < to[t]) {  // Q K^T, over the weights just used
+              ptx::tc_fence_after();
+              const uint64_t q = q_desc + t * (TILE_B >> 4);
+              const uint64_t kb = k_desc + (uint32_t)st.s * (TILE_B >> 4);
+              if (leader) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                   const int at = (kk >> 2) * (HALF_B >> 4) + (kk & 3) * 2;
-                  ptx::tc_mma_f16(tmem + S_COL + 128 * t, q + at, kb + at, IDESC_QK, kk > 0);
+                  ptx::tc_mma_f16(s_tm, q + at, kb + at, IDESC_QK, kk > 0);
                 }
                 ptx::tc_commit(sm.bar(C::B_S_FULL + t));
               }
-            }
-            if (!ok) break;
-            if (values) ptx::tc_commit(sm.bar(b_free + v_st.s));
-            if (keys) {
-              ptx::tc_commit(sm.bar(b_free + st.s));
-              if (c == it.n - 1) ptx::tc_commit(sm.bar(C::B_Q_EMPTY));
-              st.next();
+              __syncwarp();
             }
           }
           if (!ok) break;
-          ns += 2 * it.n;
-          ++nq;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) ni[t] += it.b[t] > it.a[t];
+          if (leader) {
+            if (values) ptx::tc_commit(sm.bar(b_free + v_st));
+            if (keys) ptx::tc_commit(sm.bar(b_free + st.s));
+            if (c == it.n - 1) ptx::tc_commit(sm.bar(C::B_Q_EMPTY));
+          }
+          __syncwarp();
+          if (keys) st.next();
         }
-        // drain: every product and commit issued must have landed before the end
+        if (!ok) break;
+        ns += 2 * it.n;
+        ++nq;
 #pragma unroll
+        for (int t = 0; t < 2; ++t) ni[t] += to[t] > from[t];
+      }
+      // drain: every product and commit issued must have landed before the end
+      if (leader) {
         for (int t = 0; t < 2; ++t)
-          for (int h = 0; h < 2; ++h)
-            if (np[t] > 0) drain_bar(sm.bar(C::B_O_FULL + 2 * t + h), (np[t] - 1) & 1);
+          if (np[t] > 0) drain_bar(sm.bar(C::B_O_FULL + t), (np[t] - 1) & 1);
         if (nq > 0) drain_bar(sm.bar(C::B_Q_EMPTY), (nq - 1) & 1);
         for (long long l = ns > NST ? ns - NST : 0; l < ns; ++l)
           drain_bar(sm.bar(b_free + (int)(l % NST)), (uint32_t)(l / NST) & 1);
       }
+      __syncwarp();
     } else {
       // ================= widening (e4m3) and zeroing =================
       const int x = tid - FIX_WARP * 32;
       Stage<NST> st;
       Stage<FP8 ? C::NRAW : 1> raw_st;
       int nfix = 0;
+      // e4m3: 16 elements at a time, of rows row0, row0 + 8 ...; 8 lanes take 4
+      // pieces of two neighbouring rows, whose stores then fall in different banks
+      const int row0 = ((x >> 3) & ~1) | ((x >> 2) & 1), piece = x & 3, side = (x >> 3) & 1;
+      const int from = row0 * 128 + (((4 * side + piece) ^ row0) << 4);
+      const int to0 = side * HALF_B + row0 * 128 + (((2 * piece) ^ row0) << 4);
+      const int to1 = side * HALF_B + row0 * 128 + (((2 * piece + 1) ^ row0) << 4);
       for (int k = 0;; ++k) {
         const Item it = read_item(k);
         if (it.r < 0) break;
@@ -658,25 +685,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                  wait_at(sm, sm.bar(C::B_WIDE_EMPTY + w), st.ph ^ 1, p.err, 73);
             __syncwarp();
             if (!ok) break;
-            const unsigned char* raw = sm.base + C::OFF_RAW + s * RAW_B;
+            const unsigned char* raw = sm.base + C::OFF_RAW + s * RAW_B + from;
             unsigned char* wide = sm.base + C::OFF_ST + w * TILE_B;
-            // 16 elements at a time; 8 lanes take 4 pieces of two neighbouring
-            // rows, whose stores then fall in different banks
+            const int low = it.kv_lo - key0 - row0, end = it.kv_end - key0 - row0;
+            auto widen_all = [&](auto cut) {
 #pragma unroll 4
-            for (int u = x; u < CHK * 8; u += 64) {
-              const int pc = u & 3, row = ((u >> 3) & ~1) | ((u >> 2) & 1), half = (u >> 3) & 1;
-              const int piece = 4 * half + pc;
-              uint4 v =
-                  *reinterpret_cast<const uint4*>(raw + row * 128 + ((piece ^ (row & 7)) << 4));
-              if (key0 + row < it.kv_lo || key0 + row >= it.kv_end) v = make_uint4(0, 0, 0, 0);
-              unsigned char* to = wide + half * HALF_B + row * 128;
-              *reinterpret_cast<uint4*>(to + (((2 * pc) ^ (row & 7)) << 4)) =
-                  make_uint4(widen((uint16_t)v.x), widen((uint16_t)(v.x >> 16)),
-                             widen((uint16_t)v.y), widen((uint16_t)(v.y >> 16)));
-              *reinterpret_cast<uint4*>(to + (((2 * pc + 1) ^ (row & 7)) << 4)) =
-                  make_uint4(widen((uint16_t)v.z), widen((uint16_t)(v.z >> 16)),
-                             widen((uint16_t)v.w), widen((uint16_t)(v.w >> 16)));
-            }
+              for (int i = 0; i < CHK / 8; ++i) {
+                uint4 v = *reinterpret_cast<const uint4*>(raw + i * 1024);
+                if (cut.value && (8 * i < low || 8 * i >= end)) v = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(wide + to0 + i * 1024) =
+                    make_uint4(widen((uint16_t)v.x), widen((uint16_t)(v.x >> 16)),
+                               widen((uint16_t)v.y), widen((uint16_t)(v.y >> 16)));
+                *reinterpret_cast<uint4*>(wide + to1 + i * 1024) =
+                    make_uint4(widen((uint16_t)v.z), widen((uint16_t)(v.z >> 16)),
+                               widen((uint16_t)v.w), widen((uint16_t)(v.w >> 16)));
+              }
+            };
+            if (ragged(it, c / 2)) widen_all(std::true_type());
+            else widen_all(std::false_type());
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(sm.bar(C::B_WIDE + w));
             ptx::mbar_arrive(sm.bar(C::B_EMPTY + s));
@@ -713,63 +739,79 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     }
   } else {
     // ================= softmax and epilogue =================
-    const int t = warp >> 2;
+    const int t = warp >> 3, half = (warp >> 2) & 1;
     const int row = tid & 127, tok = row / G, hd = row % G;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lane_base + S_COL + 128 * t;
-    const uint32_t o_col = tmem + lane_base + O_COL + 128 * t;
+    const uint32_t s_col = tmem + lane_base + S_COL + 128 * t + 64 * half;
+    const uint32_t o_col = tmem + lane_base + O_COL + 128 * t + 64 * half;
     const float ksc = FP8 ? __ldg(p.k_scale) : 1.f;
     const float vsc = FP8 ? __ldg(p.v_scale) : 1.f;
     const bool out_aligned = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
-    int nc = 0, nq = 0;  // chunks of this tile, items with chunks
+    int nc = 0, nq = 0, nx = 0;  // chunks of this tile, items with chunks, exchanges
     int merge = -1, np = 0;  // parts written
     __nv_bfloat16* merge_row = nullptr;
     auto part_at = [&](int cta, int slot) -> float* {
       return p.parts + (2 * (int64_t)cta + slot) * kPartWords;
     };
     bool ok = true;
+    // By a whole warp: whether all of its lanes' waits ended.
+    auto wait = [&](int bar, uint32_t parity, int code) -> bool {
+      const bool mine = wait_at(sm, sm.bar(bar), parity, p.err, code);
+      __syncwarp();
+      return __all_sync(0xffffffffu, mine);
+    };
+    // A word of the row's other half for one of this half's.
+    auto exchange = [&](float mine) -> float {
+      float* at = reinterpret_cast<float*>(sm.base + C::OFF_X) + ((nx & 1) * 2 + t) * 256 + row;
+      at[128 * half] = mine;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_X + t));
+      ok = wait(C::B_X + t, nx & 1, 82);
+      ++nx;
+      return at[128 * (half ^ 1)];
+    };
     for (int k = 0; ok; ++k) {
       const Item it = read_item(k);
       if (it.r < 0) break;
       const int ntok = t ? it.ntok[1] : it.ntok[0];
       const int first = t ? it.a[1] : it.a[0], last = t ? it.b[1] : it.b[0];
       // (nothing is written outside the batch, whatever the starts say)
-      const bool row_ok =
-          tok < ntok && (unsigned)(it.q0 + t * MQ + tok) < (unsigned)p.num_tokens;
+      const bool row_ok = tok < ntok && (unsigned)(it.q0 + t * MQ + tok) < (unsigned)p.num_tokens;
       const int pos = it.pos + t * MQ + tok;
-      __nv_bfloat16* orow =
-          p.out + ((int64_t)(it.q0 + t * MQ + tok) * p.num_heads + it.g * G + hd) * D;
+      __nv_bfloat16* orow = p.out +
+                            ((int64_t)(it.q0 + t * MQ + tok) * p.num_heads + it.g * G + hd) * D +
+                            64 * half;
       if (it.n == 0) {
         if (row_ok) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < 8; ++c) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0, 0, 0, 0);
         }
         continue;
       }
       float rs = p.scale_log2;
       if constexpr (FP8) {
-        // the row of q as f16, in place, under a power of two of its own
-        ok = wait_at(sm, sm.bar(C::B_Q_FULL), nq & 1, p.err, 75);
-        __syncwarp();
+        // the row's half of q as f16, in place, under the row's own power of two
+        ok = wait(C::B_Q_FULL, nq & 1, 75);
         if (!ok) break;
-        unsigned char* qrow = sm.base + C::OFF_Q + t * TILE_B + row * 128;
+        unsigned char* qrow = sm.base + C::OFF_Q + t * TILE_B + half * HALF_B + row * 128;
         float amax = 0.f;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint4 v =
-              *reinterpret_cast<const uint4*>(qrow + (c >> 3) * HALF_B + (((c ^ row) & 7) << 4));
+        for (int c = 0; c < 8; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(qrow + (((c ^ row) & 7) << 4));
           const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
         }
+        amax = fmaxf(amax, exchange(amax));
+        if (!ok) break;
         // (kept within the normal floats; an infinite or NaN q stays what it is)
         const int e2 = min(max((int)(__float_as_uint(amax) >> 23), 1), 253) - 127;
         const float inv = __int_as_float((127 - e2) << 23);
         rs *= ksc * __int_as_float((127 + e2) << 23);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          uint4* at = reinterpret_cast<uint4*>(qrow + (c >> 3) * HALF_B + (((c ^ row) & 7) << 4));
+        for (int c = 0; c < 8; ++c) {
+          uint4* at = reinterpret_cast<uint4*>(qrow + (((c ^ row) & 7) << 4));
           const uint4 v = *at;
           *at = make_uint4(pack2<true>(bf16_lo(v.x) * inv, bf16_hi(v.x) * inv),
                            pack2<true>(bf16_lo(v.y) * inv, bf16_hi(v.y) * inv),
@@ -784,6 +826,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       int lim = row_ok ? pos + 1 : 0, low = 0;
       if (row_ok && pos < it.prefix) lim = max(lim, it.prefix);
       if (p.mod.window > 0) low = max(0, pos - p.mod.window + 1);
+      const unsigned seen = (unsigned)max(0, lim - low);
       const float slope =
           p.mod.slopes ? __ldg(&p.mod.slopes[it.g * G + hd]) * 1.4426950408889634f : 0.f;
       const int pos0 = it.pos + t * MQ;  // of the tile's first token
@@ -794,190 +837,215 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // under e4m3's scales are multiplied by ru first.)
       const float ru2 = ru * ru;
       const bool ru_fits = FP8 || (fabsf(ru) >= 0x1p-13f && fabsf(ru) <= 0x1p13f);
-      float2 poly_k[4];
+      float poly_k[4];
       {
         float r = ru;
 #pragma unroll
-        for (int x = 0; x < 4; ++x, r *= ru2) poly_k[x] = both(p.mod.tanh_poly[x] * (FP8 ? 1.f : r));
+        for (int x = 0; x < 4; ++x, r *= ru2) poly_k[x] = p.mod.tanh_poly[x] * (FP8 ? 1.f : r);
       }
       // capped, without a bias, over bf16: weights are 2^s as it is
       const bool bounded = !FP8 && cap && !p.mod.slopes && p.mod.cap_log2 <= kBoundedLog2;
       float m_ref = bounded && first < last ? 0.f : -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
-      for (int c2 = 2 * first; c2 < 2 * last; ++c2) {
-        const int h = c2 & 1;
-        const uint32_t sh_col = s_col + 64 * (1 - h);  // a chunk's later half first
-        if (h == 0) {
-          ok = wait_at(sm, sm.bar(C::B_S_FULL + t), nc & 1, p.err, 76);
-          __syncwarp();
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-        }
-        float2 s[32];
-        {
-          float v[2][32];
-          ptx::tmem_ld_x32(sh_col, v[0]);
-          ptx::tmem_ld_x32(sh_col + 32, v[1]);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            s[e] = make_float2(v[e >> 4][2 * (e & 15)], v[e >> 4][2 * (e & 15) + 1]);
-        }
-        const int key0 = it.jl * CHK + 64 - c2 * 64;
+      for (int c = first; c < last; ++c) {
+        ok = wait(C::B_S_FULL + t, nc & 1, 76);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const int key0 = (it.jl - c) * CHK + 64 * half;
         // every row of a full tile sees every key between the last token's
         // window and the first token
         const bool whole = ntok == MQ && key0 + 64 <= pos0 + 1 &&
                            (p.mod.window <= 0 || key0 >= pos0 + MQ - p.mod.window);
-        float top[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
-        if (!bounded) {
+        // 32 logits at a time, from key 32 x of the half on
+        auto load = [&](float2 (&s)[16], int x) {
+          float v[32];
+          ptx::tmem_ld_x32(s_col + 32 * x, v);
+          ptx::tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) top[e & 1] = fmaxf(top[e & 1], fmaxf(s[e].x, s[e].y));
-        }
-        if (cap) {
+          for (int e = 0; e < 16; ++e) s[e] = make_float2(v[2 * e], v[2 * e + 1]);
+        };
+        auto largest = [](const float2 (&s)[16]) {
+          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            size[e & 1] = fmaxf(size[e & 1], fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
-        }
-        // The row's largest logit: of whole halves without a bias that of the
-        // raw ones, changed (the cap is monotonic); others are changed first.
-        const bool poly =
-            cap && __all_sync(0xffffffffu, ru_fits && fmaxf(size[0], size[1]) * fabsf(ru) <= 0.75f);
-        const bool late = whole && !p.mod.slopes && (bounded || rs >= 0.f) && (poly || !cap);
-        float cm = 0.f;
-        if (late && !bounded) {
-          cm = fmaxf(top[0], top[1]) * rs;
-          if (cap)
-            cm = p.mod.cap_log2 *
-                 (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(cm * p.mod.inv_cap_log2)));
-        } else if (!late) {
-          if (poly) {
+          for (int e = 0; e < 16; ++e) top[e & 1] = fmaxf(top[e & 1], fmaxf(s[e].x, s[e].y));
+          return fmaxf(top[0], top[1]);
+        };
+        auto largest_size = [](const float2 (&s)[16]) {
+          float top[2] = {0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], poly_k, both(0.f));
-          } else if (cap) {
-            const float re = rs * p.mod.inv_cap_log2, two = -2.f * p.mod.cap_log2;
+          for (int e = 0; e < 16; ++e)
+            top[e & 1] = fmaxf(top[e & 1], fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
+          return fmaxf(top[0], top[1]);
+        };
+        auto fits = [&](float size) {
+          return __all_sync(0xffffffffu, ru_fits && size * fabsf(ru) <= 0.75f) != 0;
+        };
+        auto by_poly = [&](float2 (&s)[16], float2 plus) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              s[e].x = fmaf(two, fast_reciprocal(1.f + fast_exp2(s[e].x * re)), p.mod.cap_log2);
-              s[e].y = fmaf(two, fast_reciprocal(1.f + fast_exp2(s[e].y * re)), p.mod.cap_log2);
-            }
-          } else {
+          for (int e = 0; e < 16; ++e)
+            s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], poly_k, plus);
+        };
+        auto by_exp = [&](float2 (&s)[16]) {
+          const float re = rs * p.mod.inv_cap_log2, two = -2.f * p.mod.cap_log2;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = mul2(s[e], both(rs));
+          for (int e = 0; e < 16; ++e) {
+            s[e].x = fmaf(two, fast_reciprocal(1.f + fast_exp2(s[e].x * re)), p.mod.cap_log2);
+            s[e].y = fmaf(two, fast_reciprocal(1.f + fast_exp2(s[e].y * re)), p.mod.cap_log2);
           }
-          if (p.mod.slopes) {
-            const float at = (float)(pos - key0);
-            if (__all_sync(0xffffffffu, pos - key0 >= 63)) {  // no key behind a row's own
-              const float base = -slope * at;
+        };
+        auto mask = [&](float2 (&s)[16], int x) {
+          const int kf = low - key0 - 32 * x;
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                s[e] = add2(s[e], make_float2(fmaf(slope, (float)(2 * e), base),
-                                              fmaf(slope, (float)(2 * e + 1), base)));
+          for (int e = 0; e < 16; ++e) {
+            if ((unsigned)(2 * e - kf) >= seen) s[e].x = -INFINITY;
+            if ((unsigned)(2 * e + 1 - kf) >= seen) s[e].y = -INFINITY;
+          }
+        };
+        auto weigh = [&](float2 (&s)[16], int x) {  // 2^s as weights over the logits
+          float2 sum = make_float2(0.f, 0.f);
+          float w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 q = make_float2(fast_exp2(s[e].x), fast_exp2(s[e].y));
+            const uint32_t w2 = pack2<FP8>(q.x, q.y);
+            w[e] = __uint_as_float(w2);
+            // bf16: the sum is of the weights as rounded, so that a large one's
+            // rounding (2^-9) leaves the quotient; f16's 2^-12 may stay in
+            sum = add2(sum, FP8 ? q : make_float2(bf16_lo(w2), bf16_hi(w2)));
+          }
+          ptx::tmem_st_x16(s_col + 16 * x, w);
+          l2 = add2(l2, sum);
+        };
+        if (bounded) {
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            float2 s[16];
+            load(s, x);
+            if (fits(largest_size(s))) by_poly(s, both(0.f));
+            else by_exp(s);
+            if (!whole) mask(s, x);
+            weigh(s, x);
+          }
+        } else {
+          // The row's largest logit: of whole halves without a bias that of the
+          // raw ones, changed (the cap is monotonic); others are changed first.
+          float cm = -INFINITY;
+          bool late = whole && !p.mod.slopes && rs >= 0.f;
+          if (late) {
+            float size = 0.f;
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              float2 s[16];
+              load(s, x);
+              cm = fmaxf(cm, largest(s));
+              if (cap) size = fmaxf(size, largest_size(s));
+            }
+            cm *= rs;
+            if (cap) {
+              cm = p.mod.cap_log2 *
+                   (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(cm * p.mod.inv_cap_log2)));
+              late = fits(size);
+              if (!late) cm = -INFINITY;
+            }
+          }
+          if (!late) {
+            // no key behind a row's own: the bias is a line over the keys
+            const float at = (float)(pos - key0);
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              float2 s[16];
+              load(s, x);
+              if (!cap) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[e] = mul2(s[e], both(rs));
+              } else if (fits(largest_size(s))) {
+                by_poly(s, both(0.f));
+              } else {
+                by_exp(s);
+              }
+              if (p.mod.slopes) {
+                const float d = at - 32.f * x;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  s[e].x = fmaf(-slope, fabsf(d - (float)(2 * e)), s[e].x);
+                  s[e].y = fmaf(-slope, fabsf(d - (float)(2 * e + 1)), s[e].y);
+                }
+              }
+              if (!whole) mask(s, x);
+              cm = fmaxf(cm, largest(s));
+              float v[32];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[2 * e] = s[e].x, v[2 * e + 1] = s[e].y;
+              ptx::tmem_st_x32(s_col + 32 * x, v);
+            }
+            ptx::tmem_st_wait();
+          }
+          cm = fmaxf(cm, exchange(cm));
+          if (!ok) break;
+          float alpha = 1.f;
+          if (cm > m_ref + kRescaleLog2) {
+            if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - cm);
+            m_ref = cm;
+          }
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {  // (never at an item's first keys)
+            ok = wait(C::B_O_FULL + t, (nc - 1) & 1, 77);  // the products of the chunk before
+            if (!ok) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+              float o[32];
+              ptx::tmem_ld_x32(o_col + 32 * x, o);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              ptx::tmem_st_x32(o_col + 32 * x, o);
+            }
+            l2.x *= alpha;
+            l2.y *= alpha;
+          }
+          const float2 plus = both(C::kRaise - (m_ref == -INFINITY ? 0.f : m_ref));
+          const float2 factor = both(late ? rs : 1.f);
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            float2 s[16];
+            load(s, x);
+            if (late && cap) {
+              by_poly(s, plus);
             } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                s[e].x = fmaf(-slope, fabsf(at - (float)(2 * e)), s[e].x);
-                s[e].y = fmaf(-slope, fabsf(at - (float)(2 * e + 1)), s[e].y);
-              }
+              for (int e = 0; e < 16; ++e) s[e] = fma2(s[e], factor, plus);
             }
-          }
-          if (!whole) {
-            const unsigned seen = (unsigned)max(0, lim - low);
-            const int kf = low - key0;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if ((unsigned)(2 * e - kf) >= seen) s[e].x = -INFINITY;
-              if ((unsigned)(2 * e + 1 - kf) >= seen) s[e].y = -INFINITY;
-            }
-          }
-          if (!bounded) {
-            top[0] = top[1] = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) top[e & 1] = fmaxf(top[e & 1], fmaxf(s[e].x, s[e].y));
-            cm = fmaxf(top[0], top[1]);
+            weigh(s, x);
           }
         }
-        float alpha = 1.f;
-        if (cm > m_ref + kRescaleLog2) {
-          if (m_ref != -INFINITY) alpha = fast_exp2(m_ref - cm);
-          m_ref = cm;
-        }
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {  // (never at an item's first keys)
-          // the products of the half before; those before it are done
-          ok = wait_at(sm, sm.bar(C::B_O_FULL + 2 * t + (h ^ 1)), (h ? nc : nc - 1) & 1, p.err, 77);
-          __syncwarp();
-          if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-#pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
-            float o[32];
-            ptx::tmem_ld_x32(o_col + 32 * x, o);
-            ptx::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-            ptx::tmem_st_x32(o_col + 32 * x, o);
-          }
-          ptx::tmem_st_wait();
-          l2.x *= alpha;
-          l2.y *= alpha;
-        }
-        const float2 bias = both(C::kRaise - (m_ref == -INFINITY ? 0.f : m_ref));
-        if (late && cap) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            s[e] = capped_poly(FP8 ? mul2(s[e], both(ru)) : s[e], poly_k, bias);
-        } else {
-          const float2 factor = both(late ? rs : 1.f);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] = fma2(s[e], factor, bias);
-        }
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        float w[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float2 q = make_float2(fast_exp2(s[e].x), fast_exp2(s[e].y));
-          const uint32_t w2 = pack2<FP8>(q.x, q.y);
-          w[e] = __uint_as_float(w2);
-          // bf16: the sum is of the weights as rounded, so that a large one's
-          // rounding (2^-9) leaves the quotient; f16's 2^-12 may stay in
-          sum[e & 1] = add2(sum[e & 1], FP8 ? q : make_float2(bf16_lo(w2), bf16_hi(w2)));
-        }
-        ptx::tmem_st_x32(sh_col, w);
-        l2 = add2(l2, add2(sum[0], sum[1]));
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(sm.bar(C::B_P_FULL + 2 * t + h));
-        nc += h;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_P_FULL + t));
+        ++nc;
       }
       if (!ok) break;
-      const float l = l2.x + l2.y;
+      float l = l2.x + l2.y;
+      l += exchange(l);
+      if (!ok) break;
       float* part = nullptr;
       if (it.part >= 0) {
         part = part_at(blockIdx.x, it.part);
-        __stcg(reinterpret_cast<float2*>(part + 256 * D) + tid, make_float2(m_ref, l));
+        if (half == 0)
+          __stcg(reinterpret_cast<float2*>(part + 256 * D) + 128 * t + row, make_float2(m_ref, l));
       }
       if (first < last) {  // (a tile may have no tokens, or no chunks in this part)
-        ok = wait_at(sm, sm.bar(C::B_O_FULL + 2 * t + 1), (nc - 1) & 1, p.err, 78);
-        __syncwarp();
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
+        ok = wait(C::B_O_FULL + t, (nc - 1) & 1, 78);
+        if (!ok) break;
         ptx::tc_fence_after();
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 2; ++x) {
           float o[32];
           ptx::tmem_ld_x32(o_col + 32 * x, o);
           ptx::tmem_ld_wait();
           if (it.part >= 0) {
-            float4* to = reinterpret_cast<float4*>(part) + (t * 32 + 8 * x) * 128 + row;
+            float4* to = reinterpret_cast<float4*>(part) + (t * 32 + 16 * half + 8 * x) * 128 + row;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               __stcg(to + 128 * e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
@@ -987,20 +1055,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               uint32_t w[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                w[e] = pack_bf16x2_rn(o[16 * c + 2 * e] * inv * vsc, o[16 * c + 2 * e + 1] * inv * vsc);
+                w[e] =
+                    pack_bf16x2_rn(o[16 * c + 2 * e] * inv * vsc, o[16 * c + 2 * e + 1] * inv * vsc);
               store_32(orow + 32 * x + 16 * c, w, out_aligned);  // (rows lie apart: whole sectors)
             }
           }
           __syncwarp();
         }
         ptx::tc_fence_before();
-        ptx::mbar_arrive(sm.bar(C::B_O_EMPTY + t));
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_O_EMPTY + t));
       }
       if (it.part >= 0) {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_PART));
         if (warp == 0) {  // once both tiles' sums are written
-          ok = wait_at(sm, sm.bar(C::B_PART), np & 1, p.err, 80);
+          ok = wait(C::B_PART, np & 1, 80);
           if (ok && lane == 0) {
             ptx::fence_acq_rel_gpu();
             st_release(&p.flags[2 * blockIdx.x + it.part], p.epoch);
@@ -1032,32 +1102,33 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_MERGE));
       // Both tiles' warps are done with their items: shared memory is free (a last
       // item may have products for one tile alone), and all have seen the flags.
-      const bool all = wait_at(sm, sm.bar(C::B_MERGE), 0, p.err, 81);
-      __syncwarp();
-      ok = __all_sync(0xffffffffu, ok && all);
+      const bool all = wait(C::B_MERGE, 0, 81);
+      ok = ok && all;
       if (ok && warp == 0) {  // down, for a replay of this launch
         for (int k = lane; k < count; k += 32) p.flags[2 * cta(k) + (k == 0 ? 1 : 0)] = 0;
       }
+      __syncwarp();
       if (ok && merge_row) {
-        // Sums come through shared memory, in pieces of 64 columns of a part: 16 copies a thread, of its own row, three pieces ahead.  (By
-        // plain loads, two or three parts took 15 us.)
+        // Sums come through shared memory, in pieces of 32 columns of a part:
+        // 8 copies a thread, of its own row, three pieces ahead.  (By plain loads,
+        // two or three parts took 15 us.)
         constexpr int kAhead = 3;
-        static_assert(kAhead * 256 * 256 <= C::OFF_BAR, "the pieces' room");
+        static_assert(kAhead * 512 * 128 <= C::OFF_X, "the pieces' room");
         const uint32_t own = sm.base_u32 + tid * 16;
         auto ml_of = [&](int k) {
           return __ldcg(reinterpret_cast<const float2*>(part_at(cta(k), k == 0 ? 1 : 0) + 256 * D) +
-                        tid);
+                        128 * t + row);
         };
         const int pieces = 2 * count;
-        auto fetch = [&](int i) {  // piece i: columns 64 (i / count) on, of part i % count
+        auto fetch = [&](int i) {  // piece i: columns 32 (i / count) on, of part i % count
           if (i < pieces) {
             const int x = i >= count, k = i - x * count;
             const float4* from =
                 reinterpret_cast<const float4*>(part_at(cta(k), k == 0 ? 1 : 0)) +
-                (t * 32 + 16 * x) * 128 + row;
+                (t * 32 + 16 * half + 8 * x) * 128 + row;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              cp_async_16(own + ((i % kAhead) * 16 + e) * 4096, from + 128 * e, 16);
+            for (int e = 0; e < 8; ++e)
+              cp_async_16(own + ((i % kAhead) * 8 + e) * 8192, from + 128 * e, 16);
           }
           cp_async_commit();
         };
@@ -1072,7 +1143,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (ml.x != -INFINITY || ml.y != 0.f) l += fast_exp2(ml.x - most) * ml.y;
         }
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        float4 sum[16];
+        float4 sum[8];
         float2 ml = ml_of(0);
         for (int i = 0; i < pieces; ++i) {
           const int x = i >= count, k = i - x * count;
@@ -1080,23 +1151,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           ml = ml_of(k + 1 < count ? k + 1 : 0);
           if (k == 0) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sum[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int e = 0; e < 8; ++e) sum[e] = make_float4(0.f, 0.f, 0.f, 0.f);
           }
           cp_async_wait<kAhead - 1>();
           if (now.x != -INFINITY || now.y != 0.f) {  // (else: no keys, or no sums written)
             const float f = fast_exp2(now.x - most);
             const float4* v =
-                reinterpret_cast<const float4*>(sm.base) + (i % kAhead) * 16 * 256 + tid;
+                reinterpret_cast<const float4*>(sm.base) + (i % kAhead) * 8 * 512 + tid;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float4 w = v[256 * e];
+            for (int e = 0; e < 8; ++e) {
+              const float4 w = v[512 * e];
               sum[e].x += f * w.x, sum[e].y += f * w.y, sum[e].z += f * w.z, sum[e].w += f * w.w;
             }
           }
           fetch(i + kAhead);
           if (k == count - 1) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2; ++e) {
               uint32_t w[8];
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
@@ -1104,7 +1175,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                 w[2 * y] = pack_bf16x2_rn(s.x * inv * vsc, s.y * inv * vsc);
                 w[2 * y + 1] = pack_bf16x2_rn(s.z * inv * vsc, s.w * inv * vsc);
               }
-              store_32(merge_row + 64 * x + 16 * e, w, out_aligned);
+              store_32(merge_row + 32 * x + 16 * e, w, out_aligned);
             }
           }
         }
