@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           l2 = add2(l2, sum);
         };
         if (bounded) {
-#pragma unroll 1
+#pragma unroll
           for (int x = 0; x < 2; ++x) {
             float2 s[16];
             load(s, x);
