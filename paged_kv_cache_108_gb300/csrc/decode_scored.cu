@@ -55,7 +55,10 @@ namespace pa {
 namespace {
 
 constexpr int kCtasPerSm = 2;     // what registers and shared memory are kept to
-constexpr int kWholeUnits = 6;    // units per CTA from which none is split
+// Units per CTA from which none is split: the prologue's walk over all rows is
+// saved, and a long row among so many others weighs little.  (Whole and split, us:
+// 4 units a CTA 212, 222, of shorter rows 79, 79; 6.6 148, 146; 26 198, 204.)
+constexpr int kWholeUnits = 6;
 
 template <int D, int G, KvFormat F>
 struct Cfg {
@@ -63,6 +66,8 @@ struct Cfg {
   static constexpr int kPieces = kRow / 16;
   static constexpr int kChunk = F == kBf16 ? 16 : 32;  // tokens a warp handles at a time
   static constexpr int kTile = kChunk * kRow;  // K (or V) bytes of a chunk
+  // What shared memory holds of two CTAs.  (One int8 row of 128 K tokens with 4, 5
+  // and 6 warps: 64, 69, 59 us.)
   static constexpr int kWarps = F == kBf16 ? 4 : (D == 64 ? 8 : (G > 4 ? 5 : 6));
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = F == kBf16 ? 3 : 2;

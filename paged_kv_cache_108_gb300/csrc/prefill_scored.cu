@@ -7,26 +7,31 @@
 //   s = scale q . k;  s <- cap tanh(s / cap);  s <- s - slope |i - j|
 //   out = softmax(s) V.
 //
-// Bound: with a cap the issue of the softmax's instructions (about 9 a logit,
-// 128 x 128 logits a tile and chunk), then the MMAs (4 d flop a logit).
+// Bound: each tile's chain of products and softmax; two tiles are all that
+// tensor memory holds.  A chunk of 128 keys takes a tile 5200 clocks (capped
+// bf16): 1370 of waiting for its two products (1024 on the tensor cores), 2950 of
+// softmax, the rest of an item's epilogue (650 a chunk, with 6 chunks an item).
+// The tensor cores are busy 0.4 of it, issue slots a third.
 //
 // A work item is a pair of neighbouring query tiles of one request and KV head:
 // 2 x 128 rows, row = token * G + query head in the group.  Both tiles use
 // each K and V chunk of 128 keys while it is in shared memory, and alternate on
 // the tensor cores: while one tile's softmax runs, the other's products do.
-//   S_t = Q_t K^T      M = 128 rows, N = 128 keys, K = 128, into tensor memory
-//   P_th               one thread a row, a half h of 64 logits at a time: changed,
-//                      masked, exponentiated; 16-bit weights back over them
-//   O_t += P_th V_h    A = P_th from tensor memory, B = V's rows, MN-major: of
-//                      the first half while the second's softmax runs
+//   S_t = Q_t K^T     M = 128 rows, N = 128 keys, K = 128, into tensor memory
+//   P_t               two threads a row, 64 logits each, 32 at a time: changed,
+//                     masked, exponentiated; 16-bit weights back over them
+//   O_t += P_t V      A = P_t from tensor memory, B = V's rows, MN-major
 // Tensor memory is full: S_0, S_1 (P over them), O_0, O_1 of 128 columns.
-// (Halves with logits and products of their own, N = 64, took 136 us for four
-// capped prompts of 2048.)
+// (One thread a row, 8 softmax warps in place of 16: 136 us for four capped
+// prompts of up to 2048 tokens, where this takes 121.  Halves with products of
+// their own, N = 64, under 16 warps: 131.)  The two halves of a row agree on its
+// largest logit, and add up its sum, through shared memory.
 // Capped logits without a bias need no running max over a bf16 cache: they lie
 // within the cap, and for a cap up to 55 weights from 2^-80 to 2^80 leave bf16
 // and the fp32 sums room for values and counts (2^127 = 2^80 2^17 keys 2^30 of a
-// value).  Elsewhere O is rescaled only when a row's running max grows by more than 2^8; all lanes
-// of the row's warp take part (by 1), as tensor memory accesses are a warp's.
+// value).  Elsewhere O is rescaled only when a row's running max grows by more
+// than 2^8; all lanes of the row's warps take part (by 1), as tensor memory
+// accesses are a warp's.
 //
 // The cap.  tanh(u) for |u| <= 3/4 is an odd polynomial of degree 7 (fitted to
 // the smallest largest error over that range: 3.6e-6, which a cap of 50 makes
@@ -36,16 +41,18 @@
 //
 // An e4m3 cache: two warps widen each chunk to f16 (exact) in shared memory;
 // q, scaled by a power of two a row that puts its largest |q| in [1, 2), is
-// rounded to f16 in place by the row's thread (11 bits for bf16's 8: exact down
+// rounded to f16 in place by the row's threads (11 bits for bf16's 8: exact down
 // to 2^-14 of the row's largest); weights are f16, raised by 2^7.
 //
 // Values of keys that no token of the item sees (behind the last, before a
 // window, in part not loaded) are zeroed in shared memory, so that nothing
 // they hold reaches a sum; their logits are masked by a select.
 //
-// Roles (384 threads): warps 0-3 and 4-7 softmax and epilogue of tile 0 and 1;
-// warp 8 loads (q, K, V) and hands out items; warp 9 issues the MMAs; warps
-// 10-11 widen or zero.  Every wait is bounded: error word 0, the CTA gives up.
+// Roles (640 threads): warps 0-7 and 8-15 softmax and epilogue of tile 0 and 1,
+// four warps a half of the columns; warp 16 loads (q, K, V) and hands out items;
+// warp 17 issues the MMAs; warps 18-19 widen or zero.  (Two more warps would leave
+// 80 registers a thread, and spills.)  Every wait is bounded: error word 0, the
+// CTA gives up.
 //
 // Work split: the chunks of all items of a head in a row, K in all, are cut
 // into equal ranges, each taken by H_kv neighbouring CTAs, one a head (ragged
@@ -85,8 +92,13 @@ constexpr int RAW_B = CHK * D;          // a K or V chunk in e4m3
 constexpr int NTHREADS = 640;
 constexpr int PROD_WARP = 16, MMA_WARP = 17, FIX_WARP = 18;
 constexpr int NITEM = 4;                // items published ahead
-constexpr int kItemCost = 1;            // of an item, in chunks
-constexpr int kMinUnits = 2;            // units of a CTA at least, where there are few
+// Of an item, in chunks, when CTAs' shares are made equal.  (Four capped prompts
+// with 1, 2 and 3: 136, 139, 142 us; a step of 300 new tokens each 40, 40, 38.)
+constexpr int kItemCost = 1;
+// Units of a CTA at least, where there are few: parts cost their joining.  (64
+// tokens at the end of 1000 with 1, 2 and 4: 24.4, 23.6, 26.7 us; 20 of 300 16.6,
+// 17.7, 15.4.)
+constexpr int kMinUnits = 2;
 constexpr int NFIX = 4;                 // zeroed V chunks ahead of their MMA, at most
 constexpr int S_COL = 0, O_COL = 256;   // tile t: + 128 t; logits of the h-th half: + 64 h
 constexpr float kRescaleLog2 = 8.f;
@@ -188,6 +200,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
   float2 d;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+  return d;
+}
+// The largest of three (a NaN is passed over).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
@@ -295,6 +313,15 @@ __device__ __forceinline__ float2 capped_poly(float2 s, const float (&k)[4], flo
   f = fma2(f, z, both(k[1]));
   f = fma2(f, z, both(k[0]));
   return fma2(f, s, bias);
+}
+// Without a bias, adding s^4 to `fourth`.
+__device__ __forceinline__ float2 capped_poly_sum(float2 s, const float (&k)[4], float2& fourth) {
+  const float2 z = mul2(s, s);
+  fourth = fma2(z, z, fourth);
+  float2 f = fma2(both(k[3]), z, both(k[2]));
+  f = fma2(f, z, both(k[1]));
+  f = fma2(f, z, both(k[0]));
+  return mul2(f, s);
 }
 
 template <int G, bool FP8>
@@ -867,14 +894,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         auto largest = [](const float2 (&s)[16]) {
           float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 16; ++e) top[e & 1] = fmaxf(top[e & 1], fmaxf(s[e].x, s[e].y));
+          for (int e = 0; e < 16; ++e) top[e & 1] = max3(top[e & 1], s[e].x, s[e].y);
           return fmaxf(top[0], top[1]);
         };
         auto largest_size = [](const float2 (&s)[16]) {
           float top[2] = {0.f, 0.f};
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            top[e & 1] = fmaxf(top[e & 1], fmaxf(fabsf(s[e].x), fabsf(s[e].y)));
+            top[e & 1] = max3(top[e & 1], fabsf(s[e].x), fabsf(s[e].y));
           return fmaxf(top[0], top[1]);
         };
         auto fits = [&](float size) {
@@ -921,8 +948,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int x = 0; x < 2; ++x) {
             float2 s[16];
             load(s, x);
-            if (fits(largest_size(s))) by_poly(s, both(0.f));
-            else by_exp(s);
+            // Whether the polynomial holds, after the fact: no |u| is above 3/4 where
+            // the u^4 sum to less than (3/4)^4.  (The largest |u|, before: 122 us for
+            // four capped prompts, where this takes 118.)
+            float2 fourth = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = capped_poly_sum(s[e], poly_k, fourth);
+            if (!__all_sync(0xffffffffu, ru_fits && (fourth.x + fourth.y) * (ru2 * ru2) <=
+                                                        0.31640625f)) {
+              load(s, x);
+              by_exp(s);
+            }
             if (!whole) mask(s, x);
             weigh(s, x);
           }
