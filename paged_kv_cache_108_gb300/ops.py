@@ -396,7 +396,11 @@ def decode_selected(out, q, k_cache, v_cache, block_tables, context_lens, select
 def alloc_cache_units(k_cache):
     """(k_scale, v_scale) of an int8 cache [num_blocks, block_size, H_kv, d]:
     zeroed fp32 [num_blocks, block_size, H_kv] on its device, the units that
-    ``norm_rope_and_cache`` writes."""
+    ``norm_rope_and_cache`` writes.
+
+    ``copy_blocks`` and ``swap_blocks`` take the codes as ``.view(torch.uint8)``
+    and, for block_size * H_kv a multiple of 32, the units as
+    ``.view(torch.bfloat16).view(num_blocks, 1, -1, 64)``."""
     if k_cache.dim() != 4 or k_cache.dtype != torch.int8:
         raise ValueError("cache must be int8 [num_blocks, block_size, num_kv_heads, head_dim]")
     return tuple(torch.zeros(k_cache.shape[:3], dtype=torch.float32, device=k_cache.device)

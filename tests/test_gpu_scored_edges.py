@@ -262,3 +262,24 @@ def test_infinite_and_nan_queries_stay_in_their_rows():
         assert np.isfinite(got[same]).all()
         # (a warp whose rows hold a NaN or an infinity caps by the other formula)
         assert np.abs(got - clean)[same].max() <= 2 ** -6 * np.abs(clean).max()
+
+
+def test_blocks_of_8_bit_rows_are_copied_as_bytes():
+    """A fork's copied blocks: codes and units through copy_blocks."""
+    c = _attn_case(86, "int8", [130, 40], 8, 2, 64, 16)
+    kc, vc, ks, vs = (torch.cat([t, torch.zeros_like(t)]) for t in (c["kc"], c["vc"], c["ks"], c["vs"]))
+    NB = c["kc"].shape[0]
+    pairs = _dev(np.stack([np.arange(NB), NB + np.random.default_rng(1).permutation(NB)], 1))
+    ops.copy_blocks(kc.view(torch.uint8), vc.view(torch.uint8), pairs)
+    units = [t.view(torch.bfloat16).view(2 * NB, 1, -1, 64) for t in (ks, vs)]
+    ops.copy_blocks(*units, pairs)
+    to = pairs[:, 1].cpu().numpy()
+    q = _bf16(c["rng"], 2, 8, 64)
+    outs = []
+    for tables in (c["tables"], np.where(c["tables"] < 0, -1, to[c["tables"]])):
+        out = torch.empty_like(q)
+        ops.decode_scored(out, q, kc, vc, _dev(tables), _dev(c["lens"]), c["scale"], cap=30.0,
+                          k_scale=ks, v_scale=vs)
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1])
+    _check_rows(c, outs[0], q, [(0, 0, 129), (1, 1, 39)], 30.0, 0, False)
