@@ -243,7 +243,7 @@ struct __align__(16) Item {
   int prefix;
   int jl, n;     // the last chunk's keys, count (0: zero rows); chunk c has keys jl - c
   int a[2], b[2];  // chunks of each tile: [a, b)
-  int part;      // slot of its sums, -1: the item is whole
+  int part;      // slot of its sums in the workspace, or -1
   int merge;     // the first of the CTAs that share the item, where this one adds up; or -1
 };
 static_assert(sizeof(Item) == kItemBytes, "");
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm.base + C::OFF_TMEM);
   // This CTA's head and range of chunks: [lo, hi) of K, from chunk off0 of a pair.
   __shared__ long long s_sum[NTHREADS / 32], s_others[NTHREADS / 32], s_before;
-  __shared__ int s_pair;
+  __shared__ int s_pair, s_last;  // the pairs of its first and last unit
   const int j = blockIdx.x / p.num_kv_heads, g = blockIdx.x - j * p.num_kv_heads;
   const int pairs = tp[R];
   // A pair's chunks, and kItemCost more for what an item takes besides (the
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       if (lane == 31) s_sum[warp] = incl;
       if (base == 0 && lane == 0) s_others[warp] = others;
-      if (tid == 0) s_pair = -1;
+      if (tid == 0 && base == 0) s_pair = s_last = -1;
       __syncthreads();
       long long start = before + incl - n, end = before;
       for (int w = 0; w < NTHREADS / 32; ++w) {
@@ -448,12 +448,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           hi = tc::range_lo(j + 1, K, ranges);
         }
       }
-      if (j < ranges && start <= lo && lo < start + n) {
-        s_pair = base + tid;
+      if (j < ranges && start <= lo && lo < start + n) s_pair = base + tid;
+      if (j < ranges && start < hi && hi <= start + n) {
+        s_last = base + tid;
         s_before = start;
       }
       __syncthreads();
-      if (j >= ranges || s_pair >= 0) break;
+      if (j >= ranges || s_last >= 0) break;
       before = end;
     }
   }
@@ -476,32 +477,34 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       Stage<NLOAD> st;  // K and V chunks in turn
       long long ns = 0;  // those filled
       int nq = 0;        // q pairs
-      int pair = hi > lo ? s_pair : 0, off = hi > lo ? (int)(lo - s_before) : 0;
-      long long left = hi - lo;
+      // from the last pair to the first: what a later CTA waits for is done first,
+      // what is joined here last
+      const int lowest = hi > lo ? s_pair : 0;
+      int pair = hi > lo ? s_last : -1;
+      long long u0 = hi > lo ? s_before : 0;  // the pair's first unit
       for (int k = 0;; ++k) {
         const int slot = k % NITEM;
         if (!wait_at(sm, sm.bar(C::B_ITEM_EMPTY + slot), ((uint32_t)(k / NITEM) & 1) ^ 1, p.err, 61))
           break;
         Item it;
         it.r = -1;
-        while (left > 0) {
+        for (bool found = false; pair >= lowest && !found; --pair) {
           it = item_of<G>(pair, g, tp, p);
-          const int all = it.n + kItemCost, upto = (int)min((long long)all, off + left);
-          const long long u0 = hi - left - off;  // the pair's first unit
+          const int all = it.n + kItemCost;
+          if (pair < s_last) u0 -= all;
+          const int off = (int)max(lo - u0, 0ll), upto = (int)min((long long)all, hi - u0);
           const int from = max(off - kItemCost, 0), to = upto - kItemCost;
-          left -= upto - off;
-          off = 0;
-          ++pair;
-          if (it.n == 0 && upto == all) break;  // zeros
-          if (to > from) {
-            if (from > 0 || to < it.n) {
+          found = it.n == 0 || to > from;
+          if (it.n == 0) continue;  // zeros
+          if (!found) {
+            it.r = -1;  // (none of the pair's chunks)
+          } else if (from > 0 || to < it.n) {
+            if (from > 0 && to == it.n)
+              it.merge = tc::cta_of(u0 + kItemCost, K, ranges);
+            else
               it.part = from > 0 ? 0 : 1;
-              if (to == it.n) it.merge = tc::cta_of(u0 + kItemCost, K, ranges);
-              restrict_to(it, from, to);
-            }
-            break;
+            restrict_to(it, from, to);
           }
-          it.r = -1;  // (none of the pair's chunks)
         }
         if (lane == 0) {
           items[slot] = it;
@@ -775,8 +778,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const float vsc = FP8 ? __ldg(p.v_scale) : 1.f;
     const bool out_aligned = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
     int nc = 0, nq = 0, nx = 0;  // chunks of this tile, items with chunks, exchanges
-    int merge = -1, np = 0;  // parts written
-    __nv_bfloat16* merge_row = nullptr;
+    int np = 0;  // parts written
+    int merge = -1;  // the item to join: its first CTA, this CTA's max and sum, if any
+    float m_own = -INFINITY, l_own = 0.f;
+    bool some = false;
+    __nv_bfloat16* own_row = nullptr;
     auto part_at = [&](int cta, int slot) -> float* {
       return p.parts + (2 * (int64_t)cta + slot) * kPartWords;
     };
@@ -796,6 +802,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       ok = wait(C::B_X + t, nx & 1, 82);
       ++nx;
       return at[128 * (half ^ 1)];
+    };
+    auto store_row = [&](__nv_bfloat16* to, const float (&o)[32], float inv) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          w[e] = pack_bf16x2_rn(o[16 * c + 2 * e] * inv * vsc, o[16 * c + 2 * e + 1] * inv * vsc);
+        store_32(to + 16 * c, w, out_aligned);  // (rows lie apart: whole sectors)
+      }
     };
     for (int k = 0; ok; ++k) {
       const Item it = read_item(k);
@@ -1064,16 +1080,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       float l = l2.x + l2.y;
       l += exchange(l);
       if (!ok) break;
+      if (first < last) {  // (a tile may have no tokens, or no chunks in this part)
+        ok = wait(C::B_O_FULL + t, (nc - 1) & 1, 78);
+        if (!ok) break;
+        ptx::tc_fence_after();
+      }
+      if (it.merge >= 0) {  // the CTA's last item
+        merge = it.merge;
+        m_own = m_ref;
+        l_own = l;
+        some = first < last;
+        own_row = row_ok ? orow : nullptr;
+        break;
+      }
       float* part = nullptr;
       if (it.part >= 0) {
         part = part_at(blockIdx.x, it.part);
         if (half == 0)
           __stcg(reinterpret_cast<float2*>(part + 256 * D) + 128 * t + row, make_float2(m_ref, l));
       }
-      if (first < last) {  // (a tile may have no tokens, or no chunks in this part)
-        ok = wait(C::B_O_FULL + t, (nc - 1) & 1, 78);
-        if (!ok) break;
-        ptx::tc_fence_after();
+      if (first < last) {
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {
@@ -1086,15 +1112,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int e = 0; e < 8; ++e)
               __stcg(to + 128 * e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
           } else if (row_ok) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                w[e] =
-                    pack_bf16x2_rn(o[16 * c + 2 * e] * inv * vsc, o[16 * c + 2 * e + 1] * inv * vsc);
-              store_32(orow + 32 * x + 16 * c, w, out_aligned);  // (rows lie apart: whole sectors)
-            }
+            store_row(orow + 32 * x, o, inv);
           }
           __syncwarp();
         }
@@ -1113,17 +1131,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
         ++np;
-        if (it.merge >= 0) {  // (once: the CTA's first item)
-          merge = it.merge;
-          merge_row = row_ok ? orow : nullptr;
-        }
       }
     }
-    // ---- the item whose end this CTA holds: its parts, in the CTAs' order ----
+    // The item whose end this CTA holds: its own sums (in tensor memory, if it
+    // has some) and the parts of the CTAs before it, in their order.
     if (ok && merge >= 0) {
-      const int count = j - merge + 1;
-      // the first CTA's part starts the item, the others' go on with it
+      const int count = j - merge;
       auto cta = [&](int k) { return (merge + k) * p.num_kv_heads + g; };
+      // the first CTA's part starts the item, the others' go on with it
       for (int k = lane; k < count; k += 32) {  // (each warp for itself)
         const long long begun = clock64();
         while (ld_acquire(&p.flags[2 * cta(k) + (k == 0 ? 1 : 0)]) != p.epoch) {
@@ -1136,17 +1151,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       ok = __all_sync(0xffffffffu, ok);
       if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_MERGE));
-      // Both tiles' warps are done with their items: shared memory is free (a last
-      // item may have products for one tile alone), and all have seen the flags.
+      // Both tiles' warps are done with their products: shared memory is free (an
+      // item may have some for one tile alone), and all have seen the flags.
       const bool all = wait(C::B_MERGE, 0, 81);
       ok = ok && all;
       if (ok && warp == 0) {  // down, for a replay of this launch
         for (int k = lane; k < count; k += 32) p.flags[2 * cta(k) + (k == 0 ? 1 : 0)] = 0;
       }
       __syncwarp();
-      if (ok && merge_row) {
-        // Sums come through shared memory, in pieces of 32 columns of a part:
-        // 8 copies a thread, of its own row, three pieces ahead.  (By plain loads,
+      if (ok) {
+        // Sums come through shared memory, in pieces of 32 columns of a part: 8
+        // copies a thread, of its own row, three pieces ahead.  (By plain loads,
         // two or three parts took 15 us.)
         constexpr int kAhead = 3;
         static_assert(kAhead * 512 * 128 <= C::OFF_X, "the pieces' room");
@@ -1159,9 +1174,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         auto fetch = [&](int i) {  // piece i: columns 32 (i / count) on, of part i % count
           if (i < pieces) {
             const int x = i >= count, k = i - x * count;
-            const float4* from =
-                reinterpret_cast<const float4*>(part_at(cta(k), k == 0 ? 1 : 0)) +
-                (t * 32 + 16 * half + 8 * x) * 128 + row;
+            const float4* from = reinterpret_cast<const float4*>(part_at(cta(k), k == 0 ? 1 : 0)) +
+                                 (t * 32 + 16 * half + 8 * x) * 128 + row;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               cp_async_16(own + ((i % kAhead) * 8 + e) * 8192, from + 128 * e, 16);
@@ -1170,50 +1184,50 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         };
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) fetch(i);
-        float most = -INFINITY, l = 0.f;
+        float most = m_own;
 #pragma unroll 4
         for (int k = 0; k < count; ++k) most = fmaxf(most, ml_of(k).x);
+        // (a part without keys has no sums written)
+        const bool mine = some && (m_own != -INFINITY || l_own != 0.f);
+        const float f_own = mine ? fast_exp2(m_own - most) : 0.f;
+        float l = mine ? f_own * l_own : 0.f;
 #pragma unroll 4
         for (int k = 0; k < count; ++k) {
           const float2 ml = ml_of(k);
           if (ml.x != -INFINITY || ml.y != 0.f) l += fast_exp2(ml.x - most) * ml.y;
         }
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        float4 sum[8];
         float2 ml = ml_of(0);
-        for (int i = 0; i < pieces; ++i) {
-          const int x = i >= count, k = i - x * count;
-          const float2 now = ml;
-          ml = ml_of(k + 1 < count ? k + 1 : 0);
-          if (k == 0) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          float o[32];
+          if (some) {
+            ptx::tmem_ld_x32(o_col + 32 * x, o);
+            ptx::tmem_ld_wait();
           }
-          cp_async_wait<kAhead - 1>();
-          if (now.x != -INFINITY || now.y != 0.f) {  // (else: no keys, or no sums written)
-            const float f = fast_exp2(now.x - most);
-            const float4* v =
-                reinterpret_cast<const float4*>(sm.base) + (i % kAhead) * 8 * 512 + tid;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 w = v[512 * e];
-              sum[e].x += f * w.x, sum[e].y += f * w.y, sum[e].z += f * w.z, sum[e].w += f * w.w;
-            }
-          }
-          fetch(i + kAhead);
-          if (k == count - 1) {
+          for (int e = 0; e < 32; ++e) o[e] = mine ? o[e] * f_own : 0.f;
+#pragma unroll 1
+          for (int k = 0; k < count; ++k) {
+            const int i = x * count + k;
+            const float2 now = ml;
+            ml = ml_of(k + 1 < count ? k + 1 : 0);
+            cp_async_wait<kAhead - 1>();
+            if (now.x != -INFINITY || now.y != 0.f) {
+              const float f = fast_exp2(now.x - most);
+              const float4* v =
+                  reinterpret_cast<const float4*>(sm.base) + (i % kAhead) * 8 * 512 + tid;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint32_t w[8];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const float4 s = sum[4 * e + y];
-                w[2 * y] = pack_bf16x2_rn(s.x * inv * vsc, s.y * inv * vsc);
-                w[2 * y + 1] = pack_bf16x2_rn(s.z * inv * vsc, s.w * inv * vsc);
+              for (int e = 0; e < 8; ++e) {
+                const float4 w = v[512 * e];
+                o[4 * e] += f * w.x, o[4 * e + 1] += f * w.y;
+                o[4 * e + 2] += f * w.z, o[4 * e + 3] += f * w.w;
               }
-              store_32(merge_row + 32 * x + 16 * e, w, out_aligned);
             }
+            fetch(i + kAhead);
           }
+          if (own_row) store_row(own_row + 32 * x, o, inv);
+          __syncwarp();
         }
         cp_async_wait<0>();
       }

@@ -450,7 +450,8 @@ def alloc_scored_workspace(num_rows, num_heads, num_kv_heads, head_dim, device=N
 
 
 def _scored_workspace(workspace, q, k_cache, stream):
-    if workspace is not None or not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3:
+    if (workspace is not None or not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3
+            or not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4):
         return workspace  # (what is wrong is refused by the binding)
     if stream is None:
         side = torch.cuda.current_stream(q.device)
