@@ -1106,12 +1106,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           float o[32];
           ptx::tmem_ld_x32(o_col + 32 * x, o);
           ptx::tmem_ld_wait();
-          if (it.part >= 0) {
+          if (it.part >= 0 && row_ok) {
             float4* to = reinterpret_cast<float4*>(part) + (t * 32 + 16 * half + 8 * x) * 128 + row;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               __stcg(to + 128 * e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
-          } else if (row_ok) {
+          } else if (it.part < 0 && row_ok) {
             store_row(orow + 32 * x, o, inv);
           }
           __syncwarp();
@@ -1172,7 +1172,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         };
         const int pieces = 2 * count;
         auto fetch = [&](int i) {  // piece i: columns 32 (i / count) on, of part i % count
-          if (i < pieces) {
+          if (i < pieces && own_row) {
             const int x = i >= count, k = i - x * count;
             const float4* from = reinterpret_cast<const float4*>(part_at(cta(k), k == 0 ? 1 : 0)) +
                                  (t * 32 + 16 * half + 8 * x) * 128 + row;
@@ -1213,7 +1213,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             const float2 now = ml;
             ml = ml_of(k + 1 < count ? k + 1 : 0);
             cp_async_wait<kAhead - 1>();
-            if (now.x != -INFINITY || now.y != 0.f) {
+            if (own_row && (now.x != -INFINITY || now.y != 0.f)) {
               const float f = fast_exp2(now.x - most);
               const float4* v =
                   reinterpret_cast<const float4*>(sm.base) + (i % kAhead) * 8 * 512 + tid;
