@@ -26,8 +26,8 @@ constexpr int kTileMinTokens = 16;
 // all, each is a row of its own; with more the tensor-core tiles serve them.
 // Rows read their keys once each, the tiles once for all but after some 15 us of
 // set-up and joining (bf16, us by rows and by tiles: 16 requests of 2000 tokens,
-// 3 new each: 51, 48; 8 each: 98, 49; one of 4000, 4 new: 17, 31; 16 new: 40, 31.
-// e4m3: 3 new each 35, 55; 8 each 62, 55; one request's 16 new 27, 33).
+// 2 new each: 35, 39; 3 each: 47, 39; one of 4000, 8 new: 24, 28; 12 new: 32, 28.
+// e4m3: 4 new each 36, 48; 6 each 49, 48; one request's 16 new 26, 31).
 struct RowsRule {
   int per_request, in_all;
 };
@@ -145,7 +145,8 @@ pa_status check_any_cache(pa_cache_desc c, const float* ks, const float* vs, con
   if (st != PA_OK) return st;
   if (rows && (!ks || !vs || !aligned(ks, 4) || !aligned(vs, 4)))
     return pa_fail(PA_ERR_INVALID,
-                   (std::string(fn) + ": an int8 cache needs k_scale and v_scale, 4-byte aligned").c_str());
+                   (std::string(fn) + ": an int8 cache needs k_scale and v_scale, 4-byte aligned")
+                       .c_str());
   return rows ? PA_OK : check_scales(c, ks, vs, fn);
 }
 
@@ -246,8 +247,10 @@ pa_status rope_params(const char* fn, void* q_out, const void* query, int64_t q_
   const int32_t pairs = rope.rot_dim / 2;
   if (rotates && (rope.max_position <= 0 || rope.num_axes < 1))
     return fail(PA_ERR_INVALID, "max_position and num_axes must be positive");
-  if (rotates && (rope.rot_dim <= 0 || rope.rot_dim % 16 || rope.rot_dim > cache.head_dim || rope.num_axes > 4))
-    return fail(PA_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16 up to head_dim, num_axes at most 4");
+  if (rotates && (rope.rot_dim <= 0 || rope.rot_dim % 16 || rope.rot_dim > cache.head_dim ||
+                  rope.num_axes > 4))
+    return fail(PA_ERR_UNSUPPORTED,
+                "rot_dim must be a multiple of 16 up to head_dim, num_axes at most 4");
   if (rope.num_axes > 1) {
     int64_t sum = 0;
     for (int a = 0; a < rope.num_axes; ++a) {

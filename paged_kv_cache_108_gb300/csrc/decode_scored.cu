@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
     Row mine = {-1, 0, 0, 0};
     int n = 0;  // steps of this thread's row
     long long others = 0;
-    for (int r = tid + kThreads; r < p.num_rows; r += kThreads) others += steps_of<kStep>(row_of(p, r));
+    for (int r = tid + kThreads; r < p.num_rows; r += kThreads)
+      others += steps_of<kStep>(row_of(p, r));
     long long before = 0;
     for (int base = 0; base < p.num_rows; base += kThreads) {
       n = 0;

@@ -23,7 +23,7 @@
 //   O_t += P_t V      A = P_t from tensor memory, B = V's rows, MN-major
 // Tensor memory is full: S_0, S_1 (P over them), O_0, O_1 of 128 columns.
 // (One thread a row, 8 softmax warps in place of 16: 136 us for four capped
-// prompts of up to 2048 tokens, where this takes 121.  Halves with products of
+// prompts of up to 2048 tokens, where that took 121.  Halves with products of
 // their own, N = 64, under 16 warps: 131.)  The two halves of a row agree on its
 // largest logit, and add up its sum, through shared memory.
 // Capped logits without a bias need no running max over a bf16 cache: they lie
@@ -93,11 +93,11 @@ constexpr int NTHREADS = 640;
 constexpr int PROD_WARP = 16, MMA_WARP = 17, FIX_WARP = 18;
 constexpr int NITEM = 4;                // items published ahead
 // Of an item, in chunks, when CTAs' shares are made equal.  (Four capped prompts
-// with 1, 2 and 3: 136, 139, 142 us; a step of 300 new tokens each 40, 40, 38.)
+// with 1 and 2: 116.5, 115.5 us; 512 new tokens behind 8 K 75.8, 78.4.)
 constexpr int kItemCost = 1;
 // Units of a CTA at least, where there are few: parts cost their joining.  (64
-// tokens at the end of 1000 with 1, 2 and 4: 24.4, 23.6, 26.7 us; 20 of 300 16.6,
-// 17.7, 15.4.)
+// tokens at the end of 1000 with 1, 2, 3 and 4: 25.4, 22.6, 23.2, 22.6 us; 20 of
+// 300 16.2, 15.2, 13.8, 13.8.)
 constexpr int kMinUnits = 2;
 constexpr int NFIX = 4;                 // zeroed V chunks ahead of their MMA, at most
 constexpr int S_COL = 0, O_COL = 256;   // tile t: + 128 t; logits of the h-th half: + 64 h
