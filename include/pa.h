@@ -733,7 +733,7 @@ typedef struct {
 /* Workspace bytes that serve both pa_decode_scored (num_rows: sequences) and
  * pa_varlen_scored (num_rows: new tokens) on the current device; 0 for bad
  * sizes.  (Partial sums of the work that the SMs share: up to 5 MB, or with
- * head_dim 128 and more than 8 rows 40 to 81 MB, whatever the lengths.)  A
+ * head_dim 128 and more than 8 rows up to 81 MB, whatever the lengths.)  A
  * workspace serves calls of any sizes that need no more, on one stream; calls
  * that share one must not overlap on the GPU.  It needs no initialisation.
  * The calls set its word 0 (int32) to a nonzero code if a bounded wait inside

@@ -192,8 +192,7 @@ pa_status check_score(const pa_score_desc& s, float scale, int32_t max_blocks, i
   return PA_OK;
 }
 
-// The scored calls' workspace: the tiles' error word and work counter, then
-// what split units need.
+// The scored calls' workspace: the error word, then what split units need.
 constexpr size_t kScoredHead = 256;
 
 // What the calls over query rows share: row r belongs to sequence

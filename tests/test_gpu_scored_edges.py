@@ -283,3 +283,20 @@ def test_blocks_of_8_bit_rows_are_copied_as_bytes():
         outs.append(out)
     assert torch.equal(outs[0], outs[1])
     _check_rows(c, outs[0], q, [(0, 0, 129), (1, 1, 39)], 30.0, 0, False)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("H,Hkv,new,n,window,prefix", [
+    (2, 2, 256, 1000, 150, 0), (2, 2, 250, 900, 40, 0), (3, 3, 256, 2000, 129, 1700),
+    (1, 1, 129, 1500, 300, 0), (4, 4, 200, 1400, 500, 1390), (8, 2, 64, 1300, 20, 0),
+])
+def test_parts_in_which_a_tile_has_no_keys(kv, H, Hkv, new, n, window, prefix):
+    """Few items over windows, each shared by CTAs: some parts hold keys of one
+    of the two tiles alone, the joining CTA's own among them."""
+    c = _attn_case(87, kv, [n], H, Hkv, 128, 16)
+    q, starts = _step(c, [new])
+    pre = [prefix] if prefix else None
+    outs = [_varlen(c, q, starts, cap=cap, window=window, prefix=pre) for cap in (0.0, 25.0, 25.0)]
+    assert torch.equal(outs[1], outs[2])
+    _check_rows(c, outs[0], q, _rows(c, starts, 19), 0.0, window, False, pre, True)
+    _check_rows(c, outs[1], q, _rows(c, starts, 19), 25.0, window, False, pre, True)
