@@ -936,12 +936,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             s[e].y = fmaf(two, fast_reciprocal(1.f + fast_exp2(s[e].y * re)), p.mod.cap_log2);
           }
         };
-        auto mask = [&](float2 (&s)[16], int x) {
+        // Logits of keys that the row does not see become `other`.
+        auto mask = [&](float2 (&s)[16], int x, float other) {
           const int kf = low - key0 - 32 * x;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            if ((unsigned)(2 * e - kf) >= seen) s[e].x = -INFINITY;
-            if ((unsigned)(2 * e + 1 - kf) >= seen) s[e].y = -INFINITY;
+            if ((unsigned)(2 * e - kf) >= seen) s[e].x = other;
+            if ((unsigned)(2 * e + 1 - kf) >= seen) s[e].y = other;
           }
         };
         auto weigh = [&](float2 (&s)[16], int x) {  // 2^s as weights over the logits
@@ -964,6 +965,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int x = 0; x < 2; ++x) {
             float2 s[16];
             load(s, x);
+            // (what is not seen, stale shared memory even, chooses no formula)
+            if (!whole) mask(s, x, 0.f);
             // Whether the polynomial holds, after the fact: no |u| is above 3/4 where
             // the u^4 sum to less than (3/4)^4.  (The largest |u|, before: 122 us for
             // four capped prompts, where this takes 118.)
@@ -975,7 +978,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               load(s, x);
               by_exp(s);
             }
-            if (!whole) mask(s, x);
+            if (!whole) mask(s, x, -INFINITY);
             weigh(s, x);
           }
         } else {
@@ -1007,6 +1010,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int x = 0; x < 2; ++x) {
               float2 s[16];
               load(s, x);
+              if (cap && !whole) mask(s, x, 0.f);
               if (!cap) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[e] = mul2(s[e], both(rs));
@@ -1023,7 +1027,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                   s[e].y = fmaf(-slope, fabsf(d - (float)(2 * e + 1)), s[e].y);
                 }
               }
-              if (!whole) mask(s, x);
+              if (!whole) mask(s, x, -INFINITY);
               cm = fmaxf(cm, largest(s));
               float v[32];
 #pragma unroll

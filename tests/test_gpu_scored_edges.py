@@ -300,3 +300,62 @@ def test_parts_in_which_a_tile_has_no_keys(kv, H, Hkv, new, n, window, prefix):
     assert torch.equal(outs[1], outs[2])
     _check_rows(c, outs[0], q, _rows(c, starts, 19), 0.0, window, False, pre, True)
     _check_rows(c, outs[1], q, _rows(c, starts, 19), 25.0, window, False, pre, True)
+
+
+def test_calls_on_two_streams_at_once():
+    """Prompts and single tokens on two streams, a workspace each: split work of
+    both at the same time."""
+    cs = [_attn_case(88, "bf16", [3000, 700], 8, 2, 128, 16),
+          _attn_case(89, "fp8", [2500, 1800, 60], 8, 2, 128, 16)]
+    jobs = []
+    for c, new in zip(cs, ([200, 70], [90, 33, 60])):
+        q, starts = _step(c, new)
+        last = q[[int(s) - 1 for s in starts[1:]]].contiguous()
+        jobs.append(dict(q=q, last=last, starts=_dev(starts), tables=_dev(c["tables"]),
+                         lens=_dev(c["lens"]), mod=_mod(c, 30.0, 0, False), side=torch.cuda.Stream(),
+                         ws=ops.alloc_scored_workspace(q.shape[0], 8, 2, 128),
+                         want=_varlen(c, q, starts, cap=30.0), outs=[], c=c, host=starts))
+    torch.cuda.synchronize()
+    for _ in range(12):
+        for j in jobs:
+            with torch.cuda.stream(j["side"]):
+                out, one = torch.empty_like(j["q"]), torch.empty_like(j["last"])
+            args = (j["c"]["kc"], j["c"]["vc"], j["tables"], j["lens"])
+            ops.varlen_scored(out, j["q"], *args, j["starts"], j["c"]["scale"], workspace=j["ws"],
+                              stream=j["side"], **j["mod"])
+            ops.decode_scored(one, j["last"], *args, j["c"]["scale"], workspace=j["ws"],
+                              stream=j["side"], **j["mod"])
+            j["outs"].append((out, one))
+    torch.cuda.synchronize()
+    for j in jobs:
+        for out, one in j["outs"]:
+            assert torch.equal(out, j["want"]) and torch.equal(one, j["outs"][0][1])
+        _check_rows(j["c"], j["outs"][0][1], j["last"],
+                    [(i, i, n - 1) for i, n in enumerate(j["c"]["lens"])], 30.0, 0, False)
+        _check_rows(j["c"], j["want"], j["q"], _rows(j["c"], j["host"], 23), 30.0, 0, False, None, True)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("cap,bias", [(30.0, False), (60.0, False), (30.0, True)])
+def test_unseen_keys_leave_no_trace(kv, cap, bias):
+    """Bit for bit: whatever lies behind the contexts and before the windows,
+    and whatever ran before (other calls' keys in the SMs' memory)."""
+    new, lens = [200, 70], [3003, 717]
+    c = _attn_case(90, kv, lens, 8, 2, 128, 16)
+    q, starts = _step(c, new)
+    loud = _attn_case(91, kv, [900, 900], 8, 2, 128, 16)
+    lq, lstarts = _step(loud, [300, 300])
+    lq *= 50.0
+    outs = []
+    for turn in range(6):
+        if turn % 2:
+            _varlen(loud, lq, lstarts)
+        for i, n in enumerate(lens):  # behind the last token
+            for cache in (c["kc"], c["vc"]):
+                tail = cache[int(c["tables"][i, n // 16]), n % 16:]
+                tail.copy_((torch.randn(tail.shape, device=DEV) * 10.0 ** turn).to(tail.dtype)
+                           if kv == "bf16" else torch.randint_like(tail, 0, 127))
+        outs.append(_varlen(c, q, starts, cap=cap, bias=bias, window=1000))
+    for out in outs[1:]:
+        assert torch.equal(out, outs[0])
+    _check_rows(c, outs[0], q, _rows(c, starts, 17), cap, 1000, bias, None, True)
