@@ -44,9 +44,10 @@
 // rounded to f16 in place by the row's threads (11 bits for bf16's 8: exact down
 // to 2^-14 of the row's largest); weights are f16, raised by 2^7.
 //
-// Values of keys that no token of the item sees (behind the last, before a
-// window, in part not loaded) are zeroed in shared memory, so that nothing
-// they hold reaches a sum; their logits are masked by a select.
+// Keys that no token of the item sees (behind the last, before a window, in part
+// not loaded) and their values are zeroed in shared memory, so that nothing they
+// hold reaches a sum or chooses a formula for the cap; logits are masked by a
+// select.
 //
 // Roles (640 threads): warps 0-7 and 8-15 softmax and epilogue of tile 0 and 1,
 // four warps a half of the columns; warp 16 loads (q, K, V) and hands out items;
@@ -99,7 +100,7 @@ constexpr int kItemCost = 1;
 // tokens at the end of 1000 with 1, 2, 3 and 4: 25.4, 22.6, 23.2, 22.6 us; 20 of
 // 300 16.2, 15.2, 13.8, 13.8.)
 constexpr int kMinUnits = 2;
-constexpr int NFIX = 4;                 // zeroed V chunks ahead of their MMA, at most
+constexpr int NFIX = 4;                 // zeroed chunks ahead of their MMA, at most
 constexpr int S_COL = 0, O_COL = 256;   // tile t: + 128 t; logits of the h-th half: + 64 h
 constexpr float kRescaleLog2 = 8.f;
 constexpr float kBoundedLog2 = 80.f;    // caps up to this need no running max
@@ -630,7 +631,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
             st.next();
           }
-          if (keys) ok = ok && wait(b_staged + st.s, st.ph, 65);
+          if (keys) {
+            ok = ok && wait(b_staged + st.s, st.ph, 65);
+            if (!FP8 && ragged(it, c)) {
+              ok = ok && wait(C::B_FIX + nfix % NFIX, (uint32_t)(nfix / NFIX) & 1, 69);
+              ++nfix;
+            }
+          }
           if (!ok) break;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -745,7 +752,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             ok = wait_at(sm, sm.bar(C::B_FULL + s), st.ph, p.err, 74);
             __syncwarp();
             if (!ok) break;
-            if (!(x2 & 1) || !ragged(it, c)) {
+            if (!ragged(it, c)) {
               if (lane == 0) ptx::mbar_arrive(sm.bar(C::B_EMPTY + s));
               continue;
             }
@@ -921,7 +928,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           return fmaxf(top[0], top[1]);
         };
         auto fits = [&](float size) {
-          return __all_sync(0xffffffffu, ru_fits && size * fabsf(ru) <= 0.75f) != 0;
+          return __all_sync(0xffffffffu, !row_ok || (ru_fits && size * fabsf(ru) <= 0.75f)) != 0;
         };
         auto by_poly = [&](float2 (&s)[16], float2 plus) {
 #pragma unroll
@@ -936,13 +943,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             s[e].y = fmaf(two, fast_reciprocal(1.f + fast_exp2(s[e].y * re)), p.mod.cap_log2);
           }
         };
-        // Logits of keys that the row does not see become `other`.
-        auto mask = [&](float2 (&s)[16], int x, float other) {
+        auto mask = [&](float2 (&s)[16], int x) {
           const int kf = low - key0 - 32 * x;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            if ((unsigned)(2 * e - kf) >= seen) s[e].x = other;
-            if ((unsigned)(2 * e + 1 - kf) >= seen) s[e].y = other;
+            if ((unsigned)(2 * e - kf) >= seen) s[e].x = -INFINITY;
+            if ((unsigned)(2 * e + 1 - kf) >= seen) s[e].y = -INFINITY;
           }
         };
         auto weigh = [&](float2 (&s)[16], int x) {  // 2^s as weights over the logits
@@ -965,20 +971,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int x = 0; x < 2; ++x) {
             float2 s[16];
             load(s, x);
-            // (what is not seen, stale shared memory even, chooses no formula)
-            if (!whole) mask(s, x, 0.f);
             // Whether the polynomial holds, after the fact: no |u| is above 3/4 where
             // the u^4 sum to less than (3/4)^4.  (The largest |u|, before: 122 us for
             // four capped prompts, where this takes 118.)
             float2 fourth = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 16; ++e) s[e] = capped_poly_sum(s[e], poly_k, fourth);
-            if (!__all_sync(0xffffffffu, ru_fits && (fourth.x + fourth.y) * (ru2 * ru2) <=
-                                                        0.31640625f)) {
+            if (!__all_sync(0xffffffffu,
+                            !row_ok || (ru_fits && (fourth.x + fourth.y) * (ru2 * ru2) <=
+                                                       0.31640625f))) {
               load(s, x);
               by_exp(s);
             }
-            if (!whole) mask(s, x, -INFINITY);
+            if (!whole) mask(s, x);
             weigh(s, x);
           }
         } else {
@@ -1010,7 +1015,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             for (int x = 0; x < 2; ++x) {
               float2 s[16];
               load(s, x);
-              if (cap && !whole) mask(s, x, 0.f);
               if (!cap) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[e] = mul2(s[e], both(rs));
@@ -1027,7 +1031,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                   s[e].y = fmaf(-slope, fabsf(d - (float)(2 * e + 1)), s[e].y);
                 }
               }
-              if (!whole) mask(s, x, -INFINITY);
+              if (!whole) mask(s, x);
               cm = fmaxf(cm, largest(s));
               float v[32];
 #pragma unroll
