@@ -719,7 +719,9 @@ pa_status pa_gather_cache(void* k_out, void* v_out, const void* k_cache, const v
 
 /* What happens to a score s = scale q . k of the query at position i and the
  * key at position j, in this order:
- *  cap     > 0: s <- cap tanh(s / cap) (from 1e-6 to 1e6).  0: none.
+ *  cap     > 0: s <- cap tanh(s / cap) (from 1e-6 to 1e6), to within 2^-20 of
+ *          the score, or on the tiles (below) under a cap up to 64 to within
+ *          4e-6 of the cap.  0: none.
  *  slopes  device, [num_heads] fp32: s <- s - slopes[h] |i - j|.  NULL: none.
  *  window  > 0: only keys with i - j < window are seen.  0: all.
  * Blocks that lie wholly before the window of every query are not read, nor

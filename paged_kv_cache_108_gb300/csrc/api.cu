@@ -154,6 +154,13 @@ pa::KvFormat format_of(const pa_cache_desc& c) {
   return c.dtype == PA_KV_BF16 ? pa::kBf16 : c.dtype == PA_KV_INT8 ? pa::kInt8 : pa::kE4m3;
 }
 
+// The tiles' polynomial for the cap is off by up to 3.6e-6 of the cap: 2.3e-4 of
+// a weight at this one, an eighth of what its rounding to bf16 takes.  Scores
+// under larger caps are capped one by one, to within 2^-20 of themselves.  (Four
+// prompts of up to 2048 tokens, us, bf16 and e4m3: by the polynomial 146, 163, one
+// by one 170, 198.)
+constexpr float kLargeCap = 64.f;
+
 // What changes the scores, checked, in the kernels' units.
 pa_status check_score(const pa_score_desc& s, float scale, int32_t max_blocks, int32_t block_size,
                       const char* fn, pa::ScoreMod* mod) {
@@ -185,6 +192,7 @@ pa_status check_score(const pa_score_desc& s, float scale, int32_t max_blocks, i
   constexpr float kTanh[4] = {0.9999556f, -0.33222765f, 0.12577091f, -0.033778276f};
   if (s.cap > 0.f) {
     mod->inv_cap = 1.f / mod->cap_log2;
+    mod->large_cap = s.cap > kLargeCap;
     for (int k = 0; k < 4; ++k) mod->tanh_poly[k] = mod->cap_log2 * kTanh[k];
   }
   mod->slopes = s.slopes;

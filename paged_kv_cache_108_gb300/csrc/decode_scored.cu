@@ -23,8 +23,8 @@
 // P V, relative to the largest unit the warp has met (a running maximum like
 // the softmax's), so that f16 holds those products whatever the units' size.
 //
-// The cap's tanh(u) is 1 - 2 / (1 + e^2u): one exponential and one reciprocal,
-// off by about 2^-22 of the cap.
+// The cap leaves small scores as they are, to within 2^-22 of themselves, and
+// large ones to within 2^-20 (capped()).
 //
 // Work split: a unit is a (row, KV head); its visible tokens are cut into
 // steps of one chunk per warp, and the steps of all rows, K in all, into equal
@@ -516,11 +516,26 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
     load_keys(it + C::kStages, slot);  // in the place of the keys just used
     if (ch.seen) {
       if (p.mod.cap_log2 > 0.f) {
-        const float e0 = f0 * p.mod.inv_cap_log2, e1 = f1 * p.mod.inv_cap_log2;
+        bool small = true;
 #pragma unroll
         for (int i = 0; i < 2 * kGroups; ++i) {
-          x[i][0] = p.mod.cap_log2 * (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(x[i][0] * e0)));
-          x[i][1] = p.mod.cap_log2 * (1.f - 2.f * fast_reciprocal(1.f + fast_exp2(x[i][1] * e1)));
+          x[i][0] *= f0;
+          x[i][1] *= f1;
+          small &= fabsf(x[i][0] * p.mod.inv_cap) <= kTanhSmall &&
+                   fabsf(x[i][1] * p.mod.inv_cap) <= kTanhSmall;
+        }
+        if (__all_sync(0xffffffffu, small)) {  // (either way the same scores)
+#pragma unroll
+          for (int i = 0; i < 2 * kGroups; ++i) {
+            x[i][0] = capped_small(x[i][0], x[i][0] * p.mod.inv_cap);
+            x[i][1] = capped_small(x[i][1], x[i][1] * p.mod.inv_cap);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2 * kGroups; ++i) {
+            x[i][0] = capped(x[i][0], x[i][0] * p.mod.inv_cap, p.mod.cap_log2);
+            x[i][1] = capped(x[i][1], x[i][1] * p.mod.inv_cap, p.mod.cap_log2);
+          }
         }
       } else {
 #pragma unroll

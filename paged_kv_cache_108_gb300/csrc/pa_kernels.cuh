@@ -79,6 +79,7 @@ struct ScoreMod {
   const float* slopes;          // [H] or null
   const int32_t* prefix_lens;   // [S] or null
   int32_t window;               // > 0: keys of the last `window` positions only
+  bool large_cap;               // errors of a fixed share of the cap would show
 };
 
 // Causal varlen attention for prefill chunks on the tensor cores

@@ -37,7 +37,8 @@
 // the smallest largest error over that range: 3.6e-6, which a cap of 50 makes
 // 1.8e-4 of a weight, a tenth of its 16-bit rounding), five FMAs a logit; a half
 // chunk with a larger |u| in one of the warp's rows takes 1 - 2 / (1 + e^2u), one
-// exponential and one reciprocal.
+// exponential and one reciprocal.  Both are off by a fixed share of the cap: above
+// a cap of 64 each score is capped by itself, to within 2^-20 of the score.
 //
 // An e4m3 cache: two warps widen each chunk to f16 (exact) in shared memory;
 // q, scaled by a power of two a row that puts its largest |q| in [1, 2), is
@@ -325,7 +326,9 @@ __device__ __forceinline__ float2 capped_poly_sum(float2 s, const float (&k)[4],
   return mul2(f, s);
 }
 
-template <int G, bool FP8>
+// LARGE: a cap above 64.  (A kernel of its own: with the branch in one, ragged
+// e4m3 chunks under a cap of 30 took 78.3 us, where this takes 75.3.)
+template <int G, bool FP8, bool LARGE>
 __global__ void __launch_bounds__(NTHREADS, 1)
     prefill_scored_kernel(const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v,
@@ -880,7 +883,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const float slope =
           p.mod.slopes ? __ldg(&p.mod.slopes[it.g * G + hd]) * 1.4426950408889634f : 0.f;
       const int pos0 = it.pos + t * MQ;  // of the tile's first token
-      const bool cap = p.mod.cap_log2 > 0.f;
+      const bool cap = LARGE || p.mod.cap_log2 > 0.f;
       const float ru = rs * p.mod.inv_cap;  // to u = score / cap
       // The polynomial's coefficients, with the powers of ru in them; where the
       // highest leaves the normal floats, the cap is taken the other way.  (Rows
@@ -894,7 +897,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int x = 0; x < 4; ++x, r *= ru2) poly_k[x] = p.mod.tanh_poly[x] * (FP8 ? 1.f : r);
       }
       // capped, without a bias, over bf16: weights are 2^s as it is
-      const bool bounded = !FP8 && cap && !p.mod.slopes && p.mod.cap_log2 <= kBoundedLog2;
+      const bool bounded = !FP8 && !LARGE && cap && !p.mod.slopes && p.mod.cap_log2 <= kBoundedLog2;
       float m_ref = bounded && first < last ? 0.f : -INFINITY;
       float2 l2 = make_float2(0.f, 0.f);
       for (int c = first; c < last; ++c) {
@@ -941,6 +944,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int e = 0; e < 16; ++e) {
             s[e].x = fmaf(two, fast_reciprocal(1.f + fast_exp2(s[e].x * re)), p.mod.cap_log2);
             s[e].y = fmaf(two, fast_reciprocal(1.f + fast_exp2(s[e].y * re)), p.mod.cap_log2);
+          }
+        };
+        auto by_either = [&](float2 (&s)[16]) {
+          const float to_u = p.mod.inv_cap;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[e] = mul2(s[e], both(rs));
+          if (__all_sync(0xffffffffu, largest_size(s) * to_u <= kTanhSmall)) {  // (the same scores)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              s[e].x = capped_small(s[e].x, s[e].x * to_u);
+              s[e].y = capped_small(s[e].y, s[e].y * to_u);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              s[e].x = capped(s[e].x, s[e].x * to_u, p.mod.cap_log2);
+              s[e].y = capped(s[e].y, s[e].y * to_u, p.mod.cap_log2);
+            }
           }
         };
         auto mask = [&](float2 (&s)[16], int x) {
@@ -990,7 +1011,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           // The row's largest logit: of whole halves without a bias that of the
           // raw ones, changed (the cap is monotonic); others are changed first.
           float cm = -INFINITY;
-          bool late = whole && !p.mod.slopes && rs >= 0.f;
+          bool late = whole && !p.mod.slopes && rs >= 0.f && !LARGE;
           if (late) {
             float size = 0.f;
 #pragma unroll 1
@@ -1018,6 +1039,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               if (!cap) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) s[e] = mul2(s[e], both(rs));
+              } else if (LARGE) {
+                by_either(s);
               } else if (fits(largest_size(s))) {
                 by_poly(s, both(0.f));
               } else {
@@ -1262,14 +1285,21 @@ int ranges_of(int heads, int num_sms) {
 }
 size_t flag_bytes(int64_t ctas) { return (size_t)(ctas * 16 + 255) / 256 * 256; }
 
+template <int G, bool FP8, bool LARGE>
+cudaError_t launch_one(const Params& prm, const CUtensorMap& mk, const CUtensorMap& mv,
+                     const CUtensorMap& mq, cudaStream_t stream) {
+  const cudaError_t e = allow_large<prefill_scored_kernel<G, FP8, LARGE>>();
+  if (e != cudaSuccess) return e;
+  return launch_dependent<prefill_scored_kernel<G, FP8, LARGE>>(
+      dim3(prm.ranges * prm.num_kv_heads), dim3(NTHREADS), Cfg<FP8>::SMEM_BYTES, stream, 1, mk, mv, mq,
+      prm);
+}
+
 template <int G, bool FP8>
 cudaError_t launch_g(const Params& prm, const CUtensorMap& mk, const CUtensorMap& mv,
                      const CUtensorMap& mq, cudaStream_t stream) {
-  const cudaError_t e = allow_large<prefill_scored_kernel<G, FP8>>();
-  if (e != cudaSuccess) return e;
-  return launch_dependent<prefill_scored_kernel<G, FP8>>(
-      dim3(prm.ranges * prm.num_kv_heads), dim3(NTHREADS), Cfg<FP8>::SMEM_BYTES, stream, 1, mk, mv, mq,
-      prm);
+  return prm.mod.large_cap ? launch_one<G, FP8, true>(prm, mk, mv, mq, stream)
+                           : launch_one<G, FP8, false>(prm, mk, mv, mq, stream);
 }
 
 template <bool FP8>
