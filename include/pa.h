@@ -665,10 +665,12 @@ pa_status pa_decode_selected(void* out, const void* q, const void* k_cache, cons
  * then name the units, [num_blocks, block_size, num_kv_heads] fp32 at the
  * cache's slots, 4-byte aligned.  A row of zeros (or whose u underflows to 0)
  * has u = 0, c = 0; one that holds an infinity or a NaN reads back as NaNs.
- * The units of an attended token must not be negative.  pa_copy_blocks and
- * pa_swap_blocks move such a cache as bytes: the codes as an e4m3 cache of the
- * same sizes, the units (where block_size * num_kv_heads is a multiple of 32)
- * as a bf16 one of block_size 1, block_size * num_kv_heads / 32 heads, head_dim 64.
+ * The units of an attended token must not be negative; attention holds a
+ * weight times its value row's unit to 2^-11 of itself or 2^-37 of its head's
+ * largest.  pa_copy_blocks and pa_swap_blocks move such a cache as bytes: the
+ * codes as an e4m3 cache of the same sizes, the units (where block_size *
+ * num_kv_heads is a multiple of 32) as a bf16 one of block_size 1,
+ * block_size * num_kv_heads / 32 heads, head_dim 64.
  * ---------------------------------------------------------------------- */
 
 /* pa_norm_rope_and_cache -- pa_rope_and_cache into any cache, with each query

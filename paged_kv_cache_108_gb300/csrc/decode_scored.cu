@@ -19,9 +19,14 @@
 // MMA does.  8-bit elements are widened to f16 in registers (exact); q then
 // enters in f16 under a power of two per head, and P is raised by 2^14 (f16
 // ends at 2^-24) and rounded once: up to 2^-11 of a weight, an eighth of
-// the output's own rounding.  The unit of an 8-bit row multiplies its logit, and its weight in
-// P V, relative to the largest unit the warp has met (a running maximum like
-// the softmax's), so that f16 holds those products whatever the units' size.
+// the output's own rounding.  The unit of an 8-bit row multiplies its logit, and
+// its weight in P V, relative to the largest product of a weight and a unit that
+// the warp has met in the head, about (a running maximum like the softmax's, beside
+// its own): f16 then holds each product to half a step or to 2^-37 of that largest
+// one, whatever the units' size.  (Relative to the largest unit alone, one for all
+// heads, a token with all the weight was lost beside values 2^40 larger that hardly
+// counted; one int8 row of 128 K tokens took 57.9 us, where this takes 58.2, 64
+// windowed rows 38.4 and 38.9.)
 //
 // The cap leaves small scores as they are, to within 2^-22 of themselves, and
 // large ones to within 2^-20 (capped()).
@@ -115,13 +120,10 @@ __device__ __forceinline__ uint32_t widen_alternate(uint32_t w, bool odd) {
 __device__ __forceinline__ float weight(float m, float whole) {
   return whole == -INFINITY ? 1.f : fast_exp2(m - whole);
 }
-// What sums over 8-bit rows are relative to at least: the smallest normal
-// float, whose reciprocal is finite.
-constexpr float kLeastUnit = 1.17549435e-38f;
-// Units are >= 0, so they order like their bits, NaN above all.
-__device__ __forceinline__ float larger_unit(float a, float b) {
-  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
-}
+// Products of weights and units that enter P V are raised by 2^12 over their
+// reference, which leaves room for products 8 times as large before it must grow;
+// it is at least 2^-112, so that what they are multiplied by is finite.
+constexpr float kRaiseUnits = 4096.f, kRoomUnits = 8.f, kLeastProduct = 1.92592994e-34f;
 
 // A row's sequence, its position and the keys it sees, [first, end).
 struct Row {
@@ -169,7 +171,7 @@ __device__ __forceinline__ int steps_of(const Row& r) {
 }
 
 // (whole 16-byte pieces)
-constexpr int part_words(int group, int head_dim) { return (group * (head_dim + 2) + 4) / 4 * 4; }
+constexpr int part_words(int group, int head_dim) { return (group * (head_dim + 3) + 3) / 4 * 4; }
 
 // What a warp knows of a chunk that it has asked for.
 struct __align__(16) Chunk {
@@ -189,14 +191,14 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
   constexpr int kStep = kWarps * kChunk;  // tokens of a step
   constexpr int kSteps = D / 16;          // k16 steps of q . k; m16 tiles of O^T
   constexpr int kColHeads = G <= 4 ? 4 : 8;
-  constexpr int kPart = part_words(G, D);  // a partial: sums, then max and sum per head, unit
+  constexpr int kPart = part_words(G, D);  // a partial: sums, then max, sum, reference per head
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kInfos = 4;  // steps asked for at a time, at most: kStages + 1
   static_assert(C::kStages < kInfos, "");
   __shared__ Chunk s_chunk[kWarps][kInfos];
   __shared__ __align__(16) float s_o[kWarps][kColHeads][D];
   __shared__ float s_ml[kWarps][kColHeads][2];
-  __shared__ float s_unit[kWarps];
+  __shared__ float s_ref[kWarps][kColHeads];
   __shared__ long long s_sum[kWarps], s_others[kWarps], s_before;
   __shared__ Row s_cur;
   __shared__ float s_factor[kWarps][G], s_max[G], s_l[G], s_post[G];
@@ -417,16 +419,19 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
 
   float o[kSteps][4];
   float m0, m1, l0, l1;
-  float unit_max, unit_inverse;  // int8: the largest unit of a value row so far
+  // int8: the largest weight times unit so far, about, under the weights' own
+  // reference m; and what such products are multiplied by
+  float r0, r1, by0, by1;
   auto open = [&]() {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.f;
-    unit_max = kLeastUnit;
-    unit_inverse = 1.f / kLeastUnit;
+    r0 = r1 = kLeastProduct;
+    by0 = by1 = kRaiseUnits / kLeastProduct;
   };
 
+  constexpr float kPost = F == kInt8 ? 1.f / kRaiseUnits : 1.f;
   // Two outputs.  The division first: x and y are sums over all tokens, and
   // the factor may bring them past the largest float where the result is in
   // range.
@@ -575,26 +580,12 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
     cp_async_wait<kBehind>();
     __syncwarp();
     if (ch.seen) {
-      float grown = unit_max;
-      float vu[2 * kGroups];
-#pragma unroll
-      for (int i = 0; i < 2 * kGroups; ++i) vu[i] = F == kInt8 ? units[kChunk + g + 8 * i] : 1.f;
+      float vu[4] = {1.f, 1.f, 1.f, 1.f};
       if constexpr (F == kInt8) {
-        // (every lane's own token's)
-        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(units[kChunk + lane]));
-        grown = larger_unit(unit_max, __uint_as_float(most));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vu[i] = units[kChunk + g + 8 * i];
       }
-      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1) || (F == kInt8 && grown != unit_max)) {
-        float a0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0);
-        float a1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
-        l0 *= a0;
-        l1 *= a1;
-        if constexpr (F == kInt8) {
-          unit_inverse = 1.f / grown;
-          a0 *= unit_max * unit_inverse;
-          a1 *= unit_max * unit_inverse;
-          unit_max = grown;
-        }
+      auto scale_sums = [&](float a0, float a1) {
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
           o[i][0] *= a0;
@@ -602,10 +593,31 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
           o[i][2] *= a0;
           o[i][3] *= a1;
         }
+      };
+      if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+        const float a0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - n0);
+        const float a1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - n1);
+        l0 *= a0;
+        l1 *= a1;
+        if constexpr (F == kInt8) {
+          // the products' reference falls with the weights: their sums stay as they
+          // are, unless it would fall below the least
+          const float t0 = r0 * a0, t1 = r1 * a1;
+          r0 = fmaxf(t0, kLeastProduct);
+          r1 = fmaxf(t1, kLeastProduct);
+          by0 = kRaiseUnits * fast_reciprocal(r0);
+          by1 = kRaiseUnits * fast_reciprocal(r1);
+          if (__any_sync(0xffffffffu, t0 < kLeastProduct || t1 < kLeastProduct))
+            scale_sums(t0 < kLeastProduct ? t0 / kLeastProduct : 1.f,
+                       t1 < kLeastProduct ? t1 / kLeastProduct : 1.f);
+        } else {
+          scale_sums(a0, a1);
+        }
         m0 = n0;
         m1 = n1;
       }
-      constexpr float kRaise = F16 ? 14.f : 0.f;  // log2 of the factor that P and its sum carry
+      // log2 of the factor that P and its sum carry (int8: the products alone)
+      constexpr float kRaise = F == kE4m3 ? 14.f : 0.f;
       const float z0 = (m0 == -INFINITY ? 0.f : m0) - kRaise;
       const float z1 = (m1 == -INFINITY ? 0.f : m1) - kRaise;
 #pragma unroll
@@ -616,11 +628,42 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
         l1 += x[i][1];
       }
       if constexpr (F == kInt8) {
+        // (a NaN is passed over here, and stays in x)
+        const float most = fmaxf(fmaxf(vu[0], vu[1]), fmaxf(vu[2], vu[3]));
+        if (!__any_sync(0xffffffffu, most > kRoomUnits * fminf(r0, r1))) {  // weights are at most 1
 #pragma unroll
-        for (int i = 0; i < 2 * kGroups; ++i) {
-          const float u = vu[i] * unit_inverse;
-          x[i][0] *= u;
-          x[i][1] *= u;
+          for (int i = 0; i < 2 * kGroups; ++i) {
+            x[i][0] *= vu[i] * by0;
+            x[i][1] *= vu[i] * by1;
+          }
+        } else {
+          float top0 = 0.f, top1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 2 * kGroups; ++i) {
+            x[i][0] *= vu[i];
+            x[i][1] *= vu[i];
+            top0 = fmaxf(top0, x[i][0]);
+            top1 = fmaxf(top1, x[i][1]);
+          }
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) {
+            top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, d));
+            top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, d));
+          }
+          if (__any_sync(0xffffffffu, top0 > r0 || top1 > r1)) {
+            const float t0 = fmaxf(top0, r0), t1 = fmaxf(top1, r1);
+            const float i0 = fast_reciprocal(t0), i1 = fast_reciprocal(t1);
+            scale_sums(t0 > r0 ? r0 * i0 : 1.f, t1 > r1 ? r1 * i1 : 1.f);
+            r0 = t0;
+            r1 = t1;
+            by0 = kRaiseUnits * i0;
+            by1 = kRaiseUnits * i1;
+          }
+#pragma unroll
+          for (int i = 0; i < 2 * kGroups; ++i) {
+            x[i][0] *= by0;
+            x[i][1] *= by1;
+          }
         }
       }
 #pragma unroll
@@ -707,9 +750,12 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
         s_ml[warp][2 * c][1] = l0;
         s_ml[warp][2 * c + 1][0] = m1;
         s_ml[warp][2 * c + 1][1] = l1;
+        if constexpr (F == kInt8) {
+          s_ref[warp][2 * c] = r0;
+          s_ref[warp][2 * c + 1] = r1;
+        }
       }
     }
-    if (lane == 0) s_unit[warp] = unit_max;
     __syncthreads();
     const int64_t unit = (int64_t)ch.row * hkv + kvh;
     const bool starts = ch.rel >= 0, ends = ch.rel + ch.steps <= total;
@@ -717,20 +763,21 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
     // the factors of the warps' sums, and each head's max and sum over them
     if (tid < kWarps * G) {
       const int w = tid / G, h = tid % G;
-      float mm = -INFINITY, uu = kLeastUnit, l = 0.f;
+      float mm = -INFINITY, rr = kLeastProduct, l = 0.f;
 #pragma unroll
-      for (int x = 0; x < kWarps; ++x) {
-        mm = fmaxf(mm, s_ml[x][h][0]);
-        if constexpr (F == kInt8) uu = larger_unit(uu, s_unit[x]);
+      for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, s_ml[x][h][0]);
+      if constexpr (F == kInt8) {
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) rr = fmaxf(rr, weight(s_ml[x][h][0], mm) * s_ref[x][h]);
       }
       const float a = weight(s_ml[w][h][0], mm);
-      s_factor[w][h] = F == kInt8 ? a * (s_unit[w] / uu) : a;
+      s_factor[w][h] = F == kInt8 ? a * s_ref[w][h] / rr : a;
       if (w == 0) {
 #pragma unroll
         for (int x = 0; x < kWarps; ++x) l += weight(s_ml[x][h][0], mm) * s_ml[x][h][1];
         s_max[h] = mm;
         s_l[h] = l;
-        s_post[h] = F == kInt8 ? uu : post;
+        s_post[h] = F == kInt8 ? rr : post;
       }
     }
     __syncthreads();
@@ -752,13 +799,13 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
       if (split)
         *reinterpret_cast<float2*>(mine + i) = make_float2(x, y);
       else if (!(ch.flags & kNobody))
-        store(unit * G * D + i, x, y, s_l[h], s_post[h]);
+        store(unit * G * D + i, x, y, s_l[h], s_post[h] * kPost);
     }
     if (!split) continue;
     if (tid < G) {
-      mine[G * D + 2 * tid] = s_max[tid];
-      mine[G * D + 2 * tid + 1] = s_l[tid];
-      if (tid == 0) mine[G * (D + 2)] = s_post[0];
+      mine[G * D + 3 * tid] = s_max[tid];
+      mine[G * D + 3 * tid + 1] = s_l[tid];
+      mine[G * D + 3 * tid + 2] = s_post[tid];
     }
 
     __syncthreads();  // the part is written
@@ -795,18 +842,18 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
   constexpr int kBatch = C::kRing / (kPart * 4);
   constexpr int kItems = (G * D / 4 + kThreads - 1) / kThreads;
   float4 sum[kItems];
-  float top[kItems], l[kItems], uu[kItems];
+  float top[kItems], l[kItems], rr[kItems];
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {  // this CTA's own sums
     sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
     top[j] = -INFINITY;
     l[j] = 0.f;
-    uu[j] = kLeastUnit;
+    rr[j] = kLeastProduct;
     const int i = 4 * (tid + j * kThreads), h = i / D, d = i % D;
     if (i >= G * D) break;
     top[j] = s_max[h];
     l[j] = s_l[h];
-    if constexpr (F == kInt8) uu[j] = s_post[h];
+    if constexpr (F == kInt8) rr[j] = s_post[h];
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float a = s_factor[w][h];
@@ -830,35 +877,38 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
     for (int j = 0; j < kItems; ++j) {
       const int i = 4 * (tid + j * kThreads), h = i / D;
       if (i >= G * D) break;
-      const float* ml = held + G * D + 2 * h;
-      float most = top[j], unit = uu[j];
-      for (int k = 0; k < n; ++k) {
-        most = fmaxf(most, ml[k * kPart]);
-        if constexpr (F == kInt8) unit = larger_unit(unit, held[k * kPart + G * (D + 2)]);
-      }
-      const float inverse = F == kInt8 ? 1.f / unit : 1.f;
+      const float* ml = held + G * D + 3 * h;
+      float most = top[j], ref = kLeastProduct;
+      for (int k = 0; k < n; ++k) most = fmaxf(most, ml[k * kPart]);
       float a = weight(top[j], most);
       l[j] *= a;
-      if constexpr (F == kInt8) a *= uu[j] * inverse;
+      if constexpr (F == kInt8) {
+        for (int k = 0; k < n; ++k)
+          ref = fmaxf(ref, weight(ml[k * kPart], most) * ml[k * kPart + 2]);
+        a *= rr[j];
+        ref = fmaxf(ref, a);
+        a /= ref;
+      }
+      const float inverse = 1.f / ref;
       sum[j].x *= a, sum[j].y *= a, sum[j].z *= a, sum[j].w *= a;
 #pragma unroll 4
       for (int k = 0; k < n; ++k) {
         const float* q = held + k * kPart;
         a = weight(ml[k * kPart], most);
         l[j] += a * ml[k * kPart + 1];
-        if constexpr (F == kInt8) a *= q[G * (D + 2)] * inverse;
+        if constexpr (F == kInt8) a = a * ml[k * kPart + 2] * inverse;
         const float4 v = *reinterpret_cast<const float4*>(q + i);
         sum[j].x += a * v.x, sum[j].y += a * v.y, sum[j].z += a * v.z, sum[j].w += a * v.w;
       }
       top[j] = most;
-      uu[j] = unit;
+      rr[j] = ref;
     }
   }
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
     const int i = 4 * (tid + j * kThreads);
     if (i >= G * D) break;
-    const float factor = F == kInt8 ? uu[j] : post;
+    const float factor = F == kInt8 ? rr[j] * kPost : post;
     store(merge_unit * G * D + i, sum[j].x, sum[j].y, l[j], factor);
     store(merge_unit * G * D + i + 2, sum[j].z, sum[j].w, l[j], factor);
   }
