@@ -738,8 +738,11 @@ typedef struct {
  * pa_varlen_scored (num_rows: new tokens) on the current device; 0 for bad
  * sizes.  (Partial sums of the work that the SMs share: up to 5 MB, or with
  * head_dim 128 and more than 8 rows up to 81 MB, whatever the lengths.)  A
- * workspace serves calls of any sizes that need no more, on one stream; calls
+ * workspace serves calls of as many rows and of fewer, on one stream; calls
  * that share one must not overlap on the GPU.  It needs no initialisation.
+ * With head_dim 64, some hundreds of rows and more ask for no room for partial sums:
+ * where the same workspace is to serve a few long rows too, allocate the larger
+ * of the sizes for one row and for the most rows, or such a row is one CTA's.
  * The calls set its word 0 (int32) to a nonzero code if a bounded wait inside
  * a kernel expired, or (tiles) a block id was out of range; they never clear
  * it.  After such a code it must be zeroed before the call's graph is replayed. */
@@ -748,8 +751,8 @@ size_t pa_scored_workspace_size(int32_t num_rows, int32_t num_heads, int32_t num
 
 /* pa_decode_scored -- pa_decode with changed scores, over any cache.  A
  * sequence's query is at position context_lens[i] - 1.  Any finite scale.
- *  workspace     >= pa_scored_workspace_size(num_seqs, ...) bytes, 256-byte
- *                aligned.
+ *  workspace     256-byte aligned, of pa_scored_workspace_size(num_seqs, ...)
+ *                bytes; with fewer, at least 256, no row is split.
  *  Limits: num_heads / num_kv_heads in {1, 2, 4, 8}; max_blocks_per_seq *
  *  block_size up to 2^30; num_kv_heads up to 32768; num_seqs * num_kv_heads
  *  up to 2^27; else PA_ERR_UNSUPPORTED.  A block outside the pool is passed over.
@@ -769,8 +772,8 @@ pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const 
  *
  *  prefix_lens   device, [num_seqs] int32, or NULL; what is over seq_lens[r]
  *                is cut.
- *  workspace     >= pa_scored_workspace_size(num_tokens, ...) bytes, 256-byte
- *                aligned.
+ *  workspace     256-byte aligned, of pa_scored_workspace_size(num_tokens, ...)
+ *                bytes; row by row with fewer, at least 256, no row is split.
  *  Steps of many new tokens run on tensor-core tiles (more than 2 per request
  *  on average and 8 in all over bf16, 4 and 16 over e4m3), with head_dim 128,
  *  block_size >= 8, at most 256 requests and 65535 new tokens; a request that

@@ -359,16 +359,16 @@ pa_status scored_rows(const char* fn, void* out, const void* q, const void* k_ca
   const int group = num_heads / cache.num_kv_heads;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RowsRule rows = cache.dtype == PA_KV_BF16 ? kRowsBf16 : kRowsE4m3;
-  const bool tiles =
+  const bool fit =
       starts && cache.dtype != PA_KV_INT8 && num_rows > rows.in_all &&
       num_rows > rows.per_request * (int64_t)num_seqs && num_rows <= 65535 &&
-      pa::prefill_supported(cache.head_dim, group, cache.dtype == PA_KV_FP8_E4M3, num_seqs,
-                            cache.block_size);
+      pa::prefill_sizes_fit(cache.head_dim, group, num_seqs, cache.block_size);
+  const bool tiles = fit && pa::prefill_supported(cache.head_dim, group,
+                                                  cache.dtype == PA_KV_FP8_E4M3, num_seqs,
+                                                  cache.block_size);
+  // (rows are split where there is room)
   const size_t need =
-      kScoredHead +
-      (tiles ? pa::prefill_scored_workspace_bytes(cache.num_kv_heads, num_sms())
-             : pa::scored_workspace_bytes(num_rows, num_heads, cache.num_kv_heads, cache.head_dim,
-                                          num_sms()));
+      kScoredHead + (fit ? pa::prefill_scored_workspace_bytes(cache.num_kv_heads, num_sms()) : 0);
   if (workspace_bytes < need)
     return fail(PA_ERR_INVALID, ("workspace of " + std::to_string(need) + " bytes needed").c_str());
   if (tiles) {
@@ -416,8 +416,9 @@ pa_status scored_rows(const char* fn, void* out, const void* q, const void* k_ca
   p.scale_log2 = scale * 1.4426950408889634f;
   p.mod = mod;
   return cuda_status(
-      pa::launch_decode_scored(p, static_cast<char*>(workspace) + kScoredHead, cache.head_dim,
-                               group, format_of(cache), num_sms(), s),
+      pa::launch_decode_scored(p, static_cast<char*>(workspace) + kScoredHead,
+                               workspace_bytes - kScoredHead, cache.head_dim, group,
+                               format_of(cache), num_sms(), s),
       fn);
 }
 

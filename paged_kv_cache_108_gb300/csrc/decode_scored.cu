@@ -46,7 +46,8 @@
 // row of 128 K tokens 59.3 for 57.4.  A counter of arrivals, exchanged with the
 // call's tag, made 38 CTAs of one unit queue for it.)  Flags carry a tag of the
 // call, so the workspace needs no initialisation.  Where units are many times
-// the CTAs (kWholeUnits), each CTA takes one whole unit.
+// the CTAs (kWholeUnits), and where there is no room for parts, each CTA takes one
+// whole unit.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -929,7 +930,7 @@ cudaError_t launch_one(const ScoredParams& p, int num_sms, cudaStream_t stream) 
   using C = Cfg<D, G, F>;
   const int64_t units = (int64_t)p.num_rows * p.num_kv_heads;
   const int64_t at_once = (int64_t)kCtasPerSm * num_sms;
-  const bool whole = units >= kWholeUnits * at_once;
+  const bool whole = !p.flags || units >= kWholeUnits * at_once;
   const cudaError_t e = allow_large<decode_scored_kernel<D, G, F>>();
   if (e != cudaSuccess) return e;
   return launch_dependent<decode_scored_kernel<D, G, F>>(
@@ -968,20 +969,26 @@ static int64_t split_ctas(int64_t num_kv_heads, int num_sms) {
 }
 static size_t flag_bytes(int64_t ctas) { return (size_t)(ctas * 16 + 255) / 256 * 256; }
 
+static size_t split_bytes(int64_t num_kv_heads, int group, int head_dim, int num_sms) {
+  const int64_t ctas = split_ctas(num_kv_heads, num_sms);
+  return flag_bytes(ctas) + (size_t)ctas * 2 * part_words(group, head_dim) * 4;
+}
+
 size_t scored_workspace_bytes(int64_t num_rows, int64_t num_heads, int64_t num_kv_heads,
                               int head_dim, int num_sms) {
   if (num_rows * num_kv_heads >= (int64_t)kWholeUnits * kCtasPerSm * num_sms) return 0;
-  const int64_t ctas = split_ctas(num_kv_heads, num_sms);
-  return flag_bytes(ctas) +
-         (size_t)ctas * 2 * part_words((int)(num_heads / num_kv_heads), head_dim) * 4;
+  return split_bytes(num_kv_heads, (int)(num_heads / num_kv_heads), head_dim, num_sms);
 }
 
-cudaError_t launch_decode_scored(ScoredParams p, void* workspace, int head_dim, int group,
-                                 KvFormat format, int num_sms, cudaStream_t stream) {
-  p.flags = static_cast<unsigned long long*>(workspace);
-  p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                     flag_bytes(split_ctas(p.num_kv_heads, num_sms)));
-  p.epoch = tc::next_call_epoch();
+cudaError_t launch_decode_scored(ScoredParams p, void* workspace, size_t bytes, int head_dim,
+                                 int group, KvFormat format, int num_sms, cudaStream_t stream) {
+  p.flags = nullptr;
+  if (bytes >= split_bytes(p.num_kv_heads, group, head_dim, num_sms)) {
+    p.flags = static_cast<unsigned long long*>(workspace);
+    p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                       flag_bytes(split_ctas(p.num_kv_heads, num_sms)));
+    p.epoch = tc::next_call_epoch();
+  }
   return head_dim == 128 ? launch_f<128>(p, group, format, num_sms, stream)
                          : launch_f<64>(p, group, format, num_sms, stream);
 }

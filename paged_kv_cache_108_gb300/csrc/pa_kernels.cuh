@@ -104,6 +104,8 @@ struct PrefillLaunch {
   const float* v_scale;
   ScoreMod mod;            // changed scores
 };
+bool prefill_sizes_fit(int head_dim, int group, int num_seqs, int block_size);
+// That, and a driver that encodes tensor maps.
 bool prefill_supported(int head_dim, int group, bool fp8, int num_seqs, int block_size);
 cudaError_t launch_prefill_tc(const PrefillLaunch& a, cudaStream_t stream);
 // The same with changed scores (prefill_scored.cu); the limits are those above.
@@ -232,8 +234,9 @@ struct ScoredParams {
 };
 size_t scored_workspace_bytes(int64_t num_rows, int64_t num_heads, int64_t num_kv_heads,
                               int head_dim, int num_sms);
-cudaError_t launch_decode_scored(ScoredParams p, void* workspace, int head_dim, int group,
-                                 KvFormat format, int num_sms, cudaStream_t stream);
+// Without room for the parts in the workspace each unit is one CTA's.
+cudaError_t launch_decode_scored(ScoredParams p, void* workspace, size_t bytes, int head_dim,
+                                 int group, KvFormat format, int num_sms, cudaStream_t stream);
 
 // Key ranges of full blocks and block selection (block_select.cu).
 struct SummaryParams {

@@ -960,11 +960,15 @@ cudaError_t launch_g(const Params& prm, const CUtensorMap& mk, const CUtensorMap
 
 }  // namespace pf
 
-bool prefill_supported(int head_dim, int group, bool fp8, int num_seqs, int block_size) {
+bool prefill_sizes_fit(int head_dim, int group, int num_seqs, int block_size) {
   // block_size >= 8 keeps every K/V box 1024-byte aligned in smem (whole
   // 128-byte-swizzle atoms), as in the decode kernels
   return head_dim == pf::D && (group == 1 || group == 2 || group == 4 || group == 8) &&
-         num_seqs <= pf::kMaxReqs && block_size >= 8 && tc::encode_fn() != nullptr;
+         num_seqs <= pf::kMaxReqs && block_size >= 8;
+}
+
+bool prefill_supported(int head_dim, int group, bool fp8, int num_seqs, int block_size) {
+  return prefill_sizes_fit(head_dim, group, num_seqs, block_size) && tc::encode_fn() != nullptr;
 }
 
 cudaError_t launch_prefill_tc(const PrefillLaunch& a, cudaStream_t stream) {

@@ -437,7 +437,9 @@ def gather_cache(k_out, v_out, k_cache, v_cache, block_tables, context_lens, out
 
 
 def scored_workspace_size(num_rows: int, num_heads: int, num_kv_heads: int, head_dim: int) -> int:
-    return int(_lib.lib().pa_scored_workspace_size(num_rows, num_heads, num_kv_heads, head_dim))
+    """Bytes for calls of up to ``num_rows`` rows, a few long ones among them."""
+    return max(int(_lib.lib().pa_scored_workspace_size(n, num_heads, num_kv_heads, head_dim))
+               for n in (num_rows, min(num_rows, 1)))
 
 
 def alloc_scored_workspace(num_rows, num_heads, num_kv_heads, head_dim, device=None):
