@@ -740,7 +740,7 @@ typedef struct {
  * head_dim 128 and more than 8 rows up to 81 MB, whatever the lengths.)  A
  * workspace serves calls of as many rows and of fewer, on one stream; calls
  * that share one must not overlap on the GPU.  It needs no initialisation.
- * With head_dim 64, some hundreds of rows and more ask for no room for partial sums:
+ * With head_dim 64, many thousands of rows ask for no room for partial sums:
  * where the same workspace is to serve a few long rows too, allocate the larger
  * of the sizes for one row and for the most rows, or such a row is one CTA's.
  * The calls set its word 0 (int32) to a nonzero code if a bounded wait inside

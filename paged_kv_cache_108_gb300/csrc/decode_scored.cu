@@ -45,9 +45,8 @@
 // parts through memory: 64 capped rows 100.4 us, where this takes 97.3, one int8
 // row of 128 K tokens 59.3 for 57.4.  A counter of arrivals, exchanged with the
 // call's tag, made 38 CTAs of one unit queue for it.)  Flags carry a tag of the
-// call, so the workspace needs no initialisation.  Where units are many times
-// the CTAs (kWholeUnits), and where there is no room for parts, each CTA takes one
-// whole unit.
+// call, so the workspace needs no initialisation.  Where there is no room for
+// parts, and where takes_whole() says so, each CTA takes one whole unit.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -62,14 +61,13 @@ namespace pa {
 
 namespace {
 
-constexpr int kCtasPerSm = 2;     // what registers and shared memory are kept to
-// Units per CTA from which none is split: the prologue's walk over all rows is
-// saved, and a long row among so many others weighs little.  (Whole and split, us:
-// 4 units a CTA 212, 222, of shorter rows 79, 79; 6.6 148, 146; 26 198, 204.)
-constexpr int kWholeUnits = 6;
+// What registers and shared memory are kept to.  (64 channels over bf16 with two:
+// 2000 rows of 300 tokens 91 us, with three 80.)
+constexpr int ctas_per_sm(int head_dim, KvFormat f) { return head_dim == 64 && f == kBf16 ? 3 : 2; }
 
 template <int D, int G, KvFormat F>
 struct Cfg {
+  static constexpr int kCtasPerSm = ctas_per_sm(D, F);
   static constexpr int kRow = D * (F == kBf16 ? 2 : 1);  // bytes of a token's channels
   static constexpr int kPieces = kRow / 16;
   static constexpr int kChunk = F == kBf16 ? 16 : 32;  // tokens a warp handles at a time
@@ -183,7 +181,7 @@ struct __align__(16) Chunk {
 enum { kOpens = 1, kCloses = 2, kNobody = 4 };
 
 template <int D, int G, KvFormat F>
-__global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, Cfg<D, G, F>::kCtasPerSm)
     decode_scored_kernel(const __grid_constant__ ScoredParams p, bool whole_units) {
   using C = Cfg<D, G, F>;
   constexpr bool F16 = F != kBf16;
@@ -200,7 +198,7 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
   __shared__ __align__(16) float s_o[kWarps][kColHeads][D];
   __shared__ float s_ml[kWarps][kColHeads][2];
   __shared__ float s_ref[kWarps][kColHeads];
-  __shared__ long long s_sum[kWarps], s_others[kWarps], s_before;
+  __shared__ long long s_sum[kWarps], s_before;
   __shared__ Row s_cur;
   __shared__ float s_factor[kWarps][G], s_max[G], s_l[G], s_post[G];
   __shared__ int s_row;
@@ -220,59 +218,48 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
     cur = row_of(p, row);
     hi = K = steps_of<kStep>(cur);
   } else {
-    // K, and (rows in tiles of one a thread) the row that the last step lies in
+    // K, and the row that this CTA's last step lies in; each thread counts the steps
+    // of rows side by side (by tiles of kThreads rows, one behind the other: 10000 rows
+    // of 40 tokens 745 us, where this takes 713)
+    const int per = (p.num_rows + kThreads - 1) / kThreads;
+    const int r0 = min(tid * per, p.num_rows), r1 = min(r0 + per, p.num_rows);
     Row mine = {-1, 0, 0, 0};
-    int n = 0;  // steps of this thread's row
-    long long others = 0;
-    for (int r = tid + kThreads; r < p.num_rows; r += kThreads)
-      others += steps_of<kStep>(row_of(p, r));
-    long long before = 0;
-    for (int base = 0; base < p.num_rows; base += kThreads) {
-      n = 0;
-      if (base + tid < p.num_rows) {
-        mine = row_of(p, base + tid);
+    int n = 0;  // steps of this thread's last row
+    long long steps = 0;
+#pragma unroll 4
+    for (int r = r0; r < r1; ++r) {
+      mine = row_of(p, r);
+      n = steps_of<kStep>(mine);
+      steps += n;
+    }
+    long long end = steps;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long up = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end += up;
+    }
+    if (lane == 31) s_sum[warp] = end;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) end += s_sum[w];
+      K += s_sum[w];
+    }
+    ctas = (int)min((long long)(gridDim.x / hkv), K);  // (K is not 0)
+    if (part >= ctas) return;
+    lo = tc::range_lo(part, K, ctas);
+    hi = tc::range_lo(part + 1, K, ctas);
+    if (end - steps < hi && hi <= end) {
+      int r = r1 - 1;
+      for (end -= n; hi <= end; end -= n) {
+        mine = row_of(p, --r);
         n = steps_of<kStep>(mine);
       }
-      long long wide = n;
-#pragma unroll
-      for (int d = 1; d < 32; d *= 2) {
-        const long long up = __shfl_up_sync(0xffffffffu, wide, d);
-        if (lane >= d) wide += up;
-      }
-      if (base == 0) {
-#pragma unroll
-        for (int d = 16; d; d /= 2) others += __shfl_xor_sync(0xffffffffu, others, d);
-      } else {
-        __syncthreads();  // s_sum is free
-      }
-      if (lane == 31) s_sum[warp] = wide;
-      if (base == 0 && lane == 0) s_others[warp] = others;
-      if (tid == 0) s_row = -1;
-      __syncthreads();
-      long long start = before + wide - n, end = before;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) start += s_sum[w];
-        end += s_sum[w];
-      }
-      if (base == 0) {
-        K = end;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) K += s_others[w];
-        ctas = (int)min((long long)(gridDim.x / hkv), K);  // (K is not 0)
-        if (part >= ctas) return;
-        lo = tc::range_lo(part, K, ctas);
-        hi = tc::range_lo(part + 1, K, ctas);
-      }
-      if (start < hi && hi <= start + n) {
-        s_row = base + tid;
-        s_before = start;
-        s_cur = mine;
-      }
-      __syncthreads();
-      if (s_row >= 0) break;
-      before = end;
+      s_row = r;
+      s_before = end;
+      s_cur = mine;
     }
+    __syncthreads();
     row = s_row;
     cur = s_cur;
     rel = (int)(s_before - lo);
@@ -915,6 +902,26 @@ __global__ void __launch_bounds__(Cfg<D, G, F>::kThreads, kCtasPerSm)
   }
 }
 
+// Units per CTA, for two an SM, from which no room for parts is asked for.  (657,
+// rows of 400 tokens and 64 channels, whole and split, us: bf16 4043, 3796, int8
+// 4078, 3585.)
+constexpr int kManyUnits = 512;
+
+// Whether each unit goes to one CTA although its parts have room.  CTAs handed out
+// as others end, a row's heads to neighbours, keep many heads closer together than
+// equal ranges do; but a row much longer than the others is then one CTA's, so only
+// where the longest that there may be is short beside a CTA's share.  (Whole and
+// split, us, e4m3 rows of 32 heads: 256 of 2900 tokens 937, 978, 600 of 2900 2130,
+// 2280, 350 of 1200 578, 586, of lengths up to 1200 369, 353, 1000 of 300 617, 582;
+// 8 heads: 1000 rows of 2000 674, 670, 512 of up to 2000 250, 238; 228 rows of 300
+// with one of 128 K among them, bf16: 2250, 162.)
+constexpr int kWholeHeads = 16, kWholeTokens = 1024, kTokensPerUnit = 128;
+bool takes_whole(const ScoredParams& p, int64_t at_once) {
+  const int64_t longest = (int64_t)p.max_blocks << p.log2_block_size;
+  return p.num_kv_heads >= kWholeHeads && longest >= kWholeTokens &&
+         longest * at_once <= (int64_t)p.num_rows * p.num_kv_heads * kTokensPerUnit;
+}
+
 // Ranges per head: such that the fewest rounds of the CTAs that run at once
 // do the most.
 int ranges_of(int64_t heads, int64_t at_once) {
@@ -929,8 +936,8 @@ template <int D, int G, KvFormat F>
 cudaError_t launch_one(const ScoredParams& p, int num_sms, cudaStream_t stream) {
   using C = Cfg<D, G, F>;
   const int64_t units = (int64_t)p.num_rows * p.num_kv_heads;
-  const int64_t at_once = (int64_t)kCtasPerSm * num_sms;
-  const bool whole = !p.flags || units >= kWholeUnits * at_once;
+  const int64_t at_once = (int64_t)C::kCtasPerSm * num_sms;
+  const bool whole = !p.flags || takes_whole(p, at_once);
   const cudaError_t e = allow_large<decode_scored_kernel<D, G, F>>();
   if (e != cudaSuccess) return e;
   return launch_dependent<decode_scored_kernel<D, G, F>>(
@@ -964,29 +971,35 @@ cudaError_t launch_f(const ScoredParams& p, int group, KvFormat format, int num_
 }  // namespace
 
 // Flags of two parts for each CTA, then the parts.
-static int64_t split_ctas(int64_t num_kv_heads, int num_sms) {
-  return ranges_of(num_kv_heads, (int64_t)kCtasPerSm * num_sms) * num_kv_heads;
+static int64_t split_ctas(int64_t num_kv_heads, int num_sms, int per_sm) {
+  return ranges_of(num_kv_heads, (int64_t)per_sm * num_sms) * num_kv_heads;
 }
 static size_t flag_bytes(int64_t ctas) { return (size_t)(ctas * 16 + 255) / 256 * 256; }
-
-static size_t split_bytes(int64_t num_kv_heads, int group, int head_dim, int num_sms) {
-  const int64_t ctas = split_ctas(num_kv_heads, num_sms);
+static size_t split_bytes(int64_t num_kv_heads, int group, int head_dim, int num_sms, int per_sm) {
+  const int64_t ctas = split_ctas(num_kv_heads, num_sms, per_sm);
   return flag_bytes(ctas) + (size_t)ctas * 2 * part_words(group, head_dim) * 4;
 }
 
 size_t scored_workspace_bytes(int64_t num_rows, int64_t num_heads, int64_t num_kv_heads,
                               int head_dim, int num_sms) {
-  if (num_rows * num_kv_heads >= (int64_t)kWholeUnits * kCtasPerSm * num_sms) return 0;
-  return split_bytes(num_kv_heads, (int)(num_heads / num_kv_heads), head_dim, num_sms);
+  if (num_rows * num_kv_heads >= (int64_t)kManyUnits * 2 * num_sms) return 0;
+  const int group = (int)(num_heads / num_kv_heads);
+  size_t most = 0;
+  for (KvFormat f : {kBf16, kE4m3, kInt8}) {
+    const size_t n = split_bytes(num_kv_heads, group, head_dim, num_sms, ctas_per_sm(head_dim, f));
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 cudaError_t launch_decode_scored(ScoredParams p, void* workspace, size_t bytes, int head_dim,
                                  int group, KvFormat format, int num_sms, cudaStream_t stream) {
+  const int per_sm = ctas_per_sm(head_dim, format);
   p.flags = nullptr;
-  if (bytes >= split_bytes(p.num_kv_heads, group, head_dim, num_sms)) {
+  if (bytes >= split_bytes(p.num_kv_heads, group, head_dim, num_sms, per_sm)) {
     p.flags = static_cast<unsigned long long*>(workspace);
     p.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                       flag_bytes(split_ctas(p.num_kv_heads, num_sms)));
+                                       flag_bytes(split_ctas(p.num_kv_heads, num_sms, per_sm)));
     p.epoch = tc::next_call_epoch();
   }
   return head_dim == 128 ? launch_f<128>(p, group, format, num_sms, stream)
