@@ -745,7 +745,8 @@ typedef struct {
  * of the sizes for one row and for the most rows, or such a row is one CTA's.
  * The calls set its word 0 (int32) to a nonzero code if a bounded wait inside
  * a kernel expired, or (tiles) a block id was out of range; they never clear
- * it.  After such a code it must be zeroed before the call's graph is replayed. */
+ * it: zero it once to know its codes from what the memory held before.  After
+ * such a code it must be zeroed before the call's graph is replayed. */
 size_t pa_scored_workspace_size(int32_t num_rows, int32_t num_heads, int32_t num_kv_heads,
                                 int32_t head_dim);
 

@@ -442,13 +442,21 @@ def scored_workspace_size(num_rows: int, num_heads: int, num_kv_heads: int, head
                for n in (num_rows, min(num_rows, 1)))
 
 
-def alloc_scored_workspace(num_rows, num_heads, num_kv_heads, head_dim, device=None):
-    """A caller-owned device workspace for ``decode_scored`` (``num_rows``
-    sequences) or ``varlen_scored`` (``num_rows`` new tokens)."""
-    device = torch.device(device or "cuda")
+def _new_scored_workspace(num_rows, num_heads, num_kv_heads, head_dim, device):
     with torch.cuda.device(device):  # the size goes by the device's SMs
         n = scored_workspace_size(num_rows, num_heads, num_kv_heads, head_dim)
         return torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+
+
+def alloc_scored_workspace(num_rows, num_heads, num_kv_heads, head_dim, device=None):
+    """A caller-owned device workspace for ``decode_scored`` (up to ``num_rows``
+    sequences) or ``varlen_scored`` (up to ``num_rows`` new tokens).  Its first
+    four bytes (int32) are the calls' error code, zeroed here: nonzero once a
+    call could not finish.  (A call without a workspace drops its own.)"""
+    ws = _new_scored_workspace(num_rows, num_heads, num_kv_heads, head_dim,
+                               torch.device(device or "cuda"))
+    ws[:4].zero_()
+    return ws
 
 
 def _scored_workspace(workspace, q, k_cache, stream):
@@ -461,8 +469,8 @@ def _scored_workspace(workspace, q, k_cache, stream):
         side = (stream if isinstance(stream, torch.cuda.Stream)
                 else torch.cuda.ExternalStream(int(stream), device=q.device))
     with torch.cuda.stream(side):
-        return alloc_scored_workspace(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2],
-                                      q.device)
+        return _new_scored_workspace(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2],
+                                     q.device)
 
 
 def decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, scale, cap=0.0, window=0,

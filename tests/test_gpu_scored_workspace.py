@@ -95,3 +95,13 @@ def test_more_rows_than_threads_of_a_cta():
     rows = [(int(starts[i]) + j, i, n - t + j) for i, (n, t) in enumerate(zip(lens, new)) if n >= t
             for j in range(t)]
     _check_rows(c, outs[0], q, rows[::13] + rows[-2:], 30.0, 0, False)
+
+
+def test_the_error_word_of_a_new_workspace_is_zero():
+    for rows, d in ((3, 64), (40, 128)):
+        n = ops.scored_workspace_size(rows, 8, 2, d)
+        torch.cuda.empty_cache()
+        junk = torch.full((n,), 255, dtype=torch.uint8, device=DEV)  # its memory is handed on
+        del junk
+        ws = ops.alloc_scored_workspace(rows, 8, 2, d)
+        assert int(ws[:4].view(torch.int32).item()) == 0
