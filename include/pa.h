@@ -686,7 +686,7 @@ pa_status pa_decode_selected(void* out, const void* q, const void* k_cache, cons
  *  k_scale, v_scale  e4m3: device scalars, read.  int8: the units, written.
  *                bf16: NULL.
  *  Other arguments, limits and refusals as pa_rope_and_cache; nor may q_out
- *  overlap the units. */
+ *  overlap the units, nor the caches and units each other. */
 pa_status pa_norm_rope_and_cache(void* q_out, const void* query, int64_t q_stride,
                                  int32_t num_heads, const void* key, int64_t k_stride,
                                  const void* value, int64_t v_stride, void* k_cache, void* v_cache,

@@ -1178,13 +1178,26 @@ pa_status pa_norm_rope_and_cache(void* q_out, const void* query, int64_t q_strid
   st = rope_params(fn, q_out, query, q_stride, num_heads, key, k_stride, value, v_stride, k_cache,
                    v_cache, cache, slot_mapping, positions, cos_sin, rope, num_tokens, &p, true);
   if (st != PA_OK || num_tokens == 0) return st;
+  // what is written must lie apart
+  auto meet = [](const void* a, int64_t bytes, const void* b, int64_t more) {
+    const auto* b0 = static_cast<const char*>(b);
+    return rows_meet(a, bytes, bytes, 1, b0, b0 + more);
+  };
+  const int64_t slots = (int64_t)cache.num_blocks * cache.block_size;
+  const int64_t pool = slots * cache.num_kv_heads * cache.head_dim *
+                       (cache.dtype == PA_KV_BF16 ? 2 : 1);
+  if (meet(k_cache, pool, v_cache, pool))
+    return pa_fail(PA_ERR_INVALID, "pa_norm_rope_and_cache: k_cache and v_cache overlap");
   if (cache.dtype == PA_KV_INT8) {
-    const int64_t units = (int64_t)cache.num_blocks * cache.block_size * cache.num_kv_heads * 4;
-    const auto* o0 = static_cast<const char*>(q_out);
-    const char* o1 = o0 + 2 * (int64_t)num_tokens * num_heads * cache.head_dim;
-    if (num_heads && (rows_meet(k_scale, units, units, 1, o0, o1) ||
-                      rows_meet(v_scale, units, units, 1, o0, o1)))
+    const int64_t units = slots * cache.num_kv_heads * 4;
+    const int64_t out = 2 * (int64_t)num_tokens * num_heads * cache.head_dim;
+    if (num_heads && (meet(k_scale, units, q_out, out) || meet(v_scale, units, q_out, out)))
       return pa_fail(PA_ERR_INVALID, "pa_norm_rope_and_cache: q_out overlaps k_scale or v_scale");
+    if (meet(k_scale, units, v_scale, units))
+      return pa_fail(PA_ERR_INVALID, "pa_norm_rope_and_cache: k_scale and v_scale overlap");
+    if (meet(k_scale, units, k_cache, pool) || meet(k_scale, units, v_cache, pool) ||
+        meet(v_scale, units, k_cache, pool) || meet(v_scale, units, v_cache, pool))
+      return pa_fail(PA_ERR_INVALID, "pa_norm_rope_and_cache: the units overlap a cache");
     p.k_units = k_scale;
     p.v_units = v_scale;
   } else {
