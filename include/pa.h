@@ -736,10 +736,11 @@ typedef struct {
 
 /* Workspace bytes that serve both pa_decode_scored (num_rows: sequences) and
  * pa_varlen_scored (num_rows: new tokens) on the current device; 0 for bad
- * sizes.  (Partial sums of the work that the SMs share: up to 5 MB, or with
- * head_dim 128 and more than 8 rows up to 81 MB, whatever the lengths.)  A
- * workspace serves calls of as many rows and of fewer, on one stream; calls
- * that share one must not overlap on the GPU.  It needs no initialisation.
+ * sizes.  (Partial sums of the work that the SMs share: up to 8 MB for up to 64
+ * KV heads, or with head_dim 128 and more than 8 rows up to 81 MB, whatever the
+ * lengths.)  A workspace serves calls of as many rows and of fewer, on one
+ * stream; calls that share one must not overlap on the GPU.  It needs no
+ * initialisation.
  * With head_dim 64, many thousands of rows ask for no room for partial sums:
  * where the same workspace is to serve a few long rows too, allocate the larger
  * of the sizes for one row and for the most rows, or such a row is one CTA's.
