@@ -778,18 +778,19 @@ pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const 
  *                bytes; row by row with fewer, at least 256, no row is split.
  *  Steps of many new tokens run on tensor-core tiles (more than 2 per request
  *  on average and 8 in all over bf16, 4 and 16 over e4m3), with head_dim 128,
- *  block_size >= 8, at most 256 requests and 65535 new tokens; a request that
- *  sees more than max_blocks_per_seq * block_size keys then gets zero rows,
- *  and a block outside the pool is replaced by block 0.  A value that is not
- *  finite makes NaNs of all rows that share a tile with one that sees it; and
- *  with a cap up to 55 and no slopes over bf16, values above 2^30 may overflow
- *  and those below 2^-40 be lost.  All other steps are computed row by row,
- *  each new token reading its keys (long prompts over 8-bit rows are better
- *  gathered first).
+ *  block_size >= 8, at most 256 requests and, for G = num_heads / num_kv_heads,
+ *  16 million / G new tokens; a request that sees more than max_blocks_per_seq *
+ *  block_size keys then gets zero rows, and a block outside the pool is replaced
+ *  by block 0.  A value that is not finite makes NaNs of all rows that share a
+ *  tile with one that sees it; and with a cap up to 55 and no slopes over bf16,
+ *  values above 2^30 may overflow and those below 2^-40 be lost.  All other steps
+ *  are computed row by row, each new token reading its keys (long prompts over
+ *  8-bit rows are better gathered first).
  *  A request whose new tokens exceed its seq_len gets zero rows.  Rows of out
  *  before query_start_loc[0] or behind query_start_loc[num_seqs] are left as
  *  they were.
- *  Limits and other arguments as pa_decode_scored and pa_varlen_attention. */
+ *  Limits as pa_decode_scored, its sequences being new tokens; other arguments as
+ *  pa_decode_scored and pa_varlen_attention. */
 pa_status pa_varlen_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
                            pa_cache_desc cache, const int32_t* block_tables,
                            int32_t max_blocks_per_seq, const int32_t* seq_lens,

@@ -361,7 +361,8 @@ pa_status scored_rows(const char* fn, void* out, const void* q, const void* k_ca
   const RowsRule rows = cache.dtype == PA_KV_BF16 ? kRowsBf16 : kRowsE4m3;
   const bool fit =
       starts && cache.dtype != PA_KV_INT8 && num_rows > rows.in_all &&
-      num_rows > rows.per_request * (int64_t)num_seqs && num_rows <= 65535 &&
+      num_rows > rows.per_request * (int64_t)num_seqs &&
+      pa::prefill_scored_fits(num_rows, group, num_seqs) &&
       pa::prefill_sizes_fit(cache.head_dim, group, num_seqs, cache.block_size);
   const bool tiles = fit && pa::prefill_supported(cache.head_dim, group,
                                                   cache.dtype == PA_KV_FP8_E4M3, num_seqs,

@@ -108,7 +108,9 @@ bool prefill_sizes_fit(int head_dim, int group, int num_seqs, int block_size);
 // That, and a driver that encodes tensor maps.
 bool prefill_supported(int head_dim, int group, bool fp8, int num_seqs, int block_size);
 cudaError_t launch_prefill_tc(const PrefillLaunch& a, cudaStream_t stream);
-// The same with changed scores (prefill_scored.cu); the limits are those above.
+// The same with changed scores (prefill_scored.cu); the limits are those above, and
+// of the new tokens:
+bool prefill_scored_fits(int64_t num_tokens, int group, int num_seqs);
 // Its workspace: the error word's 256 bytes, then so many.
 size_t prefill_scored_workspace_bytes(int num_kv_heads, int num_sms);
 cudaError_t launch_prefill_scored(const PrefillLaunch& a, cudaStream_t stream);

@@ -131,7 +131,7 @@ struct Cfg {
   static constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
   static constexpr int OFF_ABORT = OFF_TMEM + 4;
   static constexpr int OFF_RING = (OFF_ABORT + 4 + 15) / 16 * 16;
-  // pairs of tiles before each request, [R + 1]; at most 65535 new tokens
+  // pairs of tiles before each request, [R + 1]: 16 bits (prefill_scored_fits)
   static constexpr int OFF_TP = OFF_RING + NITEM * kItemBytes;
   static constexpr int SMEM_BYTES = OFF_TP + (kMaxReqs + 1) * 2 + 1024;  // + alignment slack
   static constexpr float kRaise = FP8 ? 7.f : 0.f;  // log2 of the factor of P and its sum
@@ -1315,6 +1315,12 @@ cudaError_t launch_f(const Params& prm, const CUtensorMap& mk, const CUtensorMap
 }
 
 }  // namespace ps
+
+// A pair holds 2 * 128 / group tokens of one request; the last of each request
+// may hold fewer.
+bool prefill_scored_fits(int64_t num_tokens, int group, int num_seqs) {
+  return num_tokens * group / 256 + num_seqs <= 65535;
+}
 
 size_t prefill_scored_workspace_bytes(int num_kv_heads, int num_sms) {
   const int64_t ranges = ps::ranges_of(num_kv_heads, num_sms), ctas = ranges * num_kv_heads;
