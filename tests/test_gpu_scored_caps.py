@@ -16,21 +16,25 @@ import torch
 
 from oracle import scored
 from paged_kv_cache_108_gb300 import ops
-from tests.test_gpu_scored import _attn_case, _bf16, _dev, _mod, _np, _values
+from tests.test_gpu_scored import _attn_case, _bf16, _dev, _mod, _np, _slopes, _values
 from tests.test_gpu_scored_edges import _rows, _step, _varlen
 
 pytestmark = pytest.mark.gpu
 
 
-def _check(c, got, q, rows, cap, tiles, window=0):
+def _check(c, got, q, rows, cap, tiles, window=0, bias=False, prefix=None):
     """rows: (row of q, sequence, position)."""
     k, v = _values(c["kc"], c["ks"]), _values(c["vc"], c["vs"])
     got, q = _np(got), _np(q)
     most_v = np.nanmax(np.abs(v))
+    slopes = _slopes(c["H"]).astype(np.float64) if bias else None
     for r, i, pos in rows:
         n = c["lens"][i]
-        want, mag, most = scored.attend(q[r], pos, n, k, v, c["tables"][i], c["scale"], cap, window)
+        want, mag, most = scored.attend(q[r], pos, n, k, v, c["tables"][i], c["scale"], cap, window,
+                                        slopes, prefix[i] if prefix else 0)
         e = (c["d"] + 6) * 2 ** -24 * most + 2 ** -21 + 2 ** -20 * most
+        if bias:
+            e += 3 * 2 ** -24 * n * slopes.max()
         if c["kv"] == "bf16":
             e += 2 ** -9 if tiles else 2 ** -16
             floor = 0.0
@@ -96,3 +100,28 @@ def test_capped_rows_do_not_depend_on_loud_neighbours(kv):
     q[1::2] *= 256.0
     got = _varlen(c, q, starts, cap=200.0)
     assert torch.equal(got[::2], want[::2])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "int8"])
+def test_large_caps_with_biases_windows_and_prefixes(kv):
+    new, lens, prefix = [70, 129, 40], [900, 513, 60], [850, 0, 60]
+    c = _attn_case(105, kv, lens, 8, 2, 128, 16)
+    q, starts = _step(c, new)
+    q[::7] *= 64.0
+    for cap, window in ((100.0, 0), (1e4, 300)):
+        out = _varlen(c, q, starts, cap=cap, window=window, bias=True, prefix=prefix)
+        _check(c, out, q, _rows(c, starts, 17), cap, kv != "int8", window, True, prefix)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "int8"])
+def test_queries_that_are_not_finite_under_a_large_cap(kv):
+    c = _attn_case(106, kv, [200, 77], 8, 2, 128, 16)
+    q, starts = _step(c, [40, 30])
+    clean = _varlen(c, q, starts, cap=1e3)
+    q[3, 2, 5] = float("nan")
+    q[50, 7, 1] = float("inf")
+    got = _varlen(c, q, starts, cap=1e3)
+    assert torch.isnan(got[3, 2]).all()
+    same = torch.ones(got.shape[:2], dtype=torch.bool)
+    same[3, 2] = same[50, 7] = False
+    assert torch.equal(got[same.cuda()], clean[same.cuda()])
