@@ -782,10 +782,12 @@ pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const 
  *  16 million / G new tokens; a request that sees more than max_blocks_per_seq *
  *  block_size keys then gets zero rows, and a block outside the pool is replaced
  *  by block 0.  A value that is not finite makes NaNs of all rows that share a
- *  tile with one that sees it; and with a cap up to 55 and no slopes over bf16,
- *  values above 2^30 may overflow and those below 2^-40 be lost.  All other steps
- *  are computed row by row, each new token reading its keys (long prompts over
- *  8-bit rows are better gathered first).
+ *  tile with one that sees it; with a cap up to 55 and no slopes over bf16,
+ *  values above 2^30 may overflow and those below 2^-40 be lost; and a row's last
+ *  bits may depend on the rows beside it (which of two forms a cap up to 64 takes
+ *  is chosen for 32 rows at a time).  All other steps are computed row by row,
+ *  each new token reading its keys (long prompts over 8-bit rows are better
+ *  gathered first).
  *  A request whose new tokens exceed its seq_len gets zero rows.  Rows of out
  *  before query_start_loc[0] or behind query_start_loc[num_seqs] are left as
  *  they were.

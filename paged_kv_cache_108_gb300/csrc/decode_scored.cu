@@ -42,9 +42,9 @@
 // sums go to the workspace early, and the first one, whose end it holds, is joined
 // from its own sums in shared memory and the parts of the CTAs before it, in their
 // order, once their flags are up.  (From the first unit to the last, with all
-// parts through memory: 64 capped rows 100.4 us, where this takes 97.3, one int8
-// row of 128 K tokens 59.3 for 57.4.  A counter of arrivals, exchanged with the
-// call's tag, made 38 CTAs of one unit queue for it.)  Flags carry a tag of the
+// parts through memory: 64 capped rows 98.7 us, where this takes 97.6, 64 windowed
+// int8 rows 39.2 for 38.3, one int8 row of 128 K tokens the same.  A counter of
+// arrivals, exchanged with the call's tag, made 38 CTAs of one unit queue for it.)  Flags carry a tag of the
 // call, so the workspace needs no initialisation.  Where there is no room for
 // parts, and where takes_whole() says so, each CTA takes one whole unit.
 #include <cuda_bf16.h>
