@@ -754,7 +754,8 @@ size_t pa_scored_workspace_size(int32_t num_rows, int32_t num_heads, int32_t num
 /* pa_decode_scored -- pa_decode with changed scores, over any cache.  A
  * sequence's query is at position context_lens[i] - 1.  Any finite scale.
  *  workspace     256-byte aligned, of pa_scored_workspace_size(num_seqs, ...)
- *                bytes; with fewer, at least 256, no row is split.
+ *                bytes.  The size for one row, without room for tiles, serves
+ *                any number; with fewer bytes, at least 256, no row is split.
  *  Limits: num_heads / num_kv_heads in {1, 2, 4, 8}; max_blocks_per_seq *
  *  block_size up to 2^30; num_kv_heads up to 32768; num_seqs * num_kv_heads
  *  up to 2^27; else PA_ERR_UNSUPPORTED.  A block outside the pool is passed over.

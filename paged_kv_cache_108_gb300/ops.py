@@ -451,15 +451,16 @@ def _new_scored_workspace(num_rows, num_heads, num_kv_heads, head_dim, device):
 def alloc_scored_workspace(num_rows, num_heads, num_kv_heads, head_dim, device=None):
     """A caller-owned device workspace for ``decode_scored`` (up to ``num_rows``
     sequences) or ``varlen_scored`` (up to ``num_rows`` new tokens).  Its first
-    four bytes (int32) are the calls' error code, zeroed here: nonzero once a
-    call could not finish.  (A call without a workspace drops its own.)"""
+    four bytes (int32) are the calls' error code, zeroed here (on the current
+    stream): nonzero once a call could not finish.  (A call without a workspace
+    drops its own.)"""
     ws = _new_scored_workspace(num_rows, num_heads, num_kv_heads, head_dim,
                                torch.device(device or "cuda"))
     ws[:4].zero_()
     return ws
 
 
-def _scored_workspace(workspace, q, k_cache, stream):
+def _scored_workspace(workspace, q, k_cache, stream, num_rows=None):
     if (workspace is not None or not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != 3
             or not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4):
         return workspace  # (what is wrong is refused by the binding)
@@ -469,7 +470,7 @@ def _scored_workspace(workspace, q, k_cache, stream):
         side = (stream if isinstance(stream, torch.cuda.Stream)
                 else torch.cuda.ExternalStream(int(stream), device=q.device))
     with torch.cuda.stream(side):
-        return _new_scored_workspace(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2],
+        return _new_scored_workspace(num_rows or q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2],
                                      q.device)
 
 
@@ -481,7 +482,7 @@ def decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, scale, c
     bf16 and returns it."""
     status = (_lib._binding or _lib.binding()).decode_scored(
         out, q, k_cache, v_cache, block_tables, context_lens, scale, cap, window, slopes, k_scale,
-        v_scale, _scored_workspace(workspace, q, k_cache, stream), stream)
+        v_scale, _scored_workspace(workspace, q, k_cache, stream, 1), stream)  # (room for all)
     if status:
         _lib.check(status)
     return out

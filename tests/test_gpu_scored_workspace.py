@@ -105,3 +105,22 @@ def test_the_error_word_of_a_new_workspace_is_zero():
         del junk
         ws = ops.alloc_scored_workspace(rows, 8, 2, d)
         assert int(ws[:4].view(torch.int32).item()) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_decode_takes_no_room_for_tiles(kv):
+    """Without a workspace of its own a call allocates what it splits rows in,
+    with the same result."""
+    lens = [900 + 7 * i for i in range(40)]
+    c = _attn_case(125, kv, lens, 8, 2, 128, 16)
+    q = _bf16(c["rng"], len(lens), 8, 128)
+    want = _decode(c, q, ops.alloc_scored_workspace(len(lens), 8, 2, 128))
+    args = (q, c["kc"], c["vc"], _dev(c["tables"]), _dev(lens), c["scale"])
+    mod, out = _mod(c, 30.0, 0, False), torch.empty_like(q)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    ops.decode_scored(out, *args, **mod)
+    assert torch.cuda.max_memory_allocated() - before < 8 << 20
+    assert torch.equal(out, want)
